@@ -118,6 +118,12 @@ def lib() -> ctypes.CDLL:
             "lora_pool_load": [P, I32, P, P, ctypes.c_size_t, P, ctypes.c_size_t],
             "lora_sgmv_workspace_bytes": [P, I32, I32, P],
             "lora_bgmv_multi_handoff_noalloc": [P, P, I64, P, I32, I32, P],
+            # lora_step.h (marshalled by step.py)
+            "lora_kv_plan": [P, P, P, P, P, P],
+            "lora_rope_append": [P, I32, I32, P, I64, P, I64, P, I64, P, I64, P, P, I64, P, P],
+            "lora_paged_attention": [P, I32, I32, P, I64, P, I64, P, I32, P, I64, I32, P, P, ctypes.c_float, I32, P, P,
+                                     ctypes.c_size_t],
+            "lora_residual_norm": [P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -128,7 +134,8 @@ def lib() -> ctypes.CDLL:
                                 ("lora_pool_free_count", [P], I64),
                                 ("lora_pool_pages_for", [I32, I32, I32, I32], I64),
                                 ("lora_pool_load_header_bytes", [I32], ctypes.c_size_t),
-                                ("lora_handoff_bytes", [I32], ctypes.c_size_t)):
+                                ("lora_handoff_bytes", [I32], ctypes.c_size_t),
+                                ("lora_paged_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         L.lora_pick_tile_rows.restype = ctypes.c_int32

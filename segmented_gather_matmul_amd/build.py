@@ -15,8 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
 SOURCES = [os.path.join(CSRC, "lora_kernels.hip"), os.path.join(CSRC, "lora_pool.hip"),
-           os.path.join(CSRC, "lora_host.cpp")]
-HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(CSRC, "lora_internal.hpp")]
+           os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_host.cpp")]
+HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(INCLUDE, "lora_step.h"),
+           os.path.join(CSRC, "lora_internal.hpp"), os.path.join(CSRC, "lora_launch.hpp")]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,251 @@
+"""CPU: the decode-step operators' C ABI and binding -- exports, every refusal that the host
+checks make before a launch, and the references the GPU tests compare against.  No test
+here launches a kernel."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from segmented_gather_matmul_amd import binding as B
+from segmented_gather_matmul_amd import build as build_mod
+from segmented_gather_matmul_amd import step as S
+from tests import step_ref as R
+
+PTR = 0x10000   # an aligned address that is never followed: every call here is refused
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if build_mod.stale():
+        build_mod.build()
+    return B.lib()
+
+
+def test_exports():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(build_mod.INCLUDE, "lora_step.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(lora_[a-z0-9_]+)\s*\(", text))
+    assert names == set(S.EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", build_mod.LIB], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (lora_\w+)", out))
+
+
+def _cache(**kw):
+    d = dict(type=0, page_size=16, num_pages=8, kv_heads=2, head_dim=64, reserved=0, page_stride=2048, token_stride=128,
+             head_stride=64, k=PTR, v=PTR)
+    d.update(kw)
+    return S.CKVCache(*[d[f[0]] for f in S.CKVCache._fields_])
+
+
+def _code(fn, *args):
+    return getattr(B.lib(), fn)(*args)
+
+
+CACHE_FAULTS = [(dict(type=2), B.LORA_E_UNSUPPORTED), (dict(page_size=0), B.LORA_E_SHAPE),
+                (dict(page_size=12), B.LORA_E_SHAPE), (dict(page_size=2048), B.LORA_E_SHAPE),
+                (dict(num_pages=0), B.LORA_E_SHAPE), (dict(num_pages=1 << 28), B.LORA_E_SHAPE),
+                (dict(kv_heads=0), B.LORA_E_SHAPE), (dict(head_dim=0), B.LORA_E_SHAPE),
+                (dict(head_dim=60), B.LORA_E_SHAPE), (dict(head_dim=264), B.LORA_E_SHAPE),
+                (dict(reserved=1), B.LORA_E_SHAPE), (dict(k=None), B.LORA_E_NULL), (dict(v=None), B.LORA_E_NULL),
+                (dict(k=PTR + 8), B.LORA_E_ALIGN), (dict(token_stride=32), B.LORA_E_SHAPE),
+                (dict(head_stride=68), B.LORA_E_ALIGN), (dict(page_stride=-2048), B.LORA_E_SHAPE)]
+
+
+@pytest.mark.parametrize("kw,code", CACHE_FAULTS, ids=lambda x: str(x))
+def test_bad_caches_are_refused(kw, code):
+    c = _cache(**kw)
+    rope = S.CRope(0, 1, 0, 0, None, None)
+    assert _code("lora_rope_append", None, 1, 0, None, 0, None, 0, PTR, 128, PTR, 128, ctypes.byref(rope), None, 0, PTR,
+                 ctypes.byref(c)) == code
+    assert _code("lora_paged_attention", None, 1, 2, PTR, 128, PTR + 4096, 128, ctypes.byref(c), 1, PTR, 4, 4, PTR, None,
+                 1.0, 0, None, PTR, 1 << 30) == code
+    assert B.last_error()
+
+
+def _attn(**kw):
+    d = dict(n_rows=2, heads=4, out=PTR, ldo=256, q=PTR + 4096, ldq=256, cache=_cache(), n_req=2, table=PTR, ldt=4,
+             blocks=4, kv_len=PTR, req=None, scale=1.0, window=0, lse=None, work=PTR, work_bytes=1 << 30)
+    d.update(kw)
+    c = d["cache"]
+    return _code("lora_paged_attention", None, d["n_rows"], d["heads"], d["out"], d["ldo"], d["q"], d["ldq"],
+                 ctypes.byref(c) if c else None, d["n_req"], d["table"], d["ldt"], d["blocks"], d["kv_len"], d["req"],
+                 d["scale"], d["window"], d["lse"], d["work"], d["work_bytes"])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_rows=-1), B.LORA_E_SHAPE), (dict(n_req=-1), B.LORA_E_SHAPE), (dict(heads=3), B.LORA_E_SHAPE),
+    (dict(heads=0), B.LORA_E_SHAPE), (dict(cache=None), B.LORA_E_NULL), (dict(out=None), B.LORA_E_NULL),
+    (dict(q=None), B.LORA_E_NULL), (dict(q=PTR + 4098), B.LORA_E_ALIGN), (dict(ldq=255), B.LORA_E_SHAPE),
+    (dict(ldo=260), B.LORA_E_ALIGN), (dict(blocks=0), B.LORA_E_SHAPE), (dict(ldt=3), B.LORA_E_SHAPE),
+    (dict(blocks=1 << 28, ldt=1 << 28), B.LORA_E_SHAPE), (dict(kv_len=None), B.LORA_E_NULL),
+    (dict(table=None), B.LORA_E_NULL), (dict(window=-1), B.LORA_E_SHAPE), (dict(scale=float("inf")), B.LORA_E_SHAPE),
+    (dict(scale=float("nan")), B.LORA_E_SHAPE), (dict(lse=PTR + 2), B.LORA_E_ALIGN), (dict(work=None), B.LORA_E_NULL),
+    (dict(work=PTR + 128), B.LORA_E_ALIGN), (dict(work_bytes=0), B.LORA_E_SHAPE),
+    (dict(q=PTR + 16), B.LORA_E_SHAPE), (dict(q=PTR), B.LORA_E_SHAPE),
+    (dict(n_rows=1 << 29), B.LORA_E_SHAPE)], ids=lambda x: str(x))
+def test_attention_refusals(kw, code):
+    assert _attn(**kw) == code
+
+
+def test_attention_of_no_rows_is_nothing():
+    assert _attn(n_rows=0, q=None, out=None, kv_len=None, work=None) == B.LORA_OK
+
+
+def _append(**kw):
+    d = dict(n=2, heads=4, qo=PTR, ldqo=256, q=PTR + 4096, ldq=256, k=PTR + 8192, ldk=128, v=PTR + 16384, ldv=128,
+             rope=S.CRope(64, 1, 0, 0, PTR, None), pos=PTR, ldp=2, slots=PTR, cache=_cache())
+    d.update(kw)
+    r, c = d["rope"], d["cache"]
+    return _code("lora_rope_append", None, d["n"], d["heads"], d["qo"], d["ldqo"], d["q"], d["ldq"], d["k"], d["ldk"],
+                 d["v"], d["ldv"], ctypes.byref(r) if r else None, d["pos"], d["ldp"], d["slots"], ctypes.byref(c))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), B.LORA_E_SHAPE), (dict(heads=-1), B.LORA_E_SHAPE), (dict(rope=None), B.LORA_E_NULL),
+    (dict(rope=S.CRope(72, 1, 0, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(80, 1, 0, 0, PTR, None)), B.LORA_E_SHAPE),
+    (dict(rope=S.CRope(-16, 1, 0, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(64, 0, 0, 0, PTR, None)), B.LORA_E_SHAPE),
+    (dict(rope=S.CRope(64, 5, 0, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(64, 1, 2, 0, PTR, None)), B.LORA_E_SHAPE),
+    (dict(rope=S.CRope(64, 1, 0, 0, None, None)), B.LORA_E_NULL), (dict(pos=None), B.LORA_E_NULL),
+    (dict(ldp=1), B.LORA_E_SHAPE), (dict(slots=None), B.LORA_E_NULL), (dict(q=None), B.LORA_E_NULL),
+    (dict(qo=None), B.LORA_E_NULL), (dict(k=None), B.LORA_E_NULL), (dict(v=PTR + 4), B.LORA_E_ALIGN),
+    (dict(ldk=120), B.LORA_E_SHAPE), (dict(ldv=132), B.LORA_E_ALIGN), (dict(qo=PTR + 4096, ldqo=264), B.LORA_E_SHAPE),
+    (dict(qo=PTR + 8192 - 16), B.LORA_E_SHAPE), (dict(qo=PTR + 16384), B.LORA_E_SHAPE)], ids=lambda x: str(x))
+def test_append_refusals(kw, code):
+    assert _append(**kw) == code
+
+
+def _plan(pages=None, out=None, kv=PTR, new=PTR):
+    p = dict(n_req=3, page_size=16, num_pages=8, max_blocks=4, ld_table=4, block_table=PTR, free_pages=PTR, free_top=PTR)
+    o = dict(max_tokens=4, reserved=0, status=PTR, kv_end=PTR, free_top=PTR, q_ptr=PTR, tok_req=PTR, tok_pos=PTR,
+             slots=PTR, idx=None)
+    p.update(pages or {})
+    o.update(out or {})
+    cp = S.CKVPages(*[p[f[0]] for f in S.CKVPages._fields_])
+    co = S.CKVPlanOut(*[o[f[0]] for f in S.CKVPlanOut._fields_])
+    return _code("lora_kv_plan", None, ctypes.byref(cp), kv, new, None, ctypes.byref(co))
+
+
+@pytest.mark.parametrize("pages,out,code", [
+    (dict(page_size=3), {}, B.LORA_E_SHAPE), (dict(n_req=-1), {}, B.LORA_E_SHAPE), (dict(num_pages=0), {}, B.LORA_E_SHAPE),
+    (dict(num_pages=1 << 30), {}, B.LORA_E_SHAPE), (dict(max_blocks=0), {}, B.LORA_E_SHAPE),
+    (dict(ld_table=3), {}, B.LORA_E_SHAPE), (dict(block_table=None), {}, B.LORA_E_NULL),
+    (dict(free_pages=None), {}, B.LORA_E_NULL), (dict(free_top=None), {}, B.LORA_E_NULL),
+    ({}, dict(max_tokens=-1), B.LORA_E_SHAPE), ({}, dict(reserved=1), B.LORA_E_SHAPE),
+    ({}, dict(status=None), B.LORA_E_NULL), ({}, dict(kv_end=None), B.LORA_E_NULL),
+    ({}, dict(q_ptr=None), B.LORA_E_NULL), ({}, dict(slots=None), B.LORA_E_NULL)], ids=lambda x: str(x))
+def test_plan_refusals(pages, out, code):
+    assert _plan(pages, out) == code
+
+
+def test_plan_needs_its_lengths():
+    assert _plan(kv=None) == B.LORA_E_NULL and _plan(new=None) == B.LORA_E_NULL
+
+
+def _norm(**kw):
+    d = dict(type=0, n_rows=2, hidden=64, n_gates=0, y=PTR, ldy=64, res_out=PTR + 4096, ldro=64, res=PTR + 8192, ldr=64,
+             x=PTR + 16384, ldx=64, w=PTR, post_w=None, gate=None, ldg=64, gate_idx=None, alpha=1.0, eps=1e-5,
+             w_offset=0.0, reserved=0)
+    d.update(kw)
+    a = S.CNormArgs(*[d[f[0]] for f in S.CNormArgs._fields_])
+    return _code("lora_residual_norm", None, ctypes.byref(a))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(type=3), B.LORA_E_UNSUPPORTED), (dict(n_rows=-1), B.LORA_E_SHAPE), (dict(hidden=60), B.LORA_E_SHAPE),
+    (dict(hidden=0), B.LORA_E_SHAPE), (dict(hidden=65544), B.LORA_E_SHAPE), (dict(eps=-1.0), B.LORA_E_SHAPE),
+    (dict(eps=float("nan")), B.LORA_E_SHAPE), (dict(alpha=float("inf")), B.LORA_E_SHAPE),
+    (dict(y=None, res_out=None), B.LORA_E_NULL), (dict(x=None, post_w=PTR), B.LORA_E_NULL),
+    (dict(x=None, gate=PTR, n_gates=1), B.LORA_E_NULL), (dict(gate_idx=PTR), B.LORA_E_NULL), (dict(res=None), B.LORA_E_NULL),
+    (dict(w=None), B.LORA_E_NULL), (dict(ldr=56), B.LORA_E_SHAPE), (dict(ldx=68), B.LORA_E_ALIGN),
+    (dict(post_w=PTR + 2), B.LORA_E_ALIGN), (dict(gate=PTR, n_gates=2), B.LORA_E_SHAPE),
+    (dict(gate=PTR, n_gates=0, gate_idx=PTR), B.LORA_E_SHAPE), (dict(y=PTR + 8192), B.LORA_E_SHAPE),
+    (dict(y=PTR + 4096), B.LORA_E_SHAPE), (dict(res_out=PTR + 16384), B.LORA_E_SHAPE),
+    (dict(res_out=PTR + 8192 + 16), B.LORA_E_SHAPE), (dict(reserved=1), B.LORA_E_SHAPE)], ids=lambda x: str(x))
+def test_norm_refusals(kw, code):
+    assert _norm(**kw) == code
+    assert _norm(n_rows=0) == B.LORA_OK
+
+
+def test_null_descriptors():
+    assert _code("lora_residual_norm", None, None) == B.LORA_E_NULL
+    assert _code("lora_kv_plan", None, None, PTR, PTR, None, None) == B.LORA_E_NULL
+    assert B.lib().lora_paged_attention_bytes(-1, 4, 2, 64) == 0
+    assert B.lib().lora_paged_attention_bytes(2, 3, 2, 64) == 0
+
+
+# ------------------------------------------------------------------ the binding
+def test_binding_rejects_wrong_tensors():
+    h = torch.float16
+    kc = torch.zeros(4, 16, 2, 64, dtype=h)
+    cache = S.PagedKV(kc, torch.zeros_like(kc))
+    assert (cache.num_pages, cache.page_size, cache.kv_heads, cache.head_dim) == (4, 16, 2, 64)
+    q = torch.zeros(2, 256, dtype=h)
+    tab, n, w = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(64, dtype=torch.int32)
+    call = lambda **k: S.lora_paged_attention(**{**dict(out=q.clone(), q=q, cache=cache, block_table=tab, kv_len=n, work=w), **k})
+    for k, msg in ((dict(q=q.float()), "dtype"), (dict(q=q[:, :200]), "heads"), (dict(out=q[:1]), "at least"),
+                   (dict(kv_len=n.long()), "dtype"), (dict(kv_len=n[:1]), "elements"), (dict(block_table=tab.long()), "dtype"),
+                   (dict(lse=torch.zeros(3)), "elements"), (dict(lse=torch.zeros(8, dtype=h)), "dtype"),
+                   (dict(req=n.float()), "dtype"), (dict(), "GPU tensor")):
+        with pytest.raises(ValueError, match=msg):
+            call(**k)
+    k2 = torch.zeros(2, 128, dtype=h)
+    rope = S.Rope(torch.ones(32))
+    app = lambda **k: S.lora_rope_append(**{**dict(q_out=q.clone(), q=q, k=k2, v=k2.clone(), cache=cache, slots=n, rope=rope,
+                                                    positions=torch.zeros(1, 2, dtype=torch.int32)), **k})
+    for k, msg in ((dict(q_out=None), "together"), (dict(k=k2.bfloat16()), "dtype"), (dict(positions=None), "tensor"),
+                   (dict(positions=torch.zeros(1, 1, dtype=torch.int32)), "at least"), (dict(v=k2[:, :64]), "at least"),
+                   (dict(slots=n.long()), "dtype"), (dict(), "GPU tensor")):
+        with pytest.raises(ValueError, match=msg):
+            app(**k)
+    r = torch.zeros(2, 64, dtype=h)
+    nrm = lambda **k: S.lora_residual_norm(**{**dict(y=r.clone(), res=r, w=torch.ones(64, dtype=h)), **k})
+    for k, msg in ((dict(w=None), "tensor"), (dict(w=torch.ones(64)), "dtype"), (dict(x=r.t()), "stride|at least"),
+                   (dict(res=r.float()), "dtype"), (dict(gate=r, x=r.clone(), gate_idx=n[:1]), "elements"), (dict(), "GPU tensor")):
+        with pytest.raises(ValueError, match=msg):
+            nrm(**k)
+
+
+def test_descriptors_reject_wrong_layouts():
+    h = torch.float16
+    k = torch.zeros(4, 16, 2, 64, dtype=h)
+    S.PagedKV(k.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3), k.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3))
+    both = torch.zeros(4, 2, 16, 2, 64, dtype=h)
+    S.PagedKV(both[:, 0], both[:, 1])
+    for args, msg in (((k, k), "overlap"), ((k, k.bfloat16()), "dtype"), ((k.float(), k.float()), "dtype"),
+                      ((k[0], k[0]), "must be"), ((k, k.permute(0, 2, 1, 3)), "must be|strides"),
+                      ((k.expand(4, 16, 2, 64)[:1].expand(4, 16, 2, 64), torch.zeros_like(k)), "strides|overlapping")):
+        with pytest.raises(ValueError, match=msg):
+            S.PagedKV(*args)
+    t, f, top = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    S.KVPages(t, f, top, 16)
+    for args, msg in (((t, f, top, 12), "power"), ((t.long(), f, top, 16), "dtype"), ((t[0], f, top, 16), "block_table"),
+                      ((t, f[::2], top, 16), "contiguous")):
+        with pytest.raises(ValueError, match=msg):
+            S.KVPages(*args)
+    with pytest.raises(ValueError, match="frequencies"):
+        S.Rope(torch.ones(12))
+    with pytest.raises(ValueError, match="axes"):
+        S.Rope(torch.ones(16), axes=5)
+
+
+# ------------------------------------------------------------------ the references
+def test_plan_reference_on_a_worked_example():
+    # pages of 4 tokens; request 0 grows from 3 to 5, request 1 (6 tokens) ends, request 2 starts with 2
+    got = R.plan([3, 6, 0], [2, -1, 2], [[7, -1], [1, 4], [-1, -1]], [2, 9, -1, -1, -1, -1, -1, -1, -1, -1], 2, 4, 6, [5, 6, 7])
+    assert got["status"] == [0, 4, 2, 2] and got["kv_end"] == [5, 0, 2] and got["q_ptr"] == [0, 2, 2, 4]
+    # 1 and 4 go on the list (2 9 1 4); request 0 takes 4, request 2 takes 1
+    assert got["table"] == [[7, 4], [1, 4], [1, -1]] and got["free_top"] == 2 and got["free"][:4] == [2, 9, 1, 4]
+    assert got["tok_req"] == [0, 0, 2, 2, -1, -1] and got["tok_pos"] == [3, 4, 0, 1, -1, -1]
+    assert got["slots"] == [31, 16, 4, 5, -1, -1] and got["idx"] == [5, 5, 7, 7, -1, -1]
+    assert R.plan([3], [2], [[7, -1]], [2], 0, 4, 6)["status"][0] == 1
+
+
+def test_attention_reference_on_one_token_and_on_none():
+    q = torch.ones(3, 2, 8, dtype=torch.float16)
+    k, v = torch.full((2, 4, 1, 8), float("nan"), dtype=torch.float16), torch.full((2, 4, 1, 8), float("nan"), dtype=torch.float16)
+    k[1, 0], v[1, 0] = 0.5, 3.0
+    o = R.attention(q, k, v, torch.tensor([[1], [0], [5]], dtype=torch.int32), [1, 0, 2], None, 1.0, 0, 2)
+    assert torch.equal(o[0][0], torch.full((2, 8), 3.0, dtype=torch.float64)) and o[0][1].tolist() == [4.0, 4.0]
+    assert not o[1][0].any() and not o[2][0].any() and o[2][1].tolist() == [float("-inf")] * 2
