@@ -380,98 +380,455 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
 
 // ------------------------------------------------------------------------ attention
 struct AttnArgs {
-    int32_t q_heads, kv_heads, head_dim, n_req, max_blocks, window, shift;
+    int32_t n_rows, q_heads, kv_heads, head_dim, n_req, max_blocks, window, shift;
+    int32_t group, head_tiles, extra;  // query heads per key/value head; its 16-head tiles; work items beyond one per row
     float scale;
     void *out;
     const void *q;
     int64_t ldo, ldq, ld_table;
     const int32_t *table, *kv_len, *req;
     float *lse;
+    float *part_ml, *part_o;  // parts of rows that are split: (m, l) and unnormalised sums
     lora_kv_cache c;
 };
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kAttnWaves = 8;                     // wavefronts of an attention workgroup
+constexpr int kAttnTile = 32;                     // tokens a wavefront takes at a time
+constexpr int kAttnMinPart = 2 * kAttnWaves * kAttnTile;  // shortest part worth a workgroup of its own
+constexpr int kAttnGroups = 1024;                 // workgroups aimed at beyond one per (row, head tile)
 
-// One workgroup per (row, head).  Sixteen lanes take a token: 16-byte chunks of its key
-// against the query, summed over the lanes, then the softmax's running maximum and sum and
-// the value's chunks; each group of sixteen lanes keeps its own, joined at the end in LDS.
-template <typename T, int NC>
-__global__ __launch_bounds__(256) void lora_paged_attention_kernel(AttnArgs a)
+// Visible tokens [first, first + span) of row i; span -1: the row is not active.
+struct RowSpan {
+    int32_t req, first, span;
+};
+
+__device__ inline RowSpan row_span(const AttnArgs &a, int32_t i)
 {
-    __shared__ float sm[16], sl[16], so[16][LORA_KV_MAX_HEAD_DIM];
-    const int tid = threadIdx.x, li = tid & 15, grp = tid >> 4;
-    const int64_t row = blockIdx.x / a.q_heads;
-    const int head = blockIdx.x % a.q_heads, kvh = head / (a.q_heads / a.kv_heads);
-    const int32_t n = a.kv_len[row], r = a.req ? a.req[row] : (int32_t)row;
-    if (n < 0 || n > (int64_t)a.max_blocks << a.shift || r < 0 || r >= a.n_req) return;
-    const int chunks = a.head_dim / 8;
-    float q[NC][8], o[NC][8];
+    RowSpan s{0, 0, -1};
+    if (i >= a.n_rows) return s;
+    const int32_t n = a.kv_len[i];
+    s.req = a.req ? a.req[i] : i;
+    if (n < 0 || n > (int64_t)a.max_blocks << a.shift || s.req < 0 || s.req >= a.n_req) return s;
+    s.first = a.window > 0 && n > a.window ? n - a.window : 0;
+    s.span = n - s.first;
+    return s;
+}
+
+// The schedule of a launch, found by every workgroup from the lengths on the device: the
+// visible tokens of all rows are cut into parts of at most `cut` tokens, where cut is the
+// share of one of `extra` workgroups (so n_rows + extra work items always hold every
+// part), and a row's parts are consecutive items.  Parts of rows with several get slots
+// for their sums (2 * extra hold them all: such a row has fewer than 2 span / cut parts).
+struct Sched {
+    int32_t row, part, parts, slot0, cut;
+    RowSpan rs;
+};
+
+template <int THREADS>
+__device__ inline int32_t scan_items(int32_t v, int32_t *wave_sums, int32_t &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int32_t s = v;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[c][e] = o[c][e] = 0.f;
-        if (li + 16 * c < chunks)
-            unpack8<T>(load16(a.q, row * a.ldq + (int64_t)head * a.head_dim + 8 * (li + 16 * c)), q[c]);
+    for (int d = 1; d < 64; d *= 2) {
+        const int32_t up = __shfl_up(s, d);
+        if (lane >= d) s += up;
     }
+    __syncthreads();
+    if (lane == 63) wave_sums[wave] = s;
+    __syncthreads();
+    int32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        const int32_t x = wave_sums[w];
+        before += w < wave ? x : 0;
+        all += x;
+    }
+    total = all;
+    return before + s - v;
+}
+
+// Item `want` (or, with by_row, row `want`) of the schedule; false: there is no such item.
+template <int THREADS>
+__device__ inline bool find_item(const AttnArgs &a, int32_t want, bool by_row, Sched &out)
+{
+    __shared__ int32_t wave_sums[THREADS / 64];
+    __shared__ int64_t totals[THREADS / 64];
+    __shared__ Sched found;
+    const int tid = threadIdx.x;
+    RowSpan rs = row_span(a, tid);
+    int64_t total = rs.span > 0 ? rs.span : 0;
+    for (int32_t i = tid + THREADS; i < a.n_rows; i += THREADS) {
+        const int32_t sp = row_span(a, i).span;
+        total += sp > 0 ? sp : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+    if ((tid & 63) == 0) totals[tid >> 6] = total;
+    if (tid == 0) found.row = -1;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) total += totals[w];
+    int64_t share = (total + a.extra - 1) / a.extra;
+    share = share < kAttnMinPart ? kAttnMinPart : (share + kAttnTile - 1) / kAttnTile * kAttnTile;
+    const int32_t cut = (int32_t)(share < INT32_MAX ? share : INT32_MAX);
+    int32_t item0 = 0, slot0 = 0;
+    for (int32_t c = 0; c < a.n_rows; c += THREADS) {
+        if (c > 0) rs = row_span(a, c + tid);
+        const int32_t parts = rs.span < 0 ? 0 : rs.span <= cut ? 1 : (rs.span - 1) / cut + 1;
+        int32_t items, slots;
+        const int32_t at = item0 + scan_items<THREADS>(parts, wave_sums, items);
+        const int32_t slot = slot0 + scan_items<THREADS>(parts > 1 ? parts : 0, wave_sums, slots);
+        if (by_row ? c + tid == want : want >= at && want < at + parts)
+            found = Sched{c + tid, by_row ? 0 : want - at, parts, slot, cut, rs};
+        item0 += items;
+        slot0 += slots;
+        if (by_row ? want < c + THREADS : want < item0) break;
+    }
+    __syncthreads();
+    out = found;
+    return out.row >= 0;
+}
+
+__device__ inline f4_t mfma(const vec8<F16> &x, const vec8<F16> &y, const f4_t &c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+}
+__device__ inline f4_t mfma(const vec8<BF16> &x, const vec8<BF16> &y, const f4_t &c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+}
+
+// A weight p in [0, 2^kBias] as two 16-bit parts, hi + lo, both cut off (never rounded up)
+// and neither 0, so that hi * v + lo * v is what p * v is for an infinite v too.  fp16 keeps
+// 22 bits (the bias keeps weights down to 2^-38 of the largest out of its subnormals), bf16
+// 16 bits: both far below the rounding of the output.
+template <typename T>
+struct Weight;
+template <>
+struct Weight<F16> {
+    static constexpr float kBias = 14.f;
+    static __device__ inline void split(float p0, float p1, uint32_t &hi, uint32_t &lo)
+    {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(p0, p1));
+        hi = at_least(__builtin_bit_cast(uint32_t, h));
+        lo = at_least(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(p0 - (float)h[0], p1 - (float)h[1])));
+    }
+    static __device__ inline uint32_t at_least(uint32_t x)
+    {
+        typedef unsigned short u2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u2, x), u2{1, 1}));
+    }
+};
+template <>
+struct Weight<BF16> {
+    static constexpr float kBias = 0.f;
+    static __device__ inline void split(float p0, float p1, uint32_t &hi, uint32_t &lo)
+    {
+        const uint32_t a = __builtin_bit_cast(uint32_t, p0), b = __builtin_bit_cast(uint32_t, p1);
+        const float r0 = p0 - __builtin_bit_cast(float, a & 0xffff0000u), r1 = p1 - __builtin_bit_cast(float, b & 0xffff0000u);
+        hi = at_least((a >> 16) | (b & 0xffff0000u));
+        lo = at_least((__builtin_bit_cast(uint32_t, r0) >> 16) | (__builtin_bit_cast(uint32_t, r1) & 0xffff0000u));
+    }
+    static __device__ inline uint32_t at_least(uint32_t x)
+    {
+        typedef unsigned short u2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u2, x), u2{0x80, 0x80}));
+    }
+};
+
+// One workgroup per (part, key/value head, 16 of its query heads).
+//
+// Each wavefront walks its 32-token tiles of the part with its own running maximum and
+// sums; nothing is shared until the end, so the loop has no barrier.  Scores are
+// S^T = K Q^T on v_mfma_f32_16x16x32: the K rows go from memory straight into the A
+// operand (lane: token l % 16, 16 bytes of it), Q^T stays in registers.  A lane then
+// holds 4 + 4 tokens of one head, which is just the B operand of O^T += V^T P^T with
+// the tokens in that order, so the weights never leave their lane.  V^T comes from a
+// wave-private LDS tile by transposing reads (ds_read_tr, 4 tokens x 16 columns per
+// sixteen lanes); its row pitch of 2 DP + 32 bytes keeps writes and reads free of bank
+// conflicts.  The next tile's K is requested when this tile's scores are done, its V when
+// this tile's V is in LDS, its page ids a tile ahead of both.
+//
+// Bound by reading K and V once; every head of a group shares the read, and 16 columns of
+// heads cost the same matrix instructions as one.
+template <typename T, int DP, bool FULL>
+__global__ __launch_bounds__(64 * kAttnWaves) void lora_paged_attention_kernel(AttnArgs a)
+{
+    typedef typename T::elem E;
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    constexpr int KC = DP / 32;              // 32-column steps of a score
+    constexpr int DB = DP / 16;              // 16-column blocks of the output
+    constexpr int kPitch = DP + 16;          // LDS row pitch, elements
+    constexpr int kRegion = kAttnTile * kPitch;
+    __shared__ __align__(16) uint16_t vt[kAttnWaves][kRegion];
+    __shared__ float jm[kAttnWaves][16], jl[kAttnWaves][16];
+    static_assert(sizeof(uint16_t) * kRegion >= sizeof(float) * 16 * DP, "the join fits the V tiles");
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int per_item = a.kv_heads * a.head_tiles;
+    const int32_t item = blockIdx.x / per_item, rest = blockIdx.x - item * per_item;
+    const int kvh = rest / a.head_tiles, ht = rest - kvh * a.head_tiles;
+    Sched sc;
+    if (!find_item<64 * kAttnWaves>(a, item, false, sc)) return;
+
+    const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
+    const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
+    const int32_t begin = sc.rs.first + sc.part * sc.cut;
+    const int32_t end = sc.rs.first + (sc.rs.span - sc.part * sc.cut < sc.cut ? sc.rs.span : (sc.part + 1) * sc.cut);
+    const int32_t *table = a.table + (int64_t)sc.rs.req * a.ld_table;
+    const int32_t in_page = (1 << a.shift) - 1;
+
+    vec8<T> q[KC];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        const int d = 32 * c + 8 * lg;
+        if (li < heads && (FULL || d < a.head_dim)) r = load16(a.q, sc.row * a.ldq + (head0 + li) * a.head_dim + d);
+        q[c] = __builtin_bit_cast(vec8<T>, r);
+    }
+
+    // Tokens t0 + li and t0 + 16 + li of a tile: table entries, then cell offsets; a token
+    // past the end or without a page reads cell 0 and is masked.
+    auto ids_of = [&](int32_t t0, int32_t (&id)[2]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t t = min(t0 + 16 * s + li, end - 1);
+            id[s] = table[t >> a.shift];
+        }
+    };
+    auto cells_of = [&](int32_t t0, const int32_t (&id)[2], int64_t (&cell)[2]) {
+        uint32_t seen = 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t t = t0 + 16 * s + li;
+            const bool ok = t < end && id[s] >= 0 && id[s] < a.c.num_pages;
+            cell[s] = ok ? (int64_t)id[s] * a.c.page_stride + (int64_t)(t & in_page) * a.c.token_stride +
+                               kvh * a.c.head_stride : 0;
+            seen |= ((uint32_t)__ballot(ok) & 0xffffu) << (16 * s);
+        }
+        return seen;
+    };
+    auto load_rows = [&](const void *base, const int64_t (&cell)[2], uint4 (&r)[2][KC]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int d = 32 * c + 8 * lg;
+                r[s][c] = load16(base, cell[s] + (FULL || d < a.head_dim ? d : 0));
+            }
+    };
+    const uint4 zero4 = make_uint4(0, 0, 0, 0);
+
     float m = -INFINITY, l = 0.f;
-    const float sc = a.scale * kLog2e;
-    const int32_t first = a.window > 0 && n > a.window ? n - a.window : 0;
-    for (int32_t t = first + grp; t < n; t += 16) {
-        const int32_t page = a.table[(int64_t)r * a.ld_table + (t >> a.shift)];
-        if (page < 0 || page >= a.c.num_pages) continue;
-        const int64_t at = (int64_t)page * a.c.page_stride + (int64_t)(t & ((1 << a.shift) - 1)) * a.c.token_stride +
-                           kvh * a.c.head_stride;
-        float s = 0.f, x[NC][8];
+    f4_t o[DB];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (li + 16 * c >= chunks) continue;
-            float k[8];
-            unpack8<T>(load16(a.c.k, at + 8 * (li + 16 * c)), k);
-            unpack8<T>(load16(a.c.v, at + 8 * (li + 16 * c)), x[c]);
+    for (int b = 0; b < DB; ++b) o[b] = f4_t{0.f, 0.f, 0.f, 0.f};
+    const float scale = a.scale * kLog2e;
+    uint16_t *const tile = vt[wave];
+    const int tr_row = 4 * lg + (li >> 2), tr_col = 4 * (li & 3);
+    typedef __attribute__((address_space(3))) s4 *lds4;
+
+    constexpr int kStep = kAttnWaves * kAttnTile;
+    int32_t t0 = begin + wave * kAttnTile;
+    if (t0 < end) {
+        int32_t id[2], id_next[2];
+        int64_t cell[2];
+        uint4 kr[2][KC], vr[2][KC];
+        ids_of(t0, id);
+        ids_of(t0 + kStep, id_next);
+        uint32_t seen = cells_of(t0, id, cell);
+        load_rows(a.c.k, cell, kr);
+        load_rows(a.c.v, cell, vr);
+        for (;;) {
+            const bool more = t0 + kStep < end;
+            f4_t s[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(q[c][e], k[e], s);
-        }
+            for (int u = 0; u < 2; ++u) {
+                s[u] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d, 16);
-        s *= sc;
-        const float mn = __builtin_fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        // a NaN score stays a NaN (fmax would drop it)
-        const float p = __builtin_amdgcn_exp2f(s - base), f = __builtin_amdgcn_exp2f(m - base);
-        m = mn;
-        l = __builtin_fmaf(l, f, p);
+                for (int c = 0; c < KC; ++c) {
+                    const uint4 r = FULL || 32 * c + 8 * lg < a.head_dim ? kr[u][c] : zero4;
+                    s[u] = mfma(__builtin_bit_cast(vec8<T>, r), q[c], s[u]);
+                }
+            }
+            const uint32_t seen_now = seen;
+            const bool mine[2] = {(seen_now >> li & 1) != 0, (seen_now >> (16 + li) & 1) != 0};
+            if (more) {
+                seen = cells_of(t0 + kStep, id_next, cell);
+                ids_of(t0 + 2 * kStep, id_next);
+                load_rows(a.c.k, cell, kr);
+            }
+            // scores in base 2, the running maximum of this lane's head
+            float x[8], mx = m;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (li + 16 * c >= chunks) continue;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[c][e] = __builtin_fmaf(p, x[c][e], o[c][e] * f);
+                for (int e = 0; e < 4; ++e) {
+                    const bool ok = seen_now >> (16 * u + 4 * lg + e) & 1;
+                    x[4 * u + e] = ok ? s[u][e] * scale : -INFINITY;
+                    mx = __builtin_fmaxf(mx, x[4 * u + e]);
+                }
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
+            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+            if (__any(mx != m)) {
+                const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
+                l *= f;
+#pragma unroll
+                for (int b = 0; b < DB; ++b) o[b] *= f;
+                m = mx;
+            }
+            const float base = (m == -INFINITY ? 0.f : m) - Weight<T>::kBias;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = __builtin_amdgcn_exp2f(x[e] - base);
+                l += x[e];
+            }
+            uint4 hi, lo;
+            Weight<T>::split(x[0], x[1], hi.x, lo.x);
+            Weight<T>::split(x[2], x[3], hi.y, lo.y);
+            Weight<T>::split(x[4], x[5], hi.z, lo.z);
+            Weight<T>::split(x[6], x[7], hi.w, lo.w);
+            const vec8<T> ph = __builtin_bit_cast(vec8<T>, hi), pl = __builtin_bit_cast(vec8<T>, lo);
+            // V rows to LDS; what is masked is 0 there
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int d = 32 * c + 8 * lg;
+                    const uint4 r = mine[u] && (FULL || d < a.head_dim) ? vr[u][c] : zero4;
+                    *reinterpret_cast<uint4 *>(&tile[(16 * u + li) * kPitch + d]) = r;
+                }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (more) load_rows(a.c.v, cell, vr);
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(&tile[tr_row * kPitch + 16 * b + tr_col]));
+                const s4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(&tile[(16 + tr_row) * kPitch + 16 * b + tr_col]));
+                const vec8<T> vv = __builtin_bit_cast(vec8<T>, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+                o[b] = mfma(vv, ph, o[b]);
+                o[b] = mfma(vv, pl, o[b]);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (!more) break;
+            t0 += kStep;
         }
     }
-    if (li == 0) {
-        sm[grp] = m;
-        sl[grp] = l;
+    // Join the wavefronts: every one's sums in LDS, scaled to the common maximum.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (lg == 0) {
+        jm[wave][li] = m;
+        jl[wave][li] = l;
     }
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-        if (li + 16 * c < chunks)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) so[grp][8 * (li + 16 * c) + e] = o[c][e];
     __syncthreads();
     float mx = -INFINITY;
-    for (int g = 0; g < 16; ++g) mx = __builtin_fmaxf(mx, sm[g]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float total = 0.f, f[16];
-    for (int g = 0; g < 16; ++g) {
-        f[g] = __builtin_amdgcn_exp2f(sm[g] - base);
-        total = __builtin_fmaf(f[g], sl[g], total);
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) mx = __builtin_fmaxf(mx, jm[w][li]);
+    const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
+    float *const mine_o = reinterpret_cast<float *>(vt[wave]);
+    if (li < heads)
+#pragma unroll
+        for (int b = 0; b < DB; ++b) *reinterpret_cast<f4_t *>(&mine_o[li * DP + 16 * b + 4 * lg]) = o[b] * f;
+    __syncthreads();
+    for (int i = tid; i < heads * (DP / 4); i += 64 * kAttnWaves) {
+        const int h = i / (DP / 4), d = 4 * (i - h * (DP / 4));
+        if (!FULL && d >= a.head_dim) continue;
+        float hm = -INFINITY, hl = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) hm = __builtin_fmaxf(hm, jm[w][h]);
+        f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) {
+            hl = __builtin_fmaf(jl[w][h], __builtin_amdgcn_exp2f(jm[w][h] - (hm == -INFINITY ? 0.f : hm)), hl);
+            sum += *reinterpret_cast<const f4_t *>(&reinterpret_cast<const float *>(vt[w])[h * DP + d]);
+        }
+        const int64_t head = head0 + h;
+        if (sc.parts > 1) {
+            const int64_t slot = (int64_t)(sc.slot0 + sc.part) * a.q_heads + head;
+            *reinterpret_cast<f4_t *>(&a.part_o[slot * a.head_dim + d]) = sum;
+            if (d == 0) {
+                a.part_ml[2 * slot] = hm;
+                a.part_ml[2 * slot + 1] = hl;
+            }
+            continue;
+        }
+        const bool none = hl == 0.f;
+        typedef E e4 __attribute__((ext_vector_type(4)));
+        e4 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = (E)(none ? 0.f : sum[e] / hl);
+        *reinterpret_cast<e4 *>(static_cast<E *>(a.out) + sc.row * a.ldo + head * a.head_dim + d) = r;
+        if (a.lse && d == 0)
+            a.lse[(int64_t)sc.row * a.q_heads + head] =
+                none ? -INFINITY : (hm + (__builtin_log2f(hl) - Weight<T>::kBias)) * kLn2;
     }
-    const bool none = total == 0.f;
+}
+
+// Joins the parts of rows that were split: one workgroup per (row, head), its lanes over
+// the parts' maxima and sums first, then over the columns; parts are added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void lora_attention_join_kernel(AttnArgs a)
+{
+    typedef typename T::elem E;
+    __shared__ float red[8];
+    const int tid = threadIdx.x;
+    const int32_t row = blockIdx.x / a.q_heads;
+    const int head = blockIdx.x - row * a.q_heads;
+    Sched sc;
+    if (!find_item<256>(a, row, true, sc) || sc.parts < 2) return;
+    const int64_t slot0 = (int64_t)sc.slot0 * a.q_heads + head;
+    float m = -INFINITY;
+    for (int p = tid; p < sc.parts; p += 256) m = __builtin_fmaxf(m, a.part_ml[2 * (slot0 + (int64_t)p * a.q_heads)]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    if ((tid & 63) == 0) red[tid >> 6] = m;
+    __syncthreads();
+    m = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int p = 0; p < sc.parts; ++p) {
+        const float *ml = &a.part_ml[2 * (slot0 + (int64_t)p * a.q_heads)];
+        l = __builtin_fmaf(ml[1], __builtin_amdgcn_exp2f(ml[0] - base), l);
+    }
+    const bool none = l == 0.f;
     for (int d = tid; d < a.head_dim; d += 256) {
         float s = 0.f;
-        for (int g = 0; g < 16; ++g) s = __builtin_fmaf(f[g], so[g][d], s);
-        typename T::elem e = (typename T::elem)(none ? 0.f : s / total);
-        static_cast<typename T::elem *>(a.out)[row * a.ldo + (int64_t)head * a.head_dim + d] = e;
+        for (int p = 0; p < sc.parts; ++p) {
+            const int64_t slot = slot0 + (int64_t)p * a.q_heads;
+            s = __builtin_fmaf(a.part_o[slot * a.head_dim + d], __builtin_amdgcn_exp2f(a.part_ml[2 * slot] - base), s);
+        }
+        static_cast<E *>(a.out)[row * a.ldo + (int64_t)head * a.head_dim + d] = (E)(none ? 0.f : s / l);
     }
-    if (a.lse && tid == 0) a.lse[row * a.q_heads + head] = none ? -INFINITY : (mx + __builtin_log2f(total)) * kLn2;
+    if (a.lse && tid == 0)
+        a.lse[(int64_t)row * a.q_heads + head] = none ? -INFINITY : (m + (__builtin_log2f(l) - Weight<T>::kBias)) * kLn2;
+}
+
+// Work items beyond one per row, by shape alone (the lengths are on the device).
+int32_t attn_extra(int32_t q_heads, int32_t kv_heads)
+{
+    const int64_t per_item = (int64_t)kv_heads * ((q_heads / kv_heads + 15) / 16);
+    return (int32_t)std::max<int64_t>(1, (kAttnGroups + per_item - 1) / per_item);
+}
+
+template <typename T>
+void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
+{
+    const int D = a.head_dim;
+#define LORA_ATTN(DP)                                                                                         \
+    (D == DP ? launch_args(lora_paged_attention_kernel<T, DP, true>, grid, 64 * kAttnWaves, 0, s, a)          \
+             : launch_args(lora_paged_attention_kernel<T, DP, false>, grid, 64 * kAttnWaves, 0, s, a))
+    if (D <= 64) LORA_ATTN(64);
+    else if (D <= 128) LORA_ATTN(128);
+    else LORA_ATTN(256);
+#undef LORA_ATTN
+    launch_args(lora_attention_join_kernel<T>, dim3((unsigned)(a.n_rows * a.q_heads)), 256, 0, s, a);
 }
 
 // ------------------------------------------------------------------------ residual add and norms
@@ -737,8 +1094,11 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
 
 size_t lora_paged_attention_bytes(int32_t n_rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim)
 {
-    if (n_rows < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || head_dim < 8) return 0;
-    return 256;
+    if (n_rows < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || head_dim < 8 ||
+        head_dim > LORA_KV_MAX_HEAD_DIM || head_dim % 8)
+        return 0;
+    const size_t slots = 2 * (size_t)attn_extra(q_heads, kv_heads) * q_heads;
+    return (slots * (head_dim + 2) * sizeof(float) + 255) & ~size_t(255);
 }
 
 int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *out, int64_t ldo, const void *q,
@@ -770,6 +1130,7 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     const size_t need = lora_paged_attention_bytes(n_rows, q_heads, cache->kv_heads, cache->head_dim);
     if (work_bytes < need) return fail(LORA_E_SHAPE, "workspace of %zu bytes < %zu for %d rows", work_bytes, need, n_rows);
     AttnArgs a{};
+    a.n_rows = n_rows;
     a.q_heads = q_heads;
     a.kv_heads = cache->kv_heads;
     a.head_dim = cache->head_dim;
@@ -777,6 +1138,9 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.max_blocks = max_blocks;
     a.window = window;
     a.shift = page_shift(cache->page_size);
+    a.group = q_heads / cache->kv_heads;
+    a.head_tiles = (a.group + 15) / 16;
+    a.extra = attn_extra(q_heads, cache->kv_heads);
     a.scale = scale;
     a.out = out;
     a.q = q;
@@ -788,13 +1152,15 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.req = req;
     a.lse = lse;
     a.c = *cache;
+    const size_t slots = 2 * (size_t)a.extra * q_heads;
+    a.part_o = static_cast<float *>(work);
+    a.part_ml = a.part_o + slots * cache->head_dim;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)(n_rows * q_heads));
-    const bool bf = cache->type == LORA_TYPE_BF16, wide = cache->head_dim > 128;
-    if (bf && wide) launch_args(lora_paged_attention_kernel<BF16, 2>, grid, 256, 0, s, a);
-    else if (bf) launch_args(lora_paged_attention_kernel<BF16, 1>, grid, 256, 0, s, a);
-    else if (wide) launch_args(lora_paged_attention_kernel<F16, 2>, grid, 256, 0, s, a);
-    else launch_args(lora_paged_attention_kernel<F16, 1>, grid, 256, 0, s, a);
+    const int64_t groups = ((int64_t)n_rows + a.extra) * a.kv_heads * a.head_tiles;
+    if (groups > (int64_t)1 << 30) return fail(LORA_E_SHAPE, "launch of %lld workgroups is too large", (long long)groups);
+    const dim3 grid((unsigned)groups);
+    if (cache->type == LORA_TYPE_BF16) attention_launch<BF16>(a, grid, s);
+    else attention_launch<F16>(a, grid, s);
     return launch_status("paged attention");
 }
 
