@@ -388,15 +388,22 @@ struct AttnArgs {
     int64_t ldo, ldq, ld_table;
     const int32_t *table, *kv_len, *req;
     float *lse;
-    float *part_ml, *part_o;  // parts of rows that are split: (m, l) and unnormalised sums
+    uint32_t *count;          // arrivals of split rows' parts (zero between calls)
+    float *part_ml, *part_o;  // their (m, l) and unnormalised sums
     lora_kv_cache c;
 };
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kAttnWaves = 8;                     // wavefronts of an attention workgroup
-constexpr int kAttnTile = 32;                     // tokens a wavefront takes at a time
-constexpr int kAttnMinPart = 2 * kAttnWaves * kAttnTile;  // shortest part worth a workgroup of its own
-constexpr int kAttnGroups = 1024;                 // workgroups aimed at beyond one per (row, head tile)
+constexpr int kAttnWaves = 4;        // wavefronts of an attention workgroup
+constexpr int kAttnTile = 32;        // tokens a wavefront takes at a time
+constexpr int kAttnMinPart = 512;    // shortest part worth a workgroup of its own
+constexpr int kAttnGroups = 2048;    // workgroups aimed at beyond one per (row, head tile)
+constexpr int kAttnJoin = 16;        // parts joined at a time
+constexpr int kAttnMaxTiles = 4096;  // key/value heads x 16-head tiles of one launch
+// Arrival counters, one per part slot and head tile: 2 * extra * tiles <= 2 * (kAttnGroups + tiles).
+// They lie first in a workspace, at one size for every shape, so calls of different shapes
+// sharing a workspace never put sums where another finds its counters.
+constexpr size_t kAttnCounters = 2 * (kAttnGroups + kAttnMaxTiles);
 
 // Visible tokens [first, first + span) of row i; span -1: the row is not active.
 struct RowSpan {
@@ -449,9 +456,9 @@ __device__ inline int32_t scan_items(int32_t v, int32_t *wave_sums, int32_t &tot
     return before + s - v;
 }
 
-// Item `want` (or, with by_row, row `want`) of the schedule; false: there is no such item.
+// Item `want` of the schedule; false: there is no such item.
 template <int THREADS>
-__device__ inline bool find_item(const AttnArgs &a, int32_t want, bool by_row, Sched &out)
+__device__ inline bool find_item(const AttnArgs &a, int32_t want, Sched &out)
 {
     __shared__ int32_t wave_sums[THREADS / 64];
     __shared__ int64_t totals[THREADS / 64];
@@ -471,7 +478,7 @@ __device__ inline bool find_item(const AttnArgs &a, int32_t want, bool by_row, S
     total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) total += totals[w];
-    int64_t share = (total + a.extra - 1) / a.extra;
+    int64_t share = a.extra > 0 ? (total + a.extra - 1) / a.extra : INT32_MAX;
     share = share < kAttnMinPart ? kAttnMinPart : (share + kAttnTile - 1) / kAttnTile * kAttnTile;
     const int32_t cut = (int32_t)(share < INT32_MAX ? share : INT32_MAX);
     int32_t item0 = 0, slot0 = 0;
@@ -481,11 +488,10 @@ __device__ inline bool find_item(const AttnArgs &a, int32_t want, bool by_row, S
         int32_t items, slots;
         const int32_t at = item0 + scan_items<THREADS>(parts, wave_sums, items);
         const int32_t slot = slot0 + scan_items<THREADS>(parts > 1 ? parts : 0, wave_sums, slots);
-        if (by_row ? c + tid == want : want >= at && want < at + parts)
-            found = Sched{c + tid, by_row ? 0 : want - at, parts, slot, cut, rs};
+        if (want >= at && want < at + parts) found = Sched{c + tid, want - at, parts, slot, cut, rs};
         item0 += items;
         slot0 += slots;
-        if (by_row ? want < c + THREADS : want < item0) break;
+        if (want < item0) break;
     }
     __syncthreads();
     out = found;
@@ -540,6 +546,114 @@ struct Weight<BF16> {
     }
 };
 
+// Four columns of a finished row: sum / l, rounded once; an empty row is 0.
+template <typename T>
+__device__ inline void write_row(const AttnArgs &a, int64_t row, int64_t head, int d, const f4_t &sum, float m, float l)
+{
+    typedef typename T::elem E;
+    typedef E e4 __attribute__((ext_vector_type(4)));
+    const bool none = l == 0.f;
+    e4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = (E)(none ? 0.f : sum[e] / l);
+    *reinterpret_cast<e4 *>(static_cast<E *>(a.out) + row * a.ldo + head * a.head_dim + d) = r;
+    if (a.lse && d == 0)
+        a.lse[row * a.q_heads + head] = none ? -INFINITY : (m + (__builtin_log2f(l) - Weight<T>::kBias)) * kLn2;
+}
+
+// A split row's sums pass between workgroups of different XCDs, whose L2s are not coherent:
+// they are stored and loaded device-coherently (relaxed atomics of device scope, which the
+// hardware takes past the local L2), ordered by the waits in last_arrival.  Fences of
+// device scope instead write back and invalidate a whole L2 each: measured on the 7B
+// decode batch, 393 us against 120.
+__device__ inline void put_part(float *p, float x, float y)
+{
+    const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, y) << 32 | __builtin_bit_cast(uint32_t, x);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline float2 get_part(const float *p)
+{
+    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__builtin_bit_cast(float, (uint32_t)v), __builtin_bit_cast(float, (uint32_t)(v >> 32)));
+}
+
+// True in the workgroup that is the n-th to come here with this counter, which is then 0
+// again.  Every wavefront waits for its own stores to complete before the workgroup
+// counts itself, so the last one's loads find all parts.
+__device__ inline bool last_arrival(uint32_t *count, int n)
+{
+    __shared__ bool last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
+        if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    return last;
+}
+
+// Adds n parts (part0, part0 + step, ...) of a split row's heads, in that order, into part0's
+// slot, or with `finish` into the row.
+template <typename T, int DP>
+__device__ inline void join_parts(const AttnArgs &a, const Sched &sc, int64_t head0, int heads, int part0, int step,
+                                  int n, bool finish)
+{
+    __shared__ float2 joined[16];
+    const int cols = a.head_dim / 4, tid = threadIdx.x;
+    const int64_t pitch = (int64_t)step * a.q_heads;
+    for (int i0 = 0; i0 < heads * cols; i0 += 64 * kAttnWaves) {
+        const int i = i0 + tid;
+        const bool on = i < heads * cols;
+        const int h = on ? i / cols : 0, d = on ? 4 * (i - h * cols) : 0;
+        const int64_t slot = (int64_t)(sc.slot0 + part0) * a.q_heads + head0 + h;
+        const float *const ml = a.part_ml + 2 * slot, *const po = a.part_o + slot * a.head_dim + d;
+        // kAttnJoin parts at a time, all their loads in flight together
+        float m = -INFINITY, l = 0.f;
+        f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int p0 = 0; p0 < n; p0 += kAttnJoin) {
+            float2 v[kAttnJoin], x[kAttnJoin], y[kAttnJoin];
+#pragma unroll
+            for (int p = 0; p < kAttnJoin; ++p) {
+                const int64_t at = min(p0 + p, n - 1) * pitch;
+                v[p] = get_part(&ml[2 * at]);
+                x[p] = get_part(&po[at * a.head_dim]);
+                y[p] = get_part(&po[at * a.head_dim + 2]);
+            }
+            float mx = m;
+#pragma unroll
+            for (int p = 0; p < kAttnJoin; ++p) mx = __builtin_fmaxf(mx, v[p].x);
+            const float base = mx == -INFINITY ? 0.f : mx, keep = __builtin_amdgcn_exp2f(m - base);
+            l *= keep;
+            sum *= keep;
+            m = mx;
+#pragma unroll
+            for (int p = 0; p < kAttnJoin; ++p) {
+                const bool in = p0 + p < n;  // past the end the last part is read again, and not added
+                const float f = __builtin_amdgcn_exp2f(v[p].x - base);
+                l = in ? __builtin_fmaf(v[p].y, f, l) : l;
+                const f4_t more = sum + f4_t{x[p].x, x[p].y, y[p].x, y[p].y} * f;
+                sum = in ? more : sum;
+            }
+        }
+        if (!on) continue;
+        if (finish) {
+            write_row<T>(a, sc.row, head0 + h, d, sum, m, l);
+        } else {
+            put_part(&a.part_o[slot * a.head_dim + d], sum[0], sum[1]);  // these columns are read by this lane only
+            put_part(&a.part_o[slot * a.head_dim + d + 2], sum[2], sum[3]);
+            if (d == 0) joined[h] = make_float2(m, l);
+        }
+    }
+    if (finish) return;
+    __syncthreads();  // every lane has read its heads' (m, l) of part0
+    if (tid < heads)
+        put_part(&a.part_ml[2 * ((int64_t)(sc.slot0 + part0) * a.q_heads + head0 + tid)], joined[tid].x, joined[tid].y);
+}
+
+// Wavefronts per SIMD the registers are kept to.
+constexpr int attn_occupancy(int dp) { return dp <= 64 ? 4 : dp <= 128 ? 3 : 1; }
+
 // One workgroup per (part, key/value head, 16 of its query heads).
 //
 // Each wavefront walks its 32-token tiles of the part with its own running maximum and
@@ -556,7 +670,8 @@ struct Weight<BF16> {
 // Bound by reading K and V once; every head of a group shares the read, and 16 columns of
 // heads cost the same matrix instructions as one.
 template <typename T, int DP, bool FULL>
-__global__ __launch_bounds__(64 * kAttnWaves) void lora_paged_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(attn_occupancy(DP)))) void
+lora_paged_attention_kernel(AttnArgs a)
 {
     typedef typename T::elem E;
     typedef short s4 __attribute__((ext_vector_type(4)));
@@ -574,7 +689,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void lora_paged_attention_kernel(A
     const int32_t item = blockIdx.x / per_item, rest = blockIdx.x - item * per_item;
     const int kvh = rest / a.head_tiles, ht = rest - kvh * a.head_tiles;
     Sched sc;
-    if (!find_item<64 * kAttnWaves>(a, item, false, sc)) return;
+    if (!find_item<64 * kAttnWaves>(a, item, sc)) return;
 
     const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
@@ -752,70 +867,33 @@ __global__ __launch_bounds__(64 * kAttnWaves) void lora_paged_attention_kernel(A
         const int64_t head = head0 + h;
         if (sc.parts > 1) {
             const int64_t slot = (int64_t)(sc.slot0 + sc.part) * a.q_heads + head;
-            *reinterpret_cast<f4_t *>(&a.part_o[slot * a.head_dim + d]) = sum;
-            if (d == 0) {
-                a.part_ml[2 * slot] = hm;
-                a.part_ml[2 * slot + 1] = hl;
-            }
-            continue;
+            put_part(&a.part_o[slot * a.head_dim + d], sum[0], sum[1]);
+            put_part(&a.part_o[slot * a.head_dim + d + 2], sum[2], sum[3]);
+            if (d == 0) put_part(&a.part_ml[2 * slot], hm, hl);
+        } else {
+            write_row<T>(a, sc.row, head, d, sum, hm, hl);
         }
-        const bool none = hl == 0.f;
-        typedef E e4 __attribute__((ext_vector_type(4)));
-        e4 r;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = (E)(none ? 0.f : sum[e] / hl);
-        *reinterpret_cast<e4 *>(static_cast<E *>(a.out) + sc.row * a.ldo + head * a.head_dim + d) = r;
-        if (a.lse && d == 0)
-            a.lse[(int64_t)sc.row * a.q_heads + head] =
-                none ? -INFINITY : (hm + (__builtin_log2f(hl) - Weight<T>::kBias)) * kLn2;
     }
+    if (sc.parts < 2) return;
+    // A split row: of every kAttnJoin parts, the workgroup that arrives last adds them up in
+    // order into the first one's slot; of those sums, the last arrival adds all and writes
+    // the row.  Who that is does not change what is added in which order.
+    const int group0 = sc.part / kAttnJoin * kAttnJoin, n_groups = (sc.parts + kAttnJoin - 1) / kAttnJoin;
+    const int in_group = min(kAttnJoin, sc.parts - group0);
+    uint32_t *const count = a.count + (int64_t)sc.slot0 * per_item + rest;
+    if (!last_arrival(count + group0 * per_item, in_group)) return;
+    join_parts<T, DP>(a, sc, head0, heads, group0, 1, in_group, n_groups == 1);
+    if (n_groups == 1 || !last_arrival(count + per_item, n_groups)) return;  // part 1 leads no group
+    join_parts<T, DP>(a, sc, head0, heads, 0, kAttnJoin, n_groups, true);
 }
 
-// Joins the parts of rows that were split: one workgroup per (row, head), its lanes over
-// the parts' maxima and sums first, then over the columns; parts are added in order.
-template <typename T>
-__global__ __launch_bounds__(256) void lora_attention_join_kernel(AttnArgs a)
+int32_t attn_tiles(int32_t q_heads, int32_t kv_heads)
 {
-    typedef typename T::elem E;
-    __shared__ float red[8];
-    const int tid = threadIdx.x;
-    const int32_t row = blockIdx.x / a.q_heads;
-    const int head = blockIdx.x - row * a.q_heads;
-    Sched sc;
-    if (!find_item<256>(a, row, true, sc) || sc.parts < 2) return;
-    const int64_t slot0 = (int64_t)sc.slot0 * a.q_heads + head;
-    float m = -INFINITY;
-    for (int p = tid; p < sc.parts; p += 256) m = __builtin_fmaxf(m, a.part_ml[2 * (slot0 + (int64_t)p * a.q_heads)]);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    if ((tid & 63) == 0) red[tid >> 6] = m;
-    __syncthreads();
-    m = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int p = 0; p < sc.parts; ++p) {
-        const float *ml = &a.part_ml[2 * (slot0 + (int64_t)p * a.q_heads)];
-        l = __builtin_fmaf(ml[1], __builtin_amdgcn_exp2f(ml[0] - base), l);
-    }
-    const bool none = l == 0.f;
-    for (int d = tid; d < a.head_dim; d += 256) {
-        float s = 0.f;
-        for (int p = 0; p < sc.parts; ++p) {
-            const int64_t slot = slot0 + (int64_t)p * a.q_heads;
-            s = __builtin_fmaf(a.part_o[slot * a.head_dim + d], __builtin_amdgcn_exp2f(a.part_ml[2 * slot] - base), s);
-        }
-        static_cast<E *>(a.out)[row * a.ldo + (int64_t)head * a.head_dim + d] = (E)(none ? 0.f : s / l);
-    }
-    if (a.lse && tid == 0)
-        a.lse[(int64_t)row * a.q_heads + head] = none ? -INFINITY : (m + (__builtin_log2f(l) - Weight<T>::kBias)) * kLn2;
+    return (int32_t)std::min<int64_t>((int64_t)kv_heads * ((q_heads / kv_heads + 15) / 16), INT32_MAX);
 }
 
 // Work items beyond one per row, by shape alone (the lengths are on the device).
-int32_t attn_extra(int32_t q_heads, int32_t kv_heads)
-{
-    const int64_t per_item = (int64_t)kv_heads * ((q_heads / kv_heads + 15) / 16);
-    return (int32_t)std::max<int64_t>(1, (kAttnGroups + per_item - 1) / per_item);
-}
+int32_t attn_extra(int32_t tiles) { return std::max(1, (kAttnGroups + tiles - 1) / tiles); }
 
 template <typename T>
 void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
@@ -828,7 +906,6 @@ void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
     else if (D <= 128) LORA_ATTN(128);
     else LORA_ATTN(256);
 #undef LORA_ATTN
-    launch_args(lora_attention_join_kernel<T>, dim3((unsigned)(a.n_rows * a.q_heads)), 256, 0, s, a);
 }
 
 // ------------------------------------------------------------------------ residual add and norms
@@ -1097,8 +1174,10 @@ size_t lora_paged_attention_bytes(int32_t n_rows, int32_t q_heads, int32_t kv_he
     if (n_rows < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || head_dim < 8 ||
         head_dim > LORA_KV_MAX_HEAD_DIM || head_dim % 8)
         return 0;
-    const size_t slots = 2 * (size_t)attn_extra(q_heads, kv_heads) * q_heads;
-    return (slots * (head_dim + 2) * sizeof(float) + 255) & ~size_t(255);
+    const int32_t tiles = attn_tiles(q_heads, kv_heads);
+    if (tiles > kAttnMaxTiles) return 0;
+    const size_t slots = 2 * (size_t)attn_extra(tiles) * q_heads;
+    return (kAttnCounters * sizeof(uint32_t) + slots * (head_dim + 2) * sizeof(float) + 255) & ~size_t(255);
 }
 
 int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *out, int64_t ldo, const void *q,
@@ -1118,6 +1197,8 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     if (!std::isfinite(scale)) return fail(LORA_E_SHAPE, "scale is not finite");
     if ((int64_t)n_rows * q_heads > (int64_t)1 << 30)
         return fail(LORA_E_SHAPE, "%d rows of %d heads are too many for one launch", n_rows, q_heads);
+    if (attn_tiles(q_heads, cache->kv_heads) > kAttnMaxTiles)
+        return fail(LORA_E_UNSUPPORTED, "%d key/value heads of %d query heads", cache->kv_heads, q_heads);
     if (n_rows == 0) return LORA_OK;
     if ((st = check_matrix(q, ldq, (int64_t)q_heads * cache->head_dim, "q"))) return st;
     if ((st = check_matrix(out, ldo, (int64_t)q_heads * cache->head_dim, "out"))) return st;
@@ -1140,7 +1221,10 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.shift = page_shift(cache->page_size);
     a.group = q_heads / cache->kv_heads;
     a.head_tiles = (a.group + 15) / 16;
-    a.extra = attn_extra(q_heads, cache->kv_heads);
+    const int32_t tiles = attn_tiles(q_heads, cache->kv_heads), most = attn_extra(tiles);
+    // no row is longer than its table or the window, so it has no more parts than that
+    const int64_t span = std::min<int64_t>((int64_t)max_blocks * cache->page_size, window > 0 ? window : INT32_MAX);
+    a.extra = (int32_t)std::min<int64_t>(most, (span - 1) / kAttnMinPart * n_rows);
     a.scale = scale;
     a.out = out;
     a.q = q;
@@ -1152,11 +1236,12 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.req = req;
     a.lse = lse;
     a.c = *cache;
-    const size_t slots = 2 * (size_t)a.extra * q_heads;
-    a.part_o = static_cast<float *>(work);
+    const size_t slots = 2 * (size_t)most * q_heads;
+    a.count = static_cast<uint32_t *>(work);
+    a.part_o = reinterpret_cast<float *>(a.count + kAttnCounters);
     a.part_ml = a.part_o + slots * cache->head_dim;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t groups = ((int64_t)n_rows + a.extra) * a.kv_heads * a.head_tiles;
+    const int64_t groups = ((int64_t)n_rows + a.extra) * tiles;
     if (groups > (int64_t)1 << 30) return fail(LORA_E_SHAPE, "launch of %lld workgroups is too large", (long long)groups);
     const dim3 grid((unsigned)groups);
     if (cache->type == LORA_TYPE_BF16) attention_launch<BF16>(a, grid, s);
