@@ -381,7 +381,8 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
 // ------------------------------------------------------------------------ attention
 struct AttnArgs {
     int32_t n_rows, q_heads, kv_heads, head_dim, n_req, max_blocks, window, shift;
-    int32_t group, head_tiles, extra;  // query heads per key/value head; its 16-head tiles; work items beyond one per row
+    int32_t group, head_tiles;  // query heads per key/value head; its 16-head tiles
+    int32_t shares;             // workgroups per head tile
     float scale;
     void *out;
     const void *q;
@@ -396,14 +397,17 @@ struct AttnArgs {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kAttnWaves = 4;        // wavefronts of an attention workgroup
 constexpr int kAttnTile = 32;        // tokens a wavefront takes at a time
-constexpr int kAttnMinPart = 512;    // shortest part worth a workgroup of its own
-constexpr int kAttnGroups = 2048;    // workgroups aimed at beyond one per (row, head tile)
+constexpr int kAttnMinShare = 16;    // tiles a workgroup takes at least
+constexpr int kAttnRowTiles = 2;     // what starting and finishing a row costs, in tiles
 constexpr int kAttnJoin = 16;        // parts joined at a time
 constexpr int kAttnMaxTiles = 4096;  // key/value heads x 16-head tiles of one launch
-// Arrival counters, one per part slot and head tile: 2 * extra * tiles <= 2 * (kAttnGroups + tiles).
-// They lie first in a workspace, at one size for every shape, so calls of different shapes
-// sharing a workspace never put sums where another finds its counters.
-constexpr size_t kAttnCounters = 2 * (kAttnGroups + kAttnMaxTiles);
+constexpr int kAttnCUs = 256;
+// Wavefronts per SIMD, and so workgroups per CU, that the registers are kept to.
+constexpr int attn_occupancy(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
+// Arrival counters: two part slots per workgroup, and at most 4 workgroups per CU or one
+// per head tile.  They lie first in a workspace, at one size for every shape, so calls of
+// different shapes sharing a workspace never put sums where another finds its counters.
+constexpr size_t kAttnCounters = 2 * (4 * kAttnCUs + kAttnMaxTiles);
 
 // Visible tokens [first, first + span) of row i; span -1: the row is not active.
 struct RowSpan {
@@ -422,80 +426,83 @@ __device__ inline RowSpan row_span(const AttnArgs &a, int32_t i)
     return s;
 }
 
-// The schedule of a launch, found by every workgroup from the lengths on the device: the
-// visible tokens of all rows are cut into parts of at most `cut` tokens, where cut is the
-// share of one of `extra` workgroups (so n_rows + extra work items always hold every
-// part), and a row's parts are consecutive items.  Parts of rows with several get slots
-// for their sums (2 * extra hold them all: such a row has fewer than 2 span / cut parts).
-struct Sched {
-    int32_t row, part, parts, slot0, cut;
+// The schedule of a launch, found by every workgroup from the lengths on the device.  Each
+// active row costs its visible tokens in 32-token tiles (at least one) and kAttnRowTiles
+// more; the rows' costs are laid end to end, and workgroup w takes [w share, (w + 1) share)
+// of them: parts of one or more rows, the same amount of work in every workgroup whatever
+// the lengths.  Row i's tiles lie at [tile0, tile0 + tiles) of that line.
+struct RowWork {
+    int32_t row;
+    int64_t tile0;
+    int32_t tiles;
     RowSpan rs;
 };
 
-template <int THREADS>
-__device__ inline int32_t scan_items(int32_t v, int32_t *wave_sums, int32_t &total)
+__device__ inline int32_t row_tiles(const RowSpan &rs)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int32_t s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int32_t up = __shfl_up(s, d);
-        if (lane >= d) s += up;
-    }
-    __syncthreads();
-    if (lane == 63) wave_sums[wave] = s;
-    __syncthreads();
-    int32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-        const int32_t x = wave_sums[w];
-        before += w < wave ? x : 0;
-        all += x;
-    }
-    total = all;
-    return before + s - v;
+    return rs.span < 0 ? 0 : rs.span <= kAttnTile ? 1 : (rs.span - 1) / kAttnTile + 1;
 }
 
-// Item `want` of the schedule; false: there is no such item.
-template <int THREADS>
-__device__ inline bool find_item(const AttnArgs &a, int32_t want, Sched &out)
+// The same value in every lane, for the scalar registers.
+__device__ inline int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t uniform(int64_t v)
 {
-    __shared__ int32_t wave_sums[THREADS / 64];
+    return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32 | (uint32_t)uniform((int32_t)v));
+}
+
+// The first row with work at or behind position w * share (row n_rows: none), and the share.
+template <int THREADS>
+__device__ inline RowWork first_row(const AttnArgs &a, int32_t w, int64_t &share)
+{
     __shared__ int64_t totals[THREADS / 64];
-    __shared__ Sched found;
-    const int tid = threadIdx.x;
+    __shared__ RowWork found;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     RowSpan rs = row_span(a, tid);
-    int64_t total = rs.span > 0 ? rs.span : 0;
-    for (int32_t i = tid + THREADS; i < a.n_rows; i += THREADS) {
-        const int32_t sp = row_span(a, i).span;
-        total += sp > 0 ? sp : 0;
+    int64_t total = 0;
+    for (int32_t i = tid; i < a.n_rows; i += THREADS) {
+        const int32_t t = row_tiles(i == tid ? rs : row_span(a, i));
+        total += t > 0 ? t + kAttnRowTiles : 0;
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-    if ((tid & 63) == 0) totals[tid >> 6] = total;
-    if (tid == 0) found.row = -1;
+    if (lane == 0) totals[wave] = total;
+    if (tid == 0) found.row = a.n_rows;
     __syncthreads();
     total = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) total += totals[w];
-    int64_t share = a.extra > 0 ? (total + a.extra - 1) / a.extra : INT32_MAX;
-    share = share < kAttnMinPart ? kAttnMinPart : (share + kAttnTile - 1) / kAttnTile * kAttnTile;
-    const int32_t cut = (int32_t)(share < INT32_MAX ? share : INT32_MAX);
-    int32_t item0 = 0, slot0 = 0;
-    for (int32_t c = 0; c < a.n_rows; c += THREADS) {
+    for (int v = 0; v < THREADS / 64; ++v) total += totals[v];
+    share = (total + a.shares - 1) / a.shares;
+    if (share < kAttnMinShare) share = kAttnMinShare;
+    const int64_t begin = w * share;
+    int64_t at0 = 0;
+    for (int32_t c = 0; c < a.n_rows && begin < total; c += THREADS) {
         if (c > 0) rs = row_span(a, c + tid);
-        const int32_t parts = rs.span < 0 ? 0 : rs.span <= cut ? 1 : (rs.span - 1) / cut + 1;
-        int32_t items, slots;
-        const int32_t at = item0 + scan_items<THREADS>(parts, wave_sums, items);
-        const int32_t slot = slot0 + scan_items<THREADS>(parts > 1 ? parts : 0, wave_sums, slots);
-        if (want >= at && want < at + parts) found = Sched{c + tid, want - at, parts, slot, cut, rs};
-        item0 += items;
-        slot0 += slots;
-        if (want < item0) break;
+        const int32_t tiles = row_tiles(rs), cost = tiles > 0 ? tiles + kAttnRowTiles : 0;
+        int64_t at = cost;  // inclusive prefix over the wavefront, then the workgroup
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int64_t up = __shfl_up(at, d);
+            if (lane >= d) at += up;
+        }
+        __syncthreads();
+        if (lane == 63) totals[wave] = at;
+        __syncthreads();
+        int64_t before = at0, all = at0;
+#pragma unroll
+        for (int v = 0; v < THREADS / 64; ++v) {
+            before += v < wave ? totals[v] : 0;
+            all += totals[v];
+        }
+        at += before - cost;  // this row's first position
+        if (cost > 0 && at <= begin && begin < at + cost) found = RowWork{c + tid, at + kAttnRowTiles, tiles, rs};
+        at0 = all;
+        if (begin < at0) break;
     }
     __syncthreads();
-    out = found;
-    return out.row >= 0;
+    share = uniform(share);
+    const RowWork r = found;
+    return RowWork{uniform(r.row), uniform(r.tile0), uniform(r.tiles),
+                   RowSpan{uniform(r.rs.req), uniform(r.rs.first), uniform(r.rs.span)}};
 }
 
 __device__ inline f4_t mfma(const vec8<F16> &x, const vec8<F16> &y, const f4_t &c)
@@ -593,42 +600,44 @@ __device__ inline bool last_arrival(uint32_t *count, int n)
     return last;
 }
 
+// Slot of part p of a row whose first part is in workgroup w0: a workgroup has one slot for
+// the row it found begun and one for the row it leaves unfinished.
+__device__ inline int32_t part_slot(int32_t w0, int32_t p) { return p == 0 ? 2 * w0 + 1 : 2 * (w0 + p); }
+
 // Adds n parts (part0, part0 + step, ...) of a split row's heads, in that order, into part0's
 // slot, or with `finish` into the row.
 template <typename T, int DP>
-__device__ inline void join_parts(const AttnArgs &a, const Sched &sc, int64_t head0, int heads, int part0, int step,
-                                  int n, bool finish)
+__device__ inline void join_parts(const AttnArgs &a, int32_t row, int32_t w0, int64_t head0, int heads, int part0,
+                                  int step, int n, bool finish)
 {
     __shared__ float2 joined[16];
+    constexpr int kBatch = 8;
     const int cols = a.head_dim / 4, tid = threadIdx.x;
-    const int64_t pitch = (int64_t)step * a.q_heads;
     for (int i0 = 0; i0 < heads * cols; i0 += 64 * kAttnWaves) {
         const int i = i0 + tid;
         const bool on = i < heads * cols;
         const int h = on ? i / cols : 0, d = on ? 4 * (i - h * cols) : 0;
-        const int64_t slot = (int64_t)(sc.slot0 + part0) * a.q_heads + head0 + h;
-        const float *const ml = a.part_ml + 2 * slot, *const po = a.part_o + slot * a.head_dim + d;
-        // kAttnJoin parts at a time, all their loads in flight together
+        // eight parts at a time, all their loads in flight together
         float m = -INFINITY, l = 0.f;
         f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
-        for (int p0 = 0; p0 < n; p0 += kAttnJoin) {
-            float2 v[kAttnJoin], x[kAttnJoin], y[kAttnJoin];
+        for (int p0 = 0; p0 < n; p0 += kBatch) {
+            float2 v[kBatch], x[kBatch], y[kBatch];
 #pragma unroll
-            for (int p = 0; p < kAttnJoin; ++p) {
-                const int64_t at = min(p0 + p, n - 1) * pitch;
-                v[p] = get_part(&ml[2 * at]);
-                x[p] = get_part(&po[at * a.head_dim]);
-                y[p] = get_part(&po[at * a.head_dim + 2]);
+            for (int p = 0; p < kBatch; ++p) {
+                const int64_t at = (int64_t)part_slot(w0, part0 + min(p0 + p, n - 1) * step) * a.q_heads + head0 + h;
+                v[p] = get_part(&a.part_ml[2 * at]);
+                x[p] = get_part(&a.part_o[at * a.head_dim + d]);
+                y[p] = get_part(&a.part_o[at * a.head_dim + d + 2]);
             }
             float mx = m;
 #pragma unroll
-            for (int p = 0; p < kAttnJoin; ++p) mx = __builtin_fmaxf(mx, v[p].x);
+            for (int p = 0; p < kBatch; ++p) mx = __builtin_fmaxf(mx, v[p].x);
             const float base = mx == -INFINITY ? 0.f : mx, keep = __builtin_amdgcn_exp2f(m - base);
             l *= keep;
             sum *= keep;
             m = mx;
 #pragma unroll
-            for (int p = 0; p < kAttnJoin; ++p) {
+            for (int p = 0; p < kBatch; ++p) {
                 const bool in = p0 + p < n;  // past the end the last part is read again, and not added
                 const float f = __builtin_amdgcn_exp2f(v[p].x - base);
                 l = in ? __builtin_fmaf(v[p].y, f, l) : l;
@@ -638,8 +647,9 @@ __device__ inline void join_parts(const AttnArgs &a, const Sched &sc, int64_t he
         }
         if (!on) continue;
         if (finish) {
-            write_row<T>(a, sc.row, head0 + h, d, sum, m, l);
+            write_row<T>(a, row, head0 + h, d, sum, m, l);
         } else {
+            const int64_t slot = (int64_t)part_slot(w0, part0) * a.q_heads + head0 + h;
             put_part(&a.part_o[slot * a.head_dim + d], sum[0], sum[1]);  // these columns are read by this lane only
             put_part(&a.part_o[slot * a.head_dim + d + 2], sum[2], sum[3]);
             if (d == 0) joined[h] = make_float2(m, l);
@@ -648,15 +658,30 @@ __device__ inline void join_parts(const AttnArgs &a, const Sched &sc, int64_t he
     if (finish) return;
     __syncthreads();  // every lane has read its heads' (m, l) of part0
     if (tid < heads)
-        put_part(&a.part_ml[2 * ((int64_t)(sc.slot0 + part0) * a.q_heads + head0 + tid)], joined[tid].x, joined[tid].y);
+        put_part(&a.part_ml[2 * ((int64_t)part_slot(w0, part0) * a.q_heads + head0 + tid)], joined[tid].x, joined[tid].y);
 }
 
-// Wavefronts per SIMD the registers are kept to.
-constexpr int attn_occupancy(int dp) { return dp <= 64 ? 4 : dp <= 128 ? 3 : 1; }
+// The part `part` of a split row is stored: of every kAttnJoin parts, the workgroup that
+// arrives last adds them up in order into the first one's slot; of those sums, the last
+// arrival adds all and writes the row.  Who that is does not change what is added in which
+// order.
+template <typename T, int DP>
+__device__ inline void join_row(const AttnArgs &a, int32_t row, int32_t w0, int32_t parts, int32_t part, int per_share,
+                                int rest, int64_t head0, int heads)
+{
+    const int group0 = part / kAttnJoin * kAttnJoin, n_groups = (parts + kAttnJoin - 1) / kAttnJoin;
+    const int in_group = min(kAttnJoin, parts - group0);
+    if (!last_arrival(a.count + (int64_t)part_slot(w0, group0) * per_share + rest, in_group)) return;
+    join_parts<T, DP>(a, row, w0, head0, heads, group0, 1, in_group, n_groups == 1);
+    // (part 1 leads no group, so its counter is free for the groups)
+    if (n_groups == 1 || !last_arrival(a.count + (int64_t)part_slot(w0, 1) * per_share + rest, n_groups)) return;
+    join_parts<T, DP>(a, row, w0, head0, heads, 0, kAttnJoin, n_groups, true);
+}
 
-// One workgroup per (part, key/value head, 16 of its query heads).
+// One workgroup per (share of the rows, key/value head, 16 of its query heads), all of them
+// resident at once; it takes the rows of its share one after another.
 //
-// Each wavefront walks its 32-token tiles of the part with its own running maximum and
+// Each wavefront walks its 32-token tiles of a row's part with its own running maximum and
 // sums; nothing is shared until the end, so the loop has no barrier.  Scores are
 // S^T = K Q^T on v_mfma_f32_16x16x32: the K rows go from memory straight into the A
 // operand (lane: token l % 16, 16 bytes of it), Q^T stays in registers.  A lane then
@@ -685,82 +710,112 @@ lora_paged_attention_kernel(AttnArgs a)
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
-    const int per_item = a.kv_heads * a.head_tiles;
-    const int32_t item = blockIdx.x / per_item, rest = blockIdx.x - item * per_item;
+    const int per_share = a.kv_heads * a.head_tiles;
+    const int32_t wg = blockIdx.x / per_share, rest = blockIdx.x - wg * per_share;
     const int kvh = rest / a.head_tiles, ht = rest - kvh * a.head_tiles;
-    Sched sc;
-    if (!find_item<64 * kAttnWaves>(a, item, sc)) return;
-
     const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
-    const int32_t begin = sc.rs.first + sc.part * sc.cut;
-    const int32_t end = sc.rs.first + (sc.rs.span - sc.part * sc.cut < sc.cut ? sc.rs.span : (sc.part + 1) * sc.cut);
-    const int32_t *table = a.table + (int64_t)sc.rs.req * a.ld_table;
     const int32_t in_page = (1 << a.shift) - 1;
+    int64_t share;
+    RowWork rw = first_row<64 * kAttnWaves>(a, wg, share);
+    const int64_t line0 = wg * share, line1 = line0 + share;
 
-    vec8<T> q[KC];
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        const int d = 32 * c + 8 * lg;
-        if (li < heads && (FULL || d < a.head_dim)) r = load16(a.q, sc.row * a.ldq + (head0 + li) * a.head_dim + d);
-        q[c] = __builtin_bit_cast(vec8<T>, r);
-    }
-
+    // A row's part in this share: tokens [begin, end); the row has `parts` parts from workgroup w0 on.
+    struct Part {
+        int32_t row, begin, end, w0, parts;
+        const int32_t *table;
+    };
+    auto next_part = [&]() {
+        while (rw.row < a.n_rows) {
+            const int64_t row_end = rw.tile0 + rw.tiles;
+            const int64_t from = max(rw.tile0, line0), to = min(row_end, line1), tile0 = rw.tile0;
+            const Part p{rw.row, rw.rs.first + (int32_t)(from - tile0) * kAttnTile,
+                         rw.rs.first + (int32_t)min((to - tile0) * kAttnTile, (int64_t)rw.rs.span),
+                         tile0 < line0 ? (int32_t)(tile0 / share) : wg, 1, a.table + (int64_t)rw.rs.req * a.ld_table};
+            int32_t last = wg;
+            if (row_end > line1) last = (int32_t)((row_end - 1) / share);
+            do {
+                rw.rs = row_span(a, ++rw.row);
+                rw.tiles = row_tiles(rw.rs);
+            } while (rw.tiles == 0 && rw.row < a.n_rows);
+            rw.tile0 = row_end + kAttnRowTiles;
+            if (row_end >= line1) rw.row = a.n_rows;
+            if (from < to) return Part{p.row, p.begin, p.end, p.w0, last - p.w0 + 1, p.table};
+            // else the row's tiles lie in the next workgroup's share
+        }
+        return Part{-1, 0, 0, 0, 0, nullptr};
+    };
     // Tokens t0 + li and t0 + 16 + li of a tile: table entries, then cell offsets; a token
     // past the end or without a page reads cell 0 and is masked.
-    auto ids_of = [&](int32_t t0, int32_t (&id)[2]) {
+    auto ids_of = [&](const Part &p, int32_t t0, int32_t (&id)[2]) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int32_t t = min(t0 + 16 * s + li, end - 1);
-            id[s] = table[t >> a.shift];
-        }
+        for (int u = 0; u < 2; ++u) id[u] = t0 < p.end ? p.table[min(t0 + 16 * u + li, p.end - 1) >> a.shift] : -1;
     };
-    auto cells_of = [&](int32_t t0, const int32_t (&id)[2], int64_t (&cell)[2]) {
+    auto cells_of = [&](const Part &p, int32_t t0, const int32_t (&id)[2], int64_t (&cell)[2]) {
         uint32_t seen = 0;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int32_t t = t0 + 16 * s + li;
-            const bool ok = t < end && id[s] >= 0 && id[s] < a.c.num_pages;
-            cell[s] = ok ? (int64_t)id[s] * a.c.page_stride + (int64_t)(t & in_page) * a.c.token_stride +
+        for (int u = 0; u < 2; ++u) {
+            const int32_t t = t0 + 16 * u + li;
+            const bool ok = t < p.end && id[u] >= 0 && id[u] < a.c.num_pages;
+            cell[u] = ok ? (int64_t)id[u] * a.c.page_stride + (int64_t)(t & in_page) * a.c.token_stride +
                                kvh * a.c.head_stride : 0;
-            seen |= ((uint32_t)__ballot(ok) & 0xffffu) << (16 * s);
+            seen |= ((uint32_t)__ballot(ok) & 0xffffu) << (16 * u);
         }
         return seen;
     };
     auto load_rows = [&](const void *base, const int64_t (&cell)[2], uint4 (&r)[2][KC]) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const int d = 32 * c + 8 * lg;
-                r[s][c] = load16(base, cell[s] + (FULL || d < a.head_dim ? d : 0));
+                r[u][c] = load16(base, cell[u] + (FULL || d < a.head_dim ? d : 0));
             }
     };
-    const uint4 zero4 = make_uint4(0, 0, 0, 0);
-
-    float m = -INFINITY, l = 0.f;
-    f4_t o[DB];
+    auto load_q = [&](int32_t row, uint4 (&r)[KC]) {
 #pragma unroll
-    for (int b = 0; b < DB; ++b) o[b] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < KC; ++c) {
+            const int d = 32 * c + 8 * lg;
+            r[c] = make_uint4(0, 0, 0, 0);
+            if (li < heads && (FULL || d < a.head_dim)) r[c] = load16(a.q, row * a.ldq + (head0 + li) * a.head_dim + d);
+        }
+    };
+
+    constexpr int kStep = kAttnWaves * kAttnTile;
+    const uint4 zero4 = make_uint4(0, 0, 0, 0);
     const float scale = a.scale * kLog2e;
     uint16_t *const tile = vt[wave];
     const int tr_row = 4 * lg + (li >> 2), tr_col = 4 * (li & 3);
     typedef __attribute__((address_space(3))) s4 *lds4;
 
-    constexpr int kStep = kAttnWaves * kAttnTile;
-    int32_t t0 = begin + wave * kAttnTile;
-    if (t0 < end) {
-        int32_t id[2], id_next[2];
-        int64_t cell[2];
-        uint4 kr[2][KC], vr[2][KC];
-        ids_of(t0, id);
-        ids_of(t0 + kStep, id_next);
-        uint32_t seen = cells_of(t0, id, cell);
-        load_rows(a.c.k, cell, kr);
-        load_rows(a.c.v, cell, vr);
+    // What is in flight: the K and V rows of this wavefront's next tile (cell, seen), which
+    // may be the first of the next part, and the page ids of the tile after it (id).
+    Part part = next_part();
+    if (part.row < 0) return;
+    int32_t id[2];
+    int64_t cell[2];
+    uint4 kr[2][KC], vr[2][KC], q[KC];
+    int32_t t0 = part.begin + wave * kAttnTile;
+    ids_of(part, t0, id);
+    load_q(part.row, q);
+    uint32_t seen = cells_of(part, t0, id, cell);
+    load_rows(a.c.k, cell, kr);
+    load_rows(a.c.v, cell, vr);
+    ids_of(part, t0 + kStep, id);
+
+    for (;;) {
+        const Part next = next_part();
+        const int32_t next_t0 = next.begin + wave * kAttnTile;
+        int32_t next_id[2];
+        ids_of(next, next_t0, next_id);
+        float m = -INFINITY, l = 0.f;
+        f4_t o[DB];
+#pragma unroll
+        for (int b = 0; b < DB; ++b) o[b] = f4_t{0.f, 0.f, 0.f, 0.f};
+
+        // A wavefront without a tile in this part runs the loop once on masked tokens.
         for (;;) {
-            const bool more = t0 + kStep < end;
+            const bool more = t0 + kStep < part.end;
             f4_t s[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -768,16 +823,20 @@ lora_paged_attention_kernel(AttnArgs a)
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
                     const uint4 r = FULL || 32 * c + 8 * lg < a.head_dim ? kr[u][c] : zero4;
-                    s[u] = mfma(__builtin_bit_cast(vec8<T>, r), q[c], s[u]);
+                    s[u] = mfma(__builtin_bit_cast(vec8<T>, r), __builtin_bit_cast(vec8<T>, q[c]), s[u]);
                 }
             }
             const uint32_t seen_now = seen;
             const bool mine[2] = {(seen_now >> li & 1) != 0, (seen_now >> (16 + li) & 1) != 0};
             if (more) {
-                seen = cells_of(t0 + kStep, id_next, cell);
-                ids_of(t0 + 2 * kStep, id_next);
-                load_rows(a.c.k, cell, kr);
+                seen = cells_of(part, t0 + kStep, id, cell);
+                ids_of(part, t0 + 2 * kStep, id);
+            } else {
+                seen = cells_of(next, next_t0, next_id, cell);
+                ids_of(next, next_t0 + kStep, id);
+                load_q(next.row < 0 ? part.row : next.row, q);
             }
+            load_rows(a.c.k, cell, kr);
             // scores in base 2, the running maximum of this lane's head
             float x[8], mx = m;
 #pragma unroll
@@ -820,7 +879,7 @@ lora_paged_attention_kernel(AttnArgs a)
                 }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
-            if (more) load_rows(a.c.v, cell, vr);
+            load_rows(a.c.v, cell, vr);
 #pragma unroll
             for (int b = 0; b < DB; ++b) {
                 const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(&tile[tr_row * kPitch + 16 * b + tr_col]));
@@ -834,57 +893,52 @@ lora_paged_attention_kernel(AttnArgs a)
             if (!more) break;
             t0 += kStep;
         }
-    }
-    // Join the wavefronts: every one's sums in LDS, scaled to the common maximum.
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (lg == 0) {
-        jm[wave][li] = m;
-        jl[wave][li] = l;
-    }
-    __syncthreads();
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mx = __builtin_fmaxf(mx, jm[w][li]);
-    const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
-    float *const mine_o = reinterpret_cast<float *>(vt[wave]);
-    if (li < heads)
-#pragma unroll
-        for (int b = 0; b < DB; ++b) *reinterpret_cast<f4_t *>(&mine_o[li * DP + 16 * b + 4 * lg]) = o[b] * f;
-    __syncthreads();
-    for (int i = tid; i < heads * (DP / 4); i += 64 * kAttnWaves) {
-        const int h = i / (DP / 4), d = 4 * (i - h * (DP / 4));
-        if (!FULL && d >= a.head_dim) continue;
-        float hm = -INFINITY, hl = 0.f;
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) hm = __builtin_fmaxf(hm, jm[w][h]);
-        f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
-            hl = __builtin_fmaf(jl[w][h], __builtin_amdgcn_exp2f(jm[w][h] - (hm == -INFINITY ? 0.f : hm)), hl);
-            sum += *reinterpret_cast<const f4_t *>(&reinterpret_cast<const float *>(vt[w])[h * DP + d]);
+        // Join the wavefronts: every one's sums in LDS, scaled to the common maximum.
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (lg == 0) {
+            jm[wave][li] = m;
+            jl[wave][li] = l;
         }
-        const int64_t head = head0 + h;
-        if (sc.parts > 1) {
-            const int64_t slot = (int64_t)(sc.slot0 + sc.part) * a.q_heads + head;
-            put_part(&a.part_o[slot * a.head_dim + d], sum[0], sum[1]);
-            put_part(&a.part_o[slot * a.head_dim + d + 2], sum[2], sum[3]);
-            if (d == 0) put_part(&a.part_ml[2 * slot], hm, hl);
-        } else {
-            write_row<T>(a, sc.row, head, d, sum, hm, hl);
+        __syncthreads();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) mx = __builtin_fmaxf(mx, jm[w][li]);
+        const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
+        float *const mine_o = reinterpret_cast<float *>(vt[wave]);
+        if (li < heads)
+#pragma unroll
+            for (int b = 0; b < DB; ++b) *reinterpret_cast<f4_t *>(&mine_o[li * DP + 16 * b + 4 * lg]) = o[b] * f;
+        __syncthreads();
+        for (int i = tid; i < heads * (DP / 4); i += 64 * kAttnWaves) {
+            const int h = i / (DP / 4), d = 4 * (i - h * (DP / 4));
+            if (!FULL && d >= a.head_dim) continue;
+            float hm = -INFINITY, hl = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) hm = __builtin_fmaxf(hm, jm[w][h]);
+            f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w) {
+                hl = __builtin_fmaf(jl[w][h], __builtin_amdgcn_exp2f(jm[w][h] - (hm == -INFINITY ? 0.f : hm)), hl);
+                sum += *reinterpret_cast<const f4_t *>(&reinterpret_cast<const float *>(vt[w])[h * DP + d]);
+            }
+            const int64_t head = head0 + h;
+            if (part.parts > 1) {
+                const int64_t slot = (int64_t)part_slot(part.w0, wg - part.w0) * a.q_heads + head;
+                put_part(&a.part_o[slot * a.head_dim + d], sum[0], sum[1]);
+                put_part(&a.part_o[slot * a.head_dim + d + 2], sum[2], sum[3]);
+                if (d == 0) put_part(&a.part_ml[2 * slot], hm, hl);
+            } else {
+                write_row<T>(a, part.row, head, d, sum, hm, hl);
+            }
         }
+        if (part.parts > 1)
+            join_row<T, DP>(a, part.row, part.w0, part.parts, wg - part.w0, per_share, rest, head0, heads);
+        if (next.row < 0) break;
+        __syncthreads();  // the join is done with the LDS tiles
+        part = next;
+        t0 = next_t0;
     }
-    if (sc.parts < 2) return;
-    // A split row: of every kAttnJoin parts, the workgroup that arrives last adds them up in
-    // order into the first one's slot; of those sums, the last arrival adds all and writes
-    // the row.  Who that is does not change what is added in which order.
-    const int group0 = sc.part / kAttnJoin * kAttnJoin, n_groups = (sc.parts + kAttnJoin - 1) / kAttnJoin;
-    const int in_group = min(kAttnJoin, sc.parts - group0);
-    uint32_t *const count = a.count + (int64_t)sc.slot0 * per_item + rest;
-    if (!last_arrival(count + group0 * per_item, in_group)) return;
-    join_parts<T, DP>(a, sc, head0, heads, group0, 1, in_group, n_groups == 1);
-    if (n_groups == 1 || !last_arrival(count + per_item, n_groups)) return;  // part 1 leads no group
-    join_parts<T, DP>(a, sc, head0, heads, 0, kAttnJoin, n_groups, true);
 }
 
 int32_t attn_tiles(int32_t q_heads, int32_t kv_heads)
@@ -892,8 +946,11 @@ int32_t attn_tiles(int32_t q_heads, int32_t kv_heads)
     return (int32_t)std::min<int64_t>((int64_t)kv_heads * ((q_heads / kv_heads + 15) / 16), INT32_MAX);
 }
 
-// Work items beyond one per row, by shape alone (the lengths are on the device).
-int32_t attn_extra(int32_t tiles) { return std::max(1, (kAttnGroups + tiles - 1) / tiles); }
+// Workgroups per head tile: what the CUs hold at once.
+int32_t attn_shares(int32_t tiles, int32_t head_dim)
+{
+    return std::max(1, kAttnCUs * attn_occupancy(head_dim) / tiles);
+}
 
 template <typename T>
 void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
@@ -1176,7 +1233,7 @@ size_t lora_paged_attention_bytes(int32_t n_rows, int32_t q_heads, int32_t kv_he
         return 0;
     const int32_t tiles = attn_tiles(q_heads, kv_heads);
     if (tiles > kAttnMaxTiles) return 0;
-    const size_t slots = 2 * (size_t)attn_extra(tiles) * q_heads;
+    const size_t slots = 2 * (size_t)attn_shares(tiles, head_dim) * q_heads;
     return (kAttnCounters * sizeof(uint32_t) + slots * (head_dim + 2) * sizeof(float) + 255) & ~size_t(255);
 }
 
@@ -1221,10 +1278,11 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.shift = page_shift(cache->page_size);
     a.group = q_heads / cache->kv_heads;
     a.head_tiles = (a.group + 15) / 16;
-    const int32_t tiles = attn_tiles(q_heads, cache->kv_heads), most = attn_extra(tiles);
-    // no row is longer than its table or the window, so it has no more parts than that
+    const int32_t tiles = attn_tiles(q_heads, cache->kv_heads), most = attn_shares(tiles, cache->head_dim);
+    // no row is longer than its table or the window, and no share shorter than kAttnMinShare
     const int64_t span = std::min<int64_t>((int64_t)max_blocks * cache->page_size, window > 0 ? window : INT32_MAX);
-    a.extra = (int32_t)std::min<int64_t>(most, (span - 1) / kAttnMinPart * n_rows);
+    const int64_t line = n_rows * ((span + kAttnTile - 1) / kAttnTile + kAttnRowTiles);
+    a.shares = (int32_t)std::min<int64_t>(most, (line + kAttnMinShare - 1) / kAttnMinShare);
     a.scale = scale;
     a.out = out;
     a.q = q;
@@ -1241,9 +1299,7 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.part_o = reinterpret_cast<float *>(a.count + kAttnCounters);
     a.part_ml = a.part_o + slots * cache->head_dim;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t groups = ((int64_t)n_rows + a.extra) * tiles;
-    if (groups > (int64_t)1 << 30) return fail(LORA_E_SHAPE, "launch of %lld workgroups is too large", (long long)groups);
-    const dim3 grid((unsigned)groups);
+    const dim3 grid((unsigned)(a.shares * tiles));
     if (cache->type == LORA_TYPE_BF16) attention_launch<BF16>(a, grid, s);
     else attention_launch<F16>(a, grid, s);
     return launch_status("paged attention");
