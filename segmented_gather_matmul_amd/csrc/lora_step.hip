@@ -398,12 +398,12 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 constexpr int kAttnWaves = 4;        // wavefronts of an attention workgroup
 constexpr int kAttnTile = 32;        // tokens a wavefront takes at a time
 constexpr int kAttnMinShare = 16;    // tiles a workgroup takes at least
-constexpr int kAttnRowTiles = 2;     // what starting and finishing a row costs, in tiles
+constexpr int kAttnRowTiles = 4;     // what starting and finishing a row costs, in tiles
 constexpr int kAttnJoin = 16;        // parts joined at a time
 constexpr int kAttnMaxTiles = 4096;  // key/value heads x 16-head tiles of one launch
 constexpr int kAttnCUs = 256;
 // Wavefronts per SIMD, and so workgroups per CU, that the registers are kept to.
-constexpr int attn_occupancy(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
+constexpr int attn_occupancy(int dp) { return dp <= 64 ? 2 : 1; }
 // Arrival counters: two part slots per workgroup, and at most 4 workgroups per CU or one
 // per head tile.  They lie first in a workspace, at one size for every shape, so calls of
 // different shapes sharing a workspace never put sums where another finds its counters.
@@ -432,9 +432,7 @@ __device__ inline RowSpan row_span(const AttnArgs &a, int32_t i)
 // of them: parts of one or more rows, the same amount of work in every workgroup whatever
 // the lengths.  Row i's tiles lie at [tile0, tile0 + tiles) of that line.
 struct RowWork {
-    int32_t row;
-    int64_t tile0;
-    int32_t tiles;
+    int32_t row, tile0, tiles;
     RowSpan rs;
 };
 
@@ -443,66 +441,51 @@ __device__ inline int32_t row_tiles(const RowSpan &rs)
     return rs.span < 0 ? 0 : rs.span <= kAttnTile ? 1 : (rs.span - 1) / kAttnTile + 1;
 }
 
-// The same value in every lane, for the scalar registers.
-__device__ inline int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline int64_t uniform(int64_t v)
+// Inclusive prefix sum over the wavefront: within rows of sixteen lanes, then across them.
+__device__ inline int32_t wave_scan(int32_t v)
 {
-    return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32 | (uint32_t)uniform((int32_t)v));
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+    return v;
 }
 
-// The first row with work at or behind position w * share (row n_rows: none), and the share.
-template <int THREADS>
-__device__ inline RowWork first_row(const AttnArgs &a, int32_t w, int64_t &share)
+// The first row with work at or behind position w * share (row n_rows: none), and the
+// share.  Every wavefront finds it for itself, 64 rows at a time, so nothing waits on a
+// barrier; the host has checked that the line fits 32 bits.
+__device__ inline RowWork first_row(const AttnArgs &a, int32_t w, int32_t &share)
 {
-    __shared__ int64_t totals[THREADS / 64];
-    __shared__ RowWork found;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    RowSpan rs = row_span(a, tid);
-    int64_t total = 0;
-    for (int32_t i = tid; i < a.n_rows; i += THREADS) {
-        const int32_t t = row_tiles(i == tid ? rs : row_span(a, i));
+    const int lane = threadIdx.x & 63;
+    const RowSpan none{0, 0, -1};
+    RowSpan rs = row_span(a, lane);
+    int32_t tiles = row_tiles(rs), total = tiles > 0 ? tiles + kAttnRowTiles : 0;
+    for (int32_t i = lane + 64; i < a.n_rows; i += 64) {
+        const int32_t t = row_tiles(row_span(a, i));
         total += t > 0 ? t + kAttnRowTiles : 0;
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-    if (lane == 0) totals[wave] = total;
-    if (tid == 0) found.row = a.n_rows;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int v = 0; v < THREADS / 64; ++v) total += totals[v];
-    share = (total + a.shares - 1) / a.shares;
-    if (share < kAttnMinShare) share = kAttnMinShare;
-    const int64_t begin = w * share;
-    int64_t at0 = 0;
-    for (int32_t c = 0; c < a.n_rows && begin < total; c += THREADS) {
-        if (c > 0) rs = row_span(a, c + tid);
-        const int32_t tiles = row_tiles(rs), cost = tiles > 0 ? tiles + kAttnRowTiles : 0;
-        int64_t at = cost;  // inclusive prefix over the wavefront, then the workgroup
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int64_t up = __shfl_up(at, d);
-            if (lane >= d) at += up;
+    total = __builtin_amdgcn_readlane(wave_scan(total), 63);
+    share = max((total + a.shares - 1) / a.shares, kAttnMinShare);
+    const int64_t begin = (int64_t)w * share;
+    int32_t at0 = 0;
+    for (int32_t c = 0; c < a.n_rows && begin < total; c += 64) {
+        if (c > 0) {
+            rs = row_span(a, c + lane);
+            tiles = row_tiles(rs);
         }
-        __syncthreads();
-        if (lane == 63) totals[wave] = at;
-        __syncthreads();
-        int64_t before = at0, all = at0;
-#pragma unroll
-        for (int v = 0; v < THREADS / 64; ++v) {
-            before += v < wave ? totals[v] : 0;
-            all += totals[v];
+        const int32_t cost = tiles > 0 ? tiles + kAttnRowTiles : 0, end = at0 + wave_scan(cost);
+        const uint64_t here = __ballot(end - cost <= begin && begin < end);
+        if (here) {
+            const int l = __builtin_ctzll(here);
+            return RowWork{c + l, __builtin_amdgcn_readlane(end - tiles, l), __builtin_amdgcn_readlane(tiles, l),
+                           RowSpan{__builtin_amdgcn_readlane(rs.req, l), __builtin_amdgcn_readlane(rs.first, l),
+                                   __builtin_amdgcn_readlane(rs.span, l)}};
         }
-        at += before - cost;  // this row's first position
-        if (cost > 0 && at <= begin && begin < at + cost) found = RowWork{c + tid, at + kAttnRowTiles, tiles, rs};
-        at0 = all;
-        if (begin < at0) break;
+        at0 = __builtin_amdgcn_readlane(end, 63);
     }
-    __syncthreads();
-    share = uniform(share);
-    const RowWork r = found;
-    return RowWork{uniform(r.row), uniform(r.tile0), uniform(r.tiles),
-                   RowSpan{uniform(r.rs.req), uniform(r.rs.first), uniform(r.rs.span)}};
+    return RowWork{a.n_rows, 0, 0, none};
 }
 
 __device__ inline f4_t mfma(const vec8<F16> &x, const vec8<F16> &y, const f4_t &c)
@@ -716,9 +699,10 @@ lora_paged_attention_kernel(AttnArgs a)
     const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
     const int32_t in_page = (1 << a.shift) - 1;
-    int64_t share;
-    RowWork rw = first_row<64 * kAttnWaves>(a, wg, share);
-    const int64_t line0 = wg * share, line1 = line0 + share;
+    int32_t share;
+    RowWork rw = first_row(a, wg, share);
+    if (rw.row >= a.n_rows) return;
+    const int32_t line0 = wg * share, line1 = (int32_t)min((int64_t)line0 + share, (int64_t)INT32_MAX);
 
     // A row's part in this share: tokens [begin, end); the row has `parts` parts from workgroup w0 on.
     struct Part {
@@ -727,13 +711,13 @@ lora_paged_attention_kernel(AttnArgs a)
     };
     auto next_part = [&]() {
         while (rw.row < a.n_rows) {
-            const int64_t row_end = rw.tile0 + rw.tiles;
-            const int64_t from = max(rw.tile0, line0), to = min(row_end, line1), tile0 = rw.tile0;
-            const Part p{rw.row, rw.rs.first + (int32_t)(from - tile0) * kAttnTile,
-                         rw.rs.first + (int32_t)min((to - tile0) * kAttnTile, (int64_t)rw.rs.span),
-                         tile0 < line0 ? (int32_t)(tile0 / share) : wg, 1, a.table + (int64_t)rw.rs.req * a.ld_table};
+            const int32_t row_end = rw.tile0 + rw.tiles;
+            const int32_t from = max(rw.tile0, line0), to = min(row_end, line1), tile0 = rw.tile0;
+            const Part p{rw.row, rw.rs.first + (from - tile0) * kAttnTile,
+                         rw.rs.first + (int32_t)min((int64_t)(to - tile0) * kAttnTile, (int64_t)rw.rs.span),
+                         tile0 < line0 ? tile0 / share : wg, 1, a.table + (int64_t)rw.rs.req * a.ld_table};
             int32_t last = wg;
-            if (row_end > line1) last = (int32_t)((row_end - 1) / share);
+            if (row_end > line1) last = (row_end - 1) / share;
             do {
                 rw.rs = row_span(a, ++rw.row);
                 rw.tiles = row_tiles(rw.rs);
@@ -1282,6 +1266,8 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     // no row is longer than its table or the window, and no share shorter than kAttnMinShare
     const int64_t span = std::min<int64_t>((int64_t)max_blocks * cache->page_size, window > 0 ? window : INT32_MAX);
     const int64_t line = n_rows * ((span + kAttnTile - 1) / kAttnTile + kAttnRowTiles);
+    if (line > INT32_MAX)
+        return fail(LORA_E_UNSUPPORTED, "%d rows of up to %lld tokens", n_rows, (long long)span);
     a.shares = (int32_t)std::min<int64_t>(most, (line + kAttnMinShare - 1) / kAttnMinShare);
     a.scale = scale;
     a.out = out;
