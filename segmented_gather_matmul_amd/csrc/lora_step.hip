@@ -58,17 +58,18 @@ struct PlanArgs {
     lora_kv_pages pg;
     lora_kv_plan_out out;
     const int32_t *kv_len, *new_len, *req_slot;
-    int32_t shift;    // log2(page_size)
-    int32_t maps;     // the first kernel writes the token maps too
+    int32_t shift;     // log2(page_size)
+    int32_t map_here;  // workgroup 0 writes the token maps (else further workgroups, or a second launch)
 };
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanMapsHere = 4096;  // token rows up to which the planning workgroup writes the maps itself
+constexpr int kPlanThreads = 1024;   // requests planned at a time
+constexpr int kPlanMapsHere = 4096;  // token rows up to which a launch of one workgroup writes the maps itself
 
 // One request of a plan; `bad` holds its LORA_KV_* bits.
 struct PlanReq {
-    int32_t len, add, had, grown, given, bad;
+    int32_t len, had;
+    uint32_t add, grown, given;
+    int32_t bad;
     int64_t end;
 };
 
@@ -91,33 +92,70 @@ __device__ inline PlanReq plan_req(const PlanArgs &a, int r)
         q.given = q.had;
     } else {
         q.end = end;
-        q.grown = (int32_t)(((end + mask) >> a.shift) - q.had);
+        q.grown = (uint32_t)(((end + mask) >> a.shift) - q.had);
     }
     return q;
 }
 
-// Exclusive prefix of v over the workgroup, and the total, in 32 bits.
-__device__ inline int32_t block_scan(int32_t v, int32_t *wave_sums, int32_t &total)
+// Inclusive prefix sum over the wavefront that stops at 2^32 - 1 (sums of that kind are
+// associative, and one that large fits no list and no batch): within rows of sixteen
+// lanes, then across them.
+__device__ inline uint32_t wave_scan_sat(uint32_t v)
+{
+#define LORA_SCAN_STEP(ctrl, rows) \
+    v = __builtin_elementwise_add_sat(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
+    LORA_SCAN_STEP(0x111, 0xf);  // row_shr:1, 2, 4, 8
+    LORA_SCAN_STEP(0x112, 0xf);
+    LORA_SCAN_STEP(0x114, 0xf);
+    LORA_SCAN_STEP(0x118, 0xf);
+    LORA_SCAN_STEP(0x142, 0xa);  // row_bcast:15 into rows 1 and 3
+    LORA_SCAN_STEP(0x143, 0xc);  // row_bcast:31 into rows 2 and 3
+#undef LORA_SCAN_STEP
+    return v;
+}
+
+// Prefix sums of a chunk of requests and their totals: pages given back, pages taken, tokens.
+struct PlanSums {
+    uint32_t given, grown, add;        // before this thread's request
+    uint32_t all_given, all_grown, all_add;
+    int32_t bad;
+};
+
+template <int THREADS>
+__device__ inline PlanSums plan_scan(const PlanReq &q, uint4 *wave_sums)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int32_t s = v;
+    const uint32_t g = wave_scan_sat(q.given), t = wave_scan_sat(q.grown), n = wave_scan_sat(q.add);
+    int32_t bad = 0;
+    for (int b = 1; b <= LORA_KV_INVALID; b *= 2) bad |= __any(q.bad & b) ? b : 0;
+    PlanSums s{0, 0, 0, 0, 0, 0, 0};
+    if (THREADS == 64) {
+        s.all_given = __builtin_amdgcn_readlane(g, 63);
+        s.all_grown = __builtin_amdgcn_readlane(t, 63);
+        s.all_add = __builtin_amdgcn_readlane(n, 63);
+        s.bad = bad;
+    } else {
+        __syncthreads();  // wave_sums may still be read from the call before
+        if (lane == 63) wave_sums[wave] = make_uint4(g, t, n, (uint32_t)bad);
+        __syncthreads();
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int32_t up = __shfl_up(s, d);
-        if (lane >= d) s += up;
+        for (int w = 0; w < THREADS / 64; ++w) {
+            const uint4 x = wave_sums[w];
+            if (w == wave) {
+                s.given = s.all_given;
+                s.grown = s.all_grown;
+                s.add = s.all_add;
+            }
+            s.all_given = __builtin_elementwise_add_sat(s.all_given, x.x);
+            s.all_grown = __builtin_elementwise_add_sat(s.all_grown, x.y);
+            s.all_add = __builtin_elementwise_add_sat(s.all_add, x.z);
+            s.bad |= (int32_t)x.w;
+        }
     }
-    __syncthreads();  // wave_sums may still be read from the call before
-    if (lane == 63) wave_sums[wave] = s;
-    __syncthreads();
-    int32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) {
-        const int32_t x = wave_sums[w];
-        before += w < wave ? x : 0;
-        all += x;
-    }
-    total = all;
-    return before + s - v;
+    s.given += g - q.given;
+    s.grown += t - q.grown;
+    s.add += n - q.add;
+    return s;
 }
 
 // Last index i in [0, n) with off[i] <= k (off[0] <= k, off non-decreasing).
@@ -142,115 +180,140 @@ __device__ inline void plan_map_row(const PlanArgs &a, int32_t t, int32_t r, int
     if (o.idx) o.idx[t] = r < 0 || !a.req_slot ? -1 : a.req_slot[r];
 }
 
-// The plan proper, in one workgroup: totals and checks over all requests first (all or
-// nothing), then, 1024 requests at a time, the pages of ended requests onto the free
-// list, and after all of those the pages of growing ones off it.  A chunk's work is spread over
-// the workgroup by page and by token, each found by a binary search in the chunk's
-// prefix sums.
-__global__ __launch_bounds__(kPlanThreads) void lora_kv_plan_kernel(PlanArgs a)
+// The plan, by one workgroup: prefix sums and checks over all requests first (all or
+// nothing), then, THREADS requests at a time, the pages of ended requests onto the free
+// list, and after all of those the pages of growing ones off it.  A chunk's work is spread
+// over the workgroup by page and by token, each found by a binary search in the chunk's
+// prefix sums.  Bound by the latency of its chain of loads (lengths, then ids), so small
+// batches run in one wavefront, where no barrier waits.
+//
+// Where a step has many token rows and one chunk holds all requests, workgroups 1, 2, ...
+// make the same sums for themselves and write the maps of THREADS rows each.  They read
+// only what workgroup 0 does not write: table entries that were there before, and the free
+// list below its old end (a page that an ended request gives back in this step is read
+// from that request's table row).  That needs kv_end and the free top to be other arrays
+// than the ones read.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void lora_kv_plan_kernel(PlanArgs a)
 {
-    __shared__ int32_t wave_sums[kPlanWaves];
-    __shared__ int64_t sums[kPlanWaves][3];
-    __shared__ int32_t bits;
-    __shared__ int32_t off[kPlanThreads], had_s[kPlanThreads], off_tok[kPlanThreads], len_s[kPlanThreads];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ uint4 wave_sums[THREADS / 64];
+    __shared__ int32_t off[THREADS], off_given[THREADS], off_tok[THREADS], had_s[THREADS], len_s[THREADS];
+    const int tid = threadIdx.x;
     const int32_t n = a.pg.n_req;
-    if (tid == 0) bits = 0;
-    __syncthreads();
-    // totals
-    int64_t tokens = 0, taken = 0, given = 0;
-    int32_t bad = 0;
-    for (int32_t r = tid; r < n; r += kPlanThreads) {
-        const PlanReq q = plan_req(a, r);
-        bad |= q.bad;
-        tokens += q.add;
-        taken += q.grown;
-        given += q.given;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        tokens += __shfl_xor(tokens, d);
-        taken += __shfl_xor(taken, d);
-        given += __shfl_xor(given, d);
-        bad |= __shfl_xor(bad, d);
-    }
-    if (lane == 0) {
-        sums[wave][0] = tokens;
-        sums[wave][1] = taken;
-        sums[wave][2] = given;
-        if (bad) atomicOr(&bits, bad);
-    }
+    const bool one = n <= THREADS;  // one chunk holds all requests
     const int32_t top0 = *a.pg.free_top;
-    __syncthreads();
-    tokens = taken = given = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) {
-        tokens += sums[w][0];
-        taken += sums[w][1];
-        given += sums[w][2];
+    PlanReq q = plan_req(a, tid);
+    PlanSums s = plan_scan<THREADS>(q, wave_sums);
+    if (!one) {
+        PlanReq sum = q;
+        for (int32_t r = tid + THREADS; r < n; r += THREADS) {
+            const PlanReq x = plan_req(a, r);
+            sum.bad |= x.bad;
+            sum.given = __builtin_elementwise_add_sat(sum.given, x.given);
+            sum.grown = __builtin_elementwise_add_sat(sum.grown, x.grown);
+            sum.add = __builtin_elementwise_add_sat(sum.add, x.add);
+        }
+        const PlanSums all = plan_scan<THREADS>(sum, wave_sums);
+        s.all_given = all.all_given;
+        s.all_grown = all.all_grown;
+        s.all_add = all.all_add;
+        s.bad = all.bad;
     }
-    bad = bits;
+    const int64_t given = s.all_given, taken = s.all_grown, tokens = s.all_add;
+    int32_t bad = s.bad;
     if (top0 < 0 || top0 > a.pg.num_pages || top0 + given > a.pg.num_pages) bad |= LORA_KV_INVALID;
     if (taken > top0 + given) bad |= LORA_KV_NO_PAGES;
     if (tokens > a.out.max_tokens) bad |= LORA_KV_TOO_MANY;
+    const int32_t top = (int32_t)(top0 + given);
+
+    if (blockIdx.x > 0) {  // the maps of THREADS rows
+        const int32_t t = (blockIdx.x - 1) * THREADS + tid;
+        off[tid] = (int32_t)s.grown;
+        off_given[tid] = (int32_t)s.given;
+        off_tok[tid] = (int32_t)s.add;
+        had_s[tid] = q.had;
+        len_s[tid] = q.len;
+        __syncthreads();
+        if (t >= a.out.max_tokens) return;
+        if (bad || t >= tokens) {
+            plan_map_row(a, t, -1, -1, 0);
+            return;
+        }
+        const int r = last_at_most(off_tok, THREADS, t);
+        const int32_t pos = len_s[r] + (t - off_tok[r]), b = pos >> a.shift;
+        int32_t page;
+        if (b < had_s[r]) {
+            page = a.pg.block_table[(int64_t)r * a.pg.ld_table + b];
+        } else {
+            const int32_t k = top - 1 - (off[r] + b - had_s[r]);
+            if (k < top0) {
+                page = a.pg.free_pages[k];
+            } else {
+                const int e = last_at_most(off_given, THREADS, k - top0);
+                page = a.pg.block_table[(int64_t)e * a.pg.ld_table + (k - top0 - off_given[e])];
+            }
+        }
+        plan_map_row(a, t, r, pos, page);
+        return;
+    }
+
     if (tid == 0) {
-        const int64_t most = INT32_MAX;
         a.out.status[0] = bad;
-        a.out.status[1] = (int32_t)(tokens < most ? tokens : most);
-        a.out.status[2] = (int32_t)(taken < most ? taken : most);
-        a.out.status[3] = (int32_t)(given < most ? given : most);
-        a.out.free_top[0] = bad ? top0 : (int32_t)(top0 + given - taken);
+        a.out.status[1] = (int32_t)min(tokens, (int64_t)INT32_MAX);
+        a.out.status[2] = (int32_t)min(taken, (int64_t)INT32_MAX);
+        a.out.status[3] = (int32_t)min(given, (int64_t)INT32_MAX);
+        a.out.free_top[0] = bad ? top0 : (int32_t)(top - taken);
         a.out.q_ptr[n] = bad ? 0 : (int32_t)tokens;
     }
     if (bad) {
-        for (int32_t r = tid; r < n; r += kPlanThreads) {
+        for (int32_t r = tid; r < n; r += THREADS) {
             a.out.kv_end[r] = a.kv_len[r];
             a.out.q_ptr[r] = 0;
         }
-        if (a.maps)
-            for (int32_t t = tid; t < a.out.max_tokens; t += kPlanThreads) plan_map_row(a, t, -1, -1, 0);
+        if (a.map_here)
+            for (int32_t t = tid; t < a.out.max_tokens; t += THREADS) plan_map_row(a, t, -1, -1, 0);
         return;
     }
     // pages of ended requests go on top of the free list
     if (given > 0) {
         int32_t at = top0;
-        for (int32_t c = 0; c < n; c += kPlanThreads) {
-            const PlanReq q = plan_req(a, c + tid);
-            int32_t total;
-            const int32_t before = block_scan(q.given, wave_sums, total);
-            off[tid] = before;
+        for (int32_t c = 0; c < n; c += THREADS) {
+            const PlanSums x = one ? s : plan_scan<THREADS>(plan_req(a, c + tid), wave_sums);
+            off_given[tid] = (int32_t)x.given;
             __syncthreads();
-            for (int32_t k = tid; k < total; k += kPlanThreads) {
-                const int i = last_at_most(off, kPlanThreads, k);
-                a.pg.free_pages[at + k] = a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + (k - off[i])];
+            const int32_t here = (int32_t)x.all_given;
+            for (int32_t k = tid; k < here; k += THREADS) {
+                const int i = last_at_most(off_given, THREADS, k);
+                a.pg.free_pages[at + k] = a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + (k - off_given[i])];
             }
-            at += total;
+            at += here;
+            __syncthreads();  // off_given, and below the list, are read by other threads
         }
-        __syncthreads();  // the list is read below by other threads of this workgroup
     }
     // growing requests and the token maps
-    int32_t at = (int32_t)(top0 + given) - 1, row0 = 0;
-    for (int32_t c = 0; c < n; c += kPlanThreads) {
-        const PlanReq q = plan_req(a, c + tid);
-        int32_t pages, rows;
-        const int32_t before = block_scan(q.grown, wave_sums, pages);
-        const int32_t before_tok = block_scan(q.add, wave_sums, rows);
-        off[tid] = before;
+    int32_t at = top - 1, row0 = 0;
+    for (int32_t c = 0; c < n; c += THREADS) {
+        if (!one) {
+            q = plan_req(a, c + tid);
+            s = plan_scan<THREADS>(q, wave_sums);
+        }
+        const int32_t pages = (int32_t)s.all_grown, rows = (int32_t)s.all_add;
+        off[tid] = (int32_t)s.grown;
         had_s[tid] = q.had;
-        off_tok[tid] = before_tok;
+        off_tok[tid] = (int32_t)s.add;
         len_s[tid] = q.len;
         if (c + tid < n) {
-            a.out.q_ptr[c + tid] = row0 + before_tok;
+            a.out.q_ptr[c + tid] = row0 + (int32_t)s.add;
             a.out.kv_end[c + tid] = (int32_t)q.end;
         }
         __syncthreads();
-        for (int32_t k = tid; k < pages; k += kPlanThreads) {
-            const int i = last_at_most(off, kPlanThreads, k);
+        for (int32_t k = tid; k < pages; k += THREADS) {
+            const int i = last_at_most(off, THREADS, k);
             a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + had_s[i] + (k - off[i])] = a.pg.free_pages[at - k];
         }
-        if (a.maps) {
-            for (int32_t k = tid; k < rows; k += kPlanThreads) {
-                const int i = last_at_most(off_tok, kPlanThreads, k);
+        if (a.map_here) {
+            for (int32_t k = tid; k < rows; k += THREADS) {
+                const int i = last_at_most(off_tok, THREADS, k);
                 const int32_t pos = len_s[i] + (k - off_tok[i]), b = pos >> a.shift;
                 const int32_t page = b < had_s[i] ? a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + b]
                                                   : a.pg.free_pages[at - (off[i] + b - had_s[i])];
@@ -261,12 +324,12 @@ __global__ __launch_bounds__(kPlanThreads) void lora_kv_plan_kernel(PlanArgs a)
         row0 += rows;
         __syncthreads();
     }
-    if (a.maps)
-        for (int32_t t = row0 + tid; t < a.out.max_tokens; t += kPlanThreads) plan_map_row(a, t, -1, -1, 0);
+    if (a.map_here)
+        for (int32_t t = row0 + tid; t < a.out.max_tokens; t += THREADS) plan_map_row(a, t, -1, -1, 0);
 }
 
-// Token maps of a step with many rows, one row per thread, from what the plan left: q_ptr
-// (searched), kv_end and the table.
+// Token maps of a step with many rows where the plan works in place or in several chunks:
+// one row per thread, from what the plan left: q_ptr (searched), kv_end and the table.
 __global__ __launch_bounds__(256) void lora_kv_maps_kernel(PlanArgs a)
 {
     const int32_t t = blockIdx.x * 256 + threadIdx.x;
@@ -1113,7 +1176,7 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
 {
     clear_error();
     if (!pages || !out) return fail(LORA_E_NULL, "pages and out are required");
-    PlanArgs a{*pages, *out, kv_len, new_len, req_slot, 0, 0};
+    PlanArgs a{*pages, *out, kv_len, new_len, req_slot, 0, 1};
     a.shift = page_shift(pages->page_size);
     if (a.shift < 0)
         return fail(LORA_E_SHAPE, "page_size = %d is not a power of two in 1..%d", pages->page_size, LORA_KV_MAX_PAGE);
@@ -1131,9 +1194,20 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     if (out->max_tokens > 0 && (!out->tok_req || !out->tok_pos || !out->slots))
         return fail(LORA_E_NULL, "tok_req, tok_pos and slots are required");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    a.maps = out->max_tokens <= kPlanMapsHere;
-    launch_args(lora_kv_plan_kernel, dim3(1), kPlanThreads, 0, s, a);
-    if (!a.maps) launch_args(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
+    // One workgroup up to kPlanMapsHere token rows; beyond that further workgroups for the
+    // maps, or a second launch where the plan works in place or in several chunks.
+    const bool in_place = out->kv_end == kv_len || out->free_top == pages->free_top;
+    a.map_here = out->max_tokens <= kPlanMapsHere;
+    if (!a.map_here && !in_place && pages->n_req <= kPlanThreads) {
+        const unsigned more = (unsigned)((out->max_tokens + (int64_t)kPlanThreads - 1) / kPlanThreads);
+        launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(1 + more), kPlanThreads, 0, s, a);
+        return launch_status("step plan");
+    }
+    if (a.map_here && pages->n_req <= 64 && out->max_tokens <= 256)
+        launch_args(lora_kv_plan_kernel<64>, dim3(1), 64, 0, s, a);
+    else
+        launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, s, a);
+    if (!a.map_here) launch_args(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
     return launch_status("step plan");
 }
 
