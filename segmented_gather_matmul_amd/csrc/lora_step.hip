@@ -53,6 +53,30 @@ __device__ inline void store16(void *base, int64_t elem, const uint4 &v)
     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + elem) = v;
 }
 
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+// Streaming forms, for what is read or written once and is larger than the caches.
+__device__ inline uint4 load16_stream(const void *base, int64_t elem)
+{
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(
+                                         reinterpret_cast<const u4_t *>(static_cast<const uint16_t *>(base) + elem)));
+}
+template <bool STREAM>
+__device__ inline void store16(void *base, int64_t elem, const uint4 &v)
+{
+    if (STREAM)
+        __builtin_nontemporal_store(__builtin_bit_cast(u4_t, v),
+                                    reinterpret_cast<u4_t *>(static_cast<uint16_t *>(base) + elem));
+    else store16(base, elem, v);
+}
+
+// Outputs of a call larger than this, the L2s of all XCDs together, are written with
+// streaming stores: lines that the next call cannot find there anyway no longer displace
+// what is being read.  Measured: rotary append of 4001 rows in the 70B layout (82 MB
+// written) 41.7 -> 27.2 us, of 12,907 rows in the 7B layout (317 MB) 122 -> 114; residual
+// norm of 12,907 rows of 4096 (211 MB) 74.7 -> 71.2.  Smaller outputs stay in the L2s for
+// the call that reads them.
+constexpr int64_t kStreamBytes = 32 << 20;
+
 // ------------------------------------------------------------------------ step plan
 struct PlanArgs {
     lora_kv_pages pg;
@@ -357,6 +381,8 @@ struct AppendArgs {
     int32_t shift;
 };
 
+constexpr int32_t kAppendFill = 1024;  // rows that fill the CUs with one workgroup each
+
 // cos and sin of position * inv_freq: the product is exact in 64 bits (31 + 24 bits), so
 // reducing it to turns in 64 bits leaves the angle right to 2^-22 turns or better at any
 // 32-bit position.
@@ -370,10 +396,13 @@ __device__ inline float2 turn_of(int32_t pos, float inv_freq)
     return cs;
 }
 
-// One workgroup per token row: the row's cos and sin go to LDS once, and every thread then
-// moves 16-byte chunks; a chunk pair (x[i..], x[i + rot/2..]) or, interleaved, one chunk
-// holds whole rotation pairs.
-template <typename T, bool INTER>
+// Workgroups of 256 threads: blockIdx.x is the token row, and the row's units go round over
+// the threads of its gridDim.y workgroups.  A unit moves one 16-byte chunk, or the two
+// chunks x[i..], x[i + rot/2..] whose elements turn together (interleaved, one chunk holds
+// whole pairs).  A thread asks for its first chunks first; while they are on their way, the
+// row's cos and sin are worked out, once, into LDS.  Bound by reading q, k, v and writing
+// q_out and the cells.
+template <typename T, bool INTER, bool STREAM>
 __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
 {
     __shared__ float2 cs[LORA_KV_MAX_HEAD_DIM / 2];
@@ -382,62 +411,75 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
     const int32_t slot = a.slots[t];
     if (slot < 0 || slot >= (int64_t)a.c.num_pages << a.shift) return;
     const int half = a.rot / 2;
+    const int64_t cell = (int64_t)(slot >> a.shift) * a.c.page_stride +
+                         (int64_t)(slot & ((1 << a.shift) - 1)) * a.c.token_stride;
+    const int n_qk = (a.q_heads + a.kv_heads) * a.units_rot;
+    const int n_all = n_qk + a.kv_heads * a.units_v;
+    // a unit's addresses; turn: first of its frequencies, -1: its chunk passes through
+    struct Unit {
+        const void *src;
+        void *dst;
+        int64_t from, to;
+        int turn;
+    };
+    auto unit_of = [&](int u) {
+        if (u >= n_qk) {
+            const int h = (u - n_qk) / a.units_v, c = (u - n_qk) - h * a.units_v;
+            return Unit{a.v, a.c.v, t * a.ldv + (int64_t)h * a.head_dim + 8 * c, cell + h * a.c.head_stride + 8 * c, -1};
+        }
+        int h = u / a.units_rot;
+        int d = 8 * (u - h * a.units_rot), turn = -1;
+        const bool is_q = h < a.q_heads;
+        if (INTER) turn = d < a.rot ? d / 2 : -1;
+        else if (d < half) turn = d;
+        else d += half;  // the chunks behind the pairs
+        if (!is_q) h -= a.q_heads;
+        return Unit{is_q ? a.q : a.k, is_q ? a.q_out : a.c.k, t * (is_q ? a.ldq : a.ldk) + (int64_t)h * a.head_dim + d,
+                    is_q ? t * a.ldqo + (int64_t)h * a.head_dim + d : cell + h * a.c.head_stride + d, turn};
+    };
+    int u = blockIdx.y * 256 + tid;
+    Unit un{};
+    uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+    auto fetch = [&]() {
+        un = unit_of(u);
+        ra = load16(un.src, un.from);
+        if (!INTER && un.turn >= 0) rb = load16(un.src, un.from + half);
+    };
+    if (u < n_all) fetch();
     for (int i = tid; i < half; i += 256) {
         const int ax = a.axis ? a.axis[i] : 0;
         cs[i] = ax >= 0 && ax < a.n_axes ? turn_of(a.pos[ax * a.ld_pos + t], a.inv_freq[i]) : make_float2(1.f, 0.f);
     }
     __syncthreads();
-    const int64_t cell = (int64_t)(slot >> a.shift) * a.c.page_stride +
-                         (int64_t)(slot & ((1 << a.shift) - 1)) * a.c.token_stride;
-    const int n_qk = (a.q_heads + a.kv_heads) * a.units_rot;
-    const int n_all = n_qk + a.kv_heads * a.units_v;
-    for (int u = tid; u < n_all; u += 256) {
-        if (u >= n_qk) {
-            const int h = (u - n_qk) / a.units_v, c = (u - n_qk) - h * a.units_v;
-            store16(a.c.v, cell + h * a.c.head_stride + 8 * c, load16(a.v, t * a.ldv + h * a.head_dim + 8 * c));
-            continue;
-        }
-        int h = u / a.units_rot;
-        const int p = u - h * a.units_rot;
-        const bool is_q = h < a.q_heads;
-        if (!is_q) h -= a.q_heads;
-        const void *src = is_q ? a.q : a.k;
-        void *dst = is_q ? a.q_out : a.c.k;
-        const int64_t from = t * (is_q ? a.ldq : a.ldk) + (int64_t)h * a.head_dim;
-        const int64_t to = is_q ? t * a.ldqo + (int64_t)h * a.head_dim : cell + h * a.c.head_stride;
-        float x[8], y[8];
-        if (INTER) {
-            const uint4 raw = load16(src, from + 8 * p);
-            if (8 * p >= a.rot) {
-                store16(dst, to + 8 * p, raw);
-                continue;
-            }
-            unpack8<T>(raw, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 w = cs[4 * p + e];
-                y[2 * e] = __builtin_fmaf(x[2 * e], w.x, -(x[2 * e + 1] * w.y));
-                y[2 * e + 1] = __builtin_fmaf(x[2 * e], w.y, x[2 * e + 1] * w.x);
-            }
-            store16(dst, to + 8 * p, pack8<T>(y));
+    while (u < n_all) {
+        if (un.turn < 0) {
+            store16<STREAM>(un.dst, un.to, ra);
         } else {
-            if (8 * p >= half) {  // a chunk that passes through
-                const int c = half + 8 * p;
-                store16(dst, to + c, load16(src, from + c));
-                continue;
-            }
-            float b[8], z[8];
-            unpack8<T>(load16(src, from + 8 * p), x);
-            unpack8<T>(load16(src, from + half + 8 * p), b);
+            float x[8], y[8];
+            unpack8<T>(ra, x);
+            if (INTER) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 w = cs[8 * p + e];
-                y[e] = __builtin_fmaf(x[e], w.x, -(b[e] * w.y));
-                z[e] = __builtin_fmaf(x[e], w.y, b[e] * w.x);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 w = cs[un.turn + e];
+                    y[2 * e] = __builtin_fmaf(x[2 * e], w.x, -(x[2 * e + 1] * w.y));
+                    y[2 * e + 1] = __builtin_fmaf(x[2 * e], w.y, x[2 * e + 1] * w.x);
+                }
+                store16<STREAM>(un.dst, un.to, pack8<T>(y));
+            } else {
+                float b[8], z[8];
+                unpack8<T>(rb, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 w = cs[un.turn + e];
+                    y[e] = __builtin_fmaf(x[e], w.x, -(b[e] * w.y));
+                    z[e] = __builtin_fmaf(x[e], w.y, b[e] * w.x);
+                }
+                store16<STREAM>(un.dst, un.to, pack8<T>(y));
+                store16<STREAM>(un.dst, un.to + half, pack8<T>(z));
             }
-            store16(dst, to + 8 * p, pack8<T>(y));
-            store16(dst, to + half + 8 * p, pack8<T>(z));
         }
+        u += 256 * gridDim.y;
+        if (u < n_all) fetch();
     }
 }
 
@@ -1030,8 +1072,9 @@ __device__ inline float block_sum(float v, float *wave_sums)
 
 // One workgroup per row; a thread keeps its NC chunks of eight elements in registers from
 // the loads to the stores, so x and res are read once and res_out and y written once.
-template <typename T, int NC>
-__global__ __launch_bounds__(1024) void lora_residual_norm_kernel(lora_norm_args a)
+template <typename T, int NC, bool STREAM>
+__global__ __launch_bounds__(1024) void
+lora_residual_norm_kernel(lora_norm_args a)
 {
     __shared__ float wave_sums[16];
     const int tid = threadIdx.x, nt = blockDim.x;
@@ -1042,16 +1085,24 @@ __global__ __launch_bounds__(1024) void lora_residual_norm_kernel(lora_norm_args
         gi = a.gate_idx ? a.gate_idx[row] : 0;
         if (gi < -1 || gi >= a.n_gates) return;
     }
+    // everything is asked for before anything waits
+    const uint4 zero4 = make_uint4(0, 0, 0, 0);
+    uint4 res[NC], x[NC], pw[NC], gate[NC], w[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = tid + i * nt;
+        const bool in = c < chunks;
+        res[i] = in ? load16(a.res, row * a.ldr + 8 * c) : zero4;
+        x[i] = a.x && in ? load16(a.x, row * a.ldx + 8 * c) : zero4;
+        pw[i] = a.post_w && in ? load16(a.post_w, 8 * c) : zero4;
+        gate[i] = gi >= 0 && in ? load16(a.gate, gi * a.ldg + 8 * c) : zero4;
+        w[i] = a.y && in ? load16(a.w, 8 * c) : zero4;
+    }
     float h[NC][8], p[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = p[i][e] = 0.f;
-        const int c = tid + i * nt;
-        if (c < chunks) {
-            unpack8<T>(load16(a.res, row * a.ldr + 8 * c), h[i]);
-            if (a.x) unpack8<T>(load16(a.x, row * a.ldx + 8 * c), p[i]);
-        }
+        unpack8<T>(res[i], h[i]);
+        unpack8<T>(x[i], p[i]);
     }
     if (a.post_w) {
         float ss = 0.f;
@@ -1062,12 +1113,10 @@ __global__ __launch_bounds__(1024) void lora_residual_norm_kernel(lora_norm_args
         const float inv = 1.f / __builtin_sqrtf(block_sum(ss, wave_sums) / (float)a.hidden + a.eps);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = tid + i * nt;
-            if (c >= chunks) continue;
-            float w[8];
-            unpack8<T>(load16(a.post_w, 8 * c), w);
+            float f[8];
+            unpack8<T>(pw[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[i][e] = p[i][e] * inv * (w[e] + a.w_offset);
+            for (int e = 0; e < 8; ++e) p[i][e] = p[i][e] * inv * (f[e] + a.w_offset);
         }
     }
     float ss = 0.f;
@@ -1077,14 +1126,14 @@ __global__ __launch_bounds__(1024) void lora_residual_norm_kernel(lora_norm_args
         if (c >= chunks) continue;
         if (gi >= 0) {
             float g[8];
-            unpack8<T>(load16(a.gate, gi * a.ldg + 8 * c), g);
+            unpack8<T>(gate[i], g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[i][e] *= g[e];
         }
         if (a.x)
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = __builtin_fmaf(a.alpha, p[i][e], h[i][e]);
-        if (a.res_out) store16(a.res_out, row * a.ldro + 8 * c, pack8<T>(h[i]));
+        if (a.res_out) store16<STREAM>(a.res_out, row * a.ldro + 8 * c, pack8<T>(h[i]));
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
     }
@@ -1094,11 +1143,11 @@ __global__ __launch_bounds__(1024) void lora_residual_norm_kernel(lora_norm_args
     for (int i = 0; i < NC; ++i) {
         const int c = tid + i * nt;
         if (c >= chunks) continue;
-        float w[8], y[8];
-        unpack8<T>(load16(a.w, 8 * c), w);
+        float f[8], y[8];
+        unpack8<T>(w[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * inv * (w[e] + a.w_offset);
-        store16(a.y, row * a.ldy + 8 * c, pack8<T>(y));
+        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * inv * (f[e] + a.w_offset);
+        store16<STREAM>(a.y, row * a.ldy + 8 * c, pack8<T>(y));
     }
 }
 
@@ -1271,16 +1320,25 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
     a.slots = slots;
     a.c = *cache;
     a.shift = page_shift(cache->page_size);
+    const bool stream_out = 2 * (int64_t)n_rows * ((int64_t)q_heads + 2 * (int64_t)cache->kv_heads) * cache->head_dim > kStreamBytes;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)n_rows);
     const bool bf = cache->type == LORA_TYPE_BF16;
+    const int64_t units = ((int64_t)q_heads + cache->kv_heads) * a.units_rot + (int64_t)cache->kv_heads * a.units_v;
+    // One workgroup per row, unless there are too few rows to fill the CUs: then one per 256
+    // units (32 rows of the 7B shape: 4.4 us against 3.0).
+    const int64_t blocks = n_rows < kAppendFill ? std::min<int64_t>((units + 255) / 256, 64) : 1;
+    const dim3 grid((unsigned)n_rows, (unsigned)blocks);
+#define LORA_APPEND(T, INTER)                                                                      \
+    (stream_out ? launch_args(lora_rope_append_kernel<T, INTER, true>, grid, 256, 0, s, a)         \
+                : launch_args(lora_rope_append_kernel<T, INTER, false>, grid, 256, 0, s, a))
     if (rope->interleaved) {
-        if (bf) launch_args(lora_rope_append_kernel<BF16, true>, grid, 256, 0, s, a);
-        else launch_args(lora_rope_append_kernel<F16, true>, grid, 256, 0, s, a);
+        if (bf) LORA_APPEND(BF16, true);
+        else LORA_APPEND(F16, true);
     } else {
-        if (bf) launch_args(lora_rope_append_kernel<BF16, false>, grid, 256, 0, s, a);
-        else launch_args(lora_rope_append_kernel<F16, false>, grid, 256, 0, s, a);
+        if (bf) LORA_APPEND(BF16, false);
+        else LORA_APPEND(F16, false);
     }
+#undef LORA_APPEND
     return launch_status("rotary append");
 }
 
@@ -1401,19 +1459,25 @@ int lora_residual_norm(void *stream, const lora_norm_args *args)
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int chunks = a.hidden / 8;
+    // One chunk per thread up to 512 threads, then two: a row of 8192 in 1024 threads of one
+    // chunk waits longer at its barriers than it gains (4001 rows with both norms and a
+    // gate: 64 us against 54).
     int threads = 64;
-    while (threads < 1024 && threads < chunks) threads *= 2;
+    while (threads < 1024 && (threads < 512 ? threads : 2 * threads) < chunks) threads *= 2;
     const int nc = (chunks + threads - 1) / threads;
+    const bool stream_out = 2 * (int64_t)a.n_rows * a.hidden * ((a.y ? 1 : 0) + (a.res_out ? 1 : 0)) > kStreamBytes;
     const dim3 grid((unsigned)a.n_rows);
     const bool bf = a.type == LORA_TYPE_BF16;
-#define LORA_NORM(NC)                                                                          \
-    (bf ? launch_args(lora_residual_norm_kernel<BF16, NC>, grid, threads, 0, s, a)             \
-        : launch_args(lora_residual_norm_kernel<F16, NC>, grid, threads, 0, s, a))
+#define LORA_NORM_T(T, NC)                                                                        \
+    (stream_out ? launch_args(lora_residual_norm_kernel<T, NC, true>, grid, threads, 0, s, a)      \
+                : launch_args(lora_residual_norm_kernel<T, NC, false>, grid, threads, 0, s, a))
+#define LORA_NORM(NC) (bf ? LORA_NORM_T(BF16, NC) : LORA_NORM_T(F16, NC))
     if (nc <= 1) LORA_NORM(1);
     else if (nc <= 2) LORA_NORM(2);
     else if (nc <= 4) LORA_NORM(4);
     else LORA_NORM(8);
 #undef LORA_NORM
+#undef LORA_NORM_T
     return launch_status("residual norm");
 }
 

@@ -71,6 +71,16 @@ def _type(t, what):
 
 def _matrix(t, what, dtype, rows, cols):
     """t: 2-D, of `dtype`, unit column stride, >= rows rows and >= cols columns; its row stride."""
+    try:
+        (n, c), (ld, sc) = t.shape, t.stride()
+        if t.dtype is dtype and n >= rows and c >= cols and sc == 1 and ld >= cols and (n > 1 or ld % 8 == 0):
+            return ld
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return _matrix_checked(t, what, dtype, rows, cols)
+
+
+def _matrix_checked(t, what, dtype, rows, cols):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what} must be a tensor (got {type(t).__name__})")
     if t.dtype is not dtype:
@@ -91,30 +101,42 @@ def _matrix(t, what, dtype, rows, cols):
 
 
 def _vector(t, what, dtype, n):
+    """t: contiguous, of `dtype`, at least n elements."""
+    try:
+        if t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what} must be a tensor (got {type(t).__name__})")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must have dtype {_NAMES[dtype]} (got {t.dtype})")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if t.numel() < n:
-        raise ValueError(f"{what} has {t.numel()} elements, needs at least {n}")
+    raise ValueError(f"{what} has {t.numel()} elements, needs at least {n}")
 
 
 def _here(names, *tensors):
     """Every tensor (None: not given) is on the current GPU; its index."""
-    dev = None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{names.split()[i]} must be a GPU tensor (got device {t.device})")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if d != dev:
-            raise ValueError(f"{names.split()[i]} is on {t.device}, the current device is cuda:{dev}")
-    return dev
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            break
+    else:
+        return dev
+    for what, t in zip(names.split(), tensors):
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{what} must be a GPU tensor (got device {t.device})")
+    dev = torch.cuda.current_device()
+    for what, t in zip(names.split(), tensors):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _call(name, *args):
+    code = getattr(B._lib or B.lib(), name)(*args)
+    if code:
+        B._check(code)
 
 
 def _stream(stream, dev):
@@ -273,8 +295,8 @@ def lora_kv_plan(plan: KVPlan, pages: KVPages, kv_len, new_len, req_slot=None, s
         _vector(req_slot, "req_slot", torch.int32, n)
     dev = _here("kv_len new_len req_slot block_table free_pages free_top status kv_end plan.free_top", kv_len, new_len,
                 req_slot, pages.block_table, pages.free_pages, pages.free_top, plan.status, plan.kv_end, plan.free_top)
-    B._check(B.lib().lora_kv_plan(_stream(stream, dev), pages.ref, kv_len.data_ptr(), new_len.data_ptr(),
-                                  _ptr(req_slot), plan.ref))
+    _call("lora_kv_plan", _stream(stream, dev), pages.ref, kv_len.data_ptr(), new_len.data_ptr(),
+                                  _ptr(req_slot), plan.ref)
 
 
 def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = None, positions=None, stream=None):
@@ -307,8 +329,8 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
         ldp = p2.stride(0) if p2.shape[0] > 1 else max(n, 1)
     dev = _here("slots k v q q_out positions cache.k inv_freq axis", slots, k, v, q, q_out, positions, cache.k,
                 rope.inv_freq, rope.axis)
-    B._check(B.lib().lora_rope_append(_stream(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
-                                      v.data_ptr(), ldv, rope.ref, _ptr(positions), ldp, slots.data_ptr(), cache.ref))
+    _call("lora_rope_append", _stream(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
+                                      v.data_ptr(), ldv, rope.ref, _ptr(positions), ldp, slots.data_ptr(), cache.ref)
 
 
 class _NoRope:
@@ -345,10 +367,10 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
         _vector(lse, "lse", torch.float32, n * heads)
     _vector(work, "work", torch.int32, 1)
     dev = _here("q out block_table kv_len req lse work cache.k", q, out, block_table, kv_len, req, lse, work, cache.k)
-    B._check(B.lib().lora_paged_attention(_stream(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
+    _call("lora_paged_attention", _stream(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
                                           cache.ref, n_req, block_table.data_ptr(), ldt, blocks, kv_len.data_ptr(),
                                           _ptr(req), 1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
-                                          _ptr(lse), work.data_ptr(), 4 * work.numel()))
+                                          _ptr(lse), work.data_ptr(), 4 * work.numel())
 
 
 def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=None, gate_idx=None, alpha=1.0, eps=1e-5,
@@ -360,28 +382,28 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
         raise ValueError(f"res must be 2-D (got {res.dim()}-D)")
     n, h = res.shape
     dt = res.dtype
-    a = CNormArgs()
-    a.type, a.n_rows, a.hidden = ty, n, h
-    a.res, a.ldr = res.data_ptr(), _matrix(res, "res", dt, n, h)
+    ldr = _matrix(res, "res", dt, n, h)
+    yp = ldy = wp = rp = ldro = xp = ldx = pp = gp = ldg = ip = None
+    n_gates = 0
     if y is not None:
-        a.y, a.ldy = y.data_ptr(), _matrix(y, "y", dt, n, h)
+        ldy, yp = _matrix(y, "y", dt, n, h), y.data_ptr()
         _vector(w, "w", dt, h)
-        a.w = w.data_ptr()
+        wp = w.data_ptr()
     else:
         w = None
     if res_out is not None:
-        a.res_out, a.ldro = res_out.data_ptr(), _matrix(res_out, "res_out", dt, n, h)
+        ldro, rp = _matrix(res_out, "res_out", dt, n, h), res_out.data_ptr()
     if x is not None:
-        a.x, a.ldx = x.data_ptr(), _matrix(x, "x", dt, n, h)
+        ldx, xp = _matrix(x, "x", dt, n, h), x.data_ptr()
     if post_w is not None:
         _vector(post_w, "post_w", dt, h)
-        a.post_w = post_w.data_ptr()
+        pp = post_w.data_ptr()
     if gate is not None:
-        a.n_gates = gate.shape[0]
-        a.gate, a.ldg = gate.data_ptr(), _matrix(gate, "gate", dt, 1, h)
+        ldg, gp, n_gates = _matrix(gate, "gate", dt, 1, h), gate.data_ptr(), gate.shape[0]
     if gate_idx is not None:
         _vector(gate_idx, "gate_idx", torch.int32, n)
-        a.gate_idx = gate_idx.data_ptr()
-    a.alpha, a.eps, a.w_offset = alpha, eps, w_offset
+        ip = gate_idx.data_ptr()
     dev = _here("res y res_out x w post_w gate gate_idx", res, y, res_out, x, w, post_w, gate, gate_idx)
-    B._check(B.lib().lora_residual_norm(_stream(stream, dev), ctypes.byref(a)))
+    a = CNormArgs(ty, n, h, n_gates, yp, ldy or 0, rp, ldro or 0, res.data_ptr(), ldr, xp, ldx or 0, wp, pp, gp,
+                  ldg or 0, ip, alpha, eps, w_offset, 0)
+    _call("lora_residual_norm", _stream(stream, dev), ctypes.byref(a))
