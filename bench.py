@@ -865,7 +865,7 @@ def layer_sweep(args):
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1234)
     side = torch.cuda.Stream()
-    out = {"sweep": "layer", "form": args.layer_form, "rank": r,
+    out = {"sweep": "layer", "form": args.layer_form, "kv": args.layer_kv, "rank": r,
            "resident_adapters": slots, "layers": L, "steps": K, "results": []}
     for model in args.sweep_models.split(","):
         shape = LY.SHAPES[model]
@@ -874,7 +874,11 @@ def layer_sweep(args):
         dims = LY.proj_dims(shape)
         for seq in seqs:
             for n in ns:
-                caches = [LY.KVCache.random(shape, n, seq, gen) for _ in range(L)]
+                pstep = None
+                if args.layer_kv == "paged":
+                    pstep, caches = paged_caches(shape, n, seq, L, gen)
+                else:
+                    caches = [LY.KVCache.random(shape, n, seq, gen) for _ in range(L)]
                 hidden = torch.randn((n, shape.hidden), generator=gen, device="cuda").half()
                 rec = dict(model=shape.name, seq_len=seq, n=n)
                 metas = {}
@@ -898,7 +902,7 @@ def layer_sweep(args):
                     def run():
                         x = hidden
                         for lay, c in zip(layers, caches):
-                            x = lay.forward(x, c, meta)
+                            x = lay.forward(x, c, meta) if pstep is None else lay.forward_paged(x, c, pstep, meta)
                         return x
 
                     eager = run().clone()
@@ -936,6 +940,30 @@ def layer_sweep(args):
         del layers
         torch.cuda.empty_cache()
     print(json.dumps(out), flush=True)
+
+
+def paged_caches(shape, n, seq, layers, gen, page=16):
+    """A planned step of n requests with seq - 1 cached tokens each (in scattered pages) and one
+    new token, with rotary positions, and `layers` caches of random contents."""
+    import torch
+    from segmented_gather_matmul_amd import layer as LY
+    from segmented_gather_matmul_amd import step as ST
+    blocks = -(-seq // page)
+    num_pages = n * (blocks + 1)
+    pstep = LY.PagedStep(shape, n, n, blocks, num_pages, page, rope=ST.Rope.base(shape.head_dim))
+    ids = torch.randperm(num_pages, generator=gen, device="cuda").int()
+    pstep.pages.block_table.copy_(ids[:n * blocks].view(n, blocks))
+    pstep.pages.free_pages[:n].copy_(ids[n * blocks:])
+    pstep.pages.free_top.fill_(n)
+    pstep.kv_len.fill_(seq - 1)
+    pstep.begin(torch.ones(n, dtype=torch.int32, device="cuda"))
+    if int(pstep.plan.status[0]) != 0:
+        raise SystemExit(f"the paged step of {n} requests of {seq} tokens does not fit")
+    caches = [pstep.new_cache() for _ in range(layers)]
+    for c in caches:
+        c.k.normal_(generator=gen)
+        c.v.normal_(generator=gen)
+    return pstep, caches
 
 
 # ------------------------------------------------------------------ main
@@ -994,6 +1022,8 @@ def main():
     ap.add_argument("--sweep-pops", default="distinct,uniform,skewed,identical")
     ap.add_argument("--sweep-models", default="7b,13b", help="layer sweep: Llama-2 shapes")
     ap.add_argument("--sweep-seqs", default="512,2048", help="layer sweep: cache lengths")
+    ap.add_argument("--layer-kv", choices=["dense", "paged"], default="dense",
+                    help="--sweep layer: a dense key/value cache, or the paged step with rotary positions")
     ap.add_argument("--layer-form", choices=["bgmv", "sgmv"], default="bgmv",
                     help="layer sweep: add-ons in the per-row or the segment form")
     args = ap.parse_args()

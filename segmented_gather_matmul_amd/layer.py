@@ -16,9 +16,16 @@ form, for tiles of fewer than 8 rows).  Optionally each shrink runs on a second 
 while the backbone GEMM of the same input runs, so only the expands stay on the layer's
 critical path.
 
-Left out of the step on purpose: rotary position embedding (elementwise on q and k) and
-sampling.  The current token's k and v are written into the last position of the cache,
-so attention spans `seq_len` positions including it.
+Left out of the step on purpose: sampling, and, in the dense step, rotary position
+embedding.  In the dense step (LoraDecoderLayer.forward) the current token's k and v are
+written into the last position of the cache, so attention spans `seq_len` positions
+including it.
+
+The paged step (forward_paged) serves requests of any lengths, new tokens of prompts and of
+decoding requests in one batch, over a paged cache: PagedStep plans the step on the
+device from the requests' lengths once for all layers (pages, cache slots, the rows'
+adapter ids), and each layer runs the residual adds with their norms, rotary positions
+with the append to the cache, and attention over it in this library's kernels too.
 """
 from __future__ import annotations
 
@@ -40,6 +47,11 @@ class LlamaShape:
     heads: int
     head_dim: int = 128
     eps: float = 1e-5
+    kv_heads: int = 0   # key/value heads (0: as many as heads)
+
+    @property
+    def kv_width(self) -> int:
+        return (self.kv_heads or self.heads) * self.head_dim
 
 
 LLAMA2_7B = LlamaShape("llama2-7b", 4096, 11008, 32)
@@ -49,14 +61,14 @@ SHAPES = {"7b": LLAMA2_7B, "13b": LLAMA2_13B}
 
 def proj_dims(shape: LlamaShape) -> dict:
     """(d_in, d_out) of each adapted projection."""
-    h, f = shape.hidden, shape.ffn
-    return {"q": (h, h), "k": (h, h), "v": (h, h), "o": (h, h), "gate": (h, f), "up": (h, f), "down": (f, h)}
+    h, f, kv = shape.hidden, shape.ffn, shape.kv_width
+    return {"q": (h, h), "k": (h, kv), "v": (h, kv), "o": (h, h), "gate": (h, f), "up": (h, f), "down": (f, h)}
 
 
 def backbone_bytes(shape: LlamaShape) -> int:
     """fp16 bytes of one layer's backbone weights (projections and the two norm vectors)."""
-    h, f = shape.hidden, shape.ffn
-    return 2 * (4 * h * h + 3 * h * f + 2 * h)
+    h, f, kv = shape.hidden, shape.ffn, shape.kv_width
+    return 2 * (2 * h * h + 2 * h * kv + 3 * h * f + 2 * h)
 
 
 class BatchMeta:
@@ -80,6 +92,58 @@ class BatchMeta:
             tiles = B.lora_build_tiles(seg_ptr, seg_slot)
             self.segs = B.segments_to_device(tiles, row_map, n_act, device)
 
+    @classmethod
+    def of_step(cls, step: "PagedStep", num_slots, form="bgmv"):
+        """The metadata of whatever `step` plans: form "bgmv" reads the plan's row -> slot ids,
+        "sgmv" takes the plan's request offsets as segments, each with its request's slot.
+        Nothing is copied, so it holds for every later step too."""
+        if form not in ("bgmv", "sgmv"):
+            raise ValueError(f"unknown form {form!r}")
+        self = cls.__new__(cls)
+        self.n, self.form, self.num_slots, self.idx, self.segs = step.max_tokens, form, int(num_slots), step.plan.idx, None
+        if form == "sgmv":
+            self.segs = B.Segments.offsets(step.plan.q_ptr, step.req_slot)
+        return self
+
+
+class PagedStep:
+    """The serving state that every layer's paged step shares: up to n_req requests, their
+    cached lengths (kv_len), adapter slots (req_slot, -1 = none), pages (of page_size tokens,
+    num_pages of them, at most max_blocks a request) and the plan of the current step over at
+    most max_tokens token rows.  rope: a step.Rope or None.
+
+    begin(new_len) plans a step on the device: new_len (int32 [n_req], on the device) tokens
+    for each request, -1 for one that has ended.  Token rows are in request order
+    (plan.q_ptr); rows behind the last one belong to no request.  plan.status[0] is 0 unless
+    the step does not fit; then nothing changes and the layers leave every cache as it is."""
+
+    def __init__(self, shape: LlamaShape, n_req, max_tokens, max_blocks, num_pages, page_size=16, rope=None,
+                 device="cuda"):
+        import torch
+        from . import step as S
+        self.shape, self.n_req, self.max_tokens, self.rope = shape, int(n_req), int(max_tokens), rope
+        self.pages = S.KVPages.fresh(n_req, max_blocks, num_pages, page_size, device)
+        self.kv_len = torch.zeros(max(self.n_req, 1), dtype=torch.int32, device=device)
+        self.req_slot = torch.full((self.n_req,), -1, dtype=torch.int32, device=device)
+        self.plan = S.KVPlan(n_req, max_tokens, device, kv_end=self.kv_len, free_top=self.pages.free_top)
+        self.row_len = torch.zeros(self.max_tokens, dtype=torch.int32, device=device)
+        self.work = S.workspace(max_tokens, shape.heads, shape.kv_heads or shape.heads, shape.head_dim, device)
+
+    def new_cache(self, dtype=None, device="cuda"):
+        """An empty cache for one layer."""
+        import torch
+        from . import step as S
+        size = (self.pages.free_pages.numel(), self.pages.page_size, self.shape.kv_heads or self.shape.heads,
+                self.shape.head_dim)
+        zeros = lambda: torch.zeros(size, dtype=torch.float16 if dtype is None else dtype, device=device)
+        return S.PagedKV(zeros(), zeros())
+
+    def begin(self, new_len):
+        import torch
+        from . import step as S
+        S.lora_kv_plan(self.plan, self.pages, self.kv_len, new_len, req_slot=self.req_slot)
+        torch.add(self.plan.tok_pos, 1, out=self.row_len)   # each row sees its request up to itself
+
 
 class KVCache:
     """One layer's cache for n sequences of seq_len positions: keys stored transposed
@@ -101,7 +165,8 @@ class KVCache:
 class LoraDecoderLayer:
     """One decoder layer: backbone weights and the seven projections' adapter stores.
 
-    backbone: dict of fp16 device tensors w_qkv [h, 3h], w_o [h, h], w_gu [h, 2f],
+    backbone: dict of fp16 device tensors w_qkv [h, 3h] ([h, h + 2 kv_width] with fewer
+    key/value heads), w_o [h, h], w_gu [h, 2f],
     w_d [f, h] (all applied as x @ W), norm1 [h], norm2 [h].
     adapters: proj -> (a_t [S, r_max, d_in], b [S, r_max, d_out]) fp16 device tensors.
     rank (int32 [S]) and scale (fp32 [S]) are the slots' ranks and scales, shared by the
@@ -193,6 +258,8 @@ class LoraDecoderLayer:
         s, bb = self.shape, self.bb
         h, f, H, dh = s.hidden, s.ffn, s.heads, s.head_dim
         n = hidden.shape[0]
+        if s.kv_width != h:
+            raise ValueError("the dense step has as many key/value heads as query heads: use forward_paged")
         if n > self.max_rows or cache.n != n or cache.heads != H or cache.head_dim != dh:
             raise ValueError(f"batch of {n} rows does not fit this layer or cache")
         if meta is not None and meta.n != n:
@@ -217,6 +284,41 @@ class LoraDecoderLayer:
                 trace[name] = t.clone()
         return h1 + d
 
+    def forward_paged(self, hidden, cache, step: PagedStep, meta: BatchMeta | None, trace: dict | None = None):
+        """hidden [step.max_tokens, h] fp16 -> the same, for the token rows of the step planned
+        last; rows behind the last token are not read by any other row.  cache: this layer's
+        step.PagedKV.  meta and trace as for forward (meta: BatchMeta.of_step)."""
+        import torch
+        import torch.nn.functional as F
+        from . import step as S
+        s, bb = self.shape, self.bb
+        h, f, kv = s.hidden, s.ffn, s.kv_width
+        n = hidden.shape[0]
+        if n > self.max_rows or n != step.max_tokens or step.shape != s:
+            raise ValueError(f"batch of {n} rows does not fit this layer or step")
+        if meta is not None and meta.n != n:
+            raise ValueError(f"metadata for {meta.n} rows, batch of {n}")
+
+        a = torch.empty_like(hidden)
+        S.lora_residual_norm(a, hidden, bb["norm1"], eps=s.eps)
+        q, k, v = self._project(meta, a, bb["w_qkv"], ("q", "k", "v"), (h, kv, kv))
+        q_rot, attn = torch.empty_like(hidden), torch.zeros_like(hidden)   # zeros: rows of no request
+        S.lora_rope_append(q_rot, q, k, v, cache, step.plan.slots, rope=step.rope, positions=step.plan.tok_pos)
+        S.lora_paged_attention(attn, q_rot, cache, step.pages.block_table, step.row_len, step.work,
+                               req=step.plan.tok_req)
+        (o,) = self._project(meta, attn, bb["w_o"], ("o",), (h,))
+        h1, a2 = torch.empty_like(hidden), torch.empty_like(hidden)
+        S.lora_residual_norm(a2, hidden, bb["norm2"], x=o, res_out=h1, eps=s.eps)
+        g, u = self._project(meta, a2, bb["w_gu"], ("gate", "up"), (f, f))
+        act = F.silu(g) * u
+        (d,) = self._project(meta, act, bb["w_d"], ("down",), (h,))
+        if trace is not None:
+            for name, t in zip(PROJS, (q, k, v, o, g, u, d)):
+                trace[name] = t.clone()
+        out = torch.empty_like(hidden)
+        S.lora_residual_norm(None, h1, x=d, res_out=out)
+        return out
+
 
 def random_layer(shape: LlamaShape, num_slots, rank, max_rows, gen, device="cuda", overlap=False, handoff=True):
     """A layer with N(0, 0.02) fp16 backbone and adapter weights drawn on the device, every
@@ -227,7 +329,7 @@ def random_layer(shape: LlamaShape, num_slots, rank, max_rows, gen, device="cuda
         return (torch.randn(sh, generator=gen, device=device) * 0.02).half()
 
     h, f = shape.hidden, shape.ffn
-    bb = dict(w_qkv=rnd(h, 3 * h), w_o=rnd(h, h), w_gu=rnd(h, 2 * f), w_d=rnd(f, h),
+    bb = dict(w_qkv=rnd(h, h + 2 * shape.kv_width), w_o=rnd(h, h), w_gu=rnd(h, 2 * f), w_d=rnd(f, h),
               norm1=torch.ones(h, dtype=torch.float16, device=device),
               norm2=torch.ones(h, dtype=torch.float16, device=device))
     ads = {p: (rnd(num_slots, rank, di), rnd(num_slots, rank, do)) for p, (di, do) in proj_dims(shape).items()}

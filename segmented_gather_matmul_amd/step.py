@@ -273,13 +273,18 @@ class Rope:
         return cls(f, axis, axes, interleaved)
 
 
-def attention_workspace(n_rows, heads, cache: PagedKV, device=None):
-    """A zeroed workspace for lora_paged_attention calls of up to n_rows rows of `heads` query
-    heads over `cache` (the library leaves its counters zero after every call)."""
-    n = int(B.lib().lora_paged_attention_bytes(int(n_rows), int(heads), cache.kv_heads, cache.head_dim))
+def workspace(n_rows, heads, kv_heads, head_dim, device="cuda"):
+    """A zeroed workspace for lora_paged_attention calls of up to n_rows rows and this head
+    layout (the library leaves its counters zero after every call)."""
+    n = int(B.lib().lora_paged_attention_bytes(int(n_rows), int(heads), int(kv_heads), int(head_dim)))
     if n == 0:
-        raise ValueError(f"{heads} query heads over {cache.kv_heads} key/value heads, {n_rows} rows")
-    return torch.zeros(n // 4, dtype=torch.int32, device=cache.k.device if device is None else device)
+        raise ValueError(f"{heads} query heads over {kv_heads} key/value heads of {head_dim}, {n_rows} rows")
+    return torch.zeros(n // 4, dtype=torch.int32, device=device)
+
+
+def attention_workspace(n_rows, heads, cache: PagedKV, device=None):
+    """workspace for calls over `cache`."""
+    return workspace(n_rows, heads, cache.kv_heads, cache.head_dim, cache.k.device if device is None else device)
 
 
 # ------------------------------------------------------------------ launches
