@@ -1049,6 +1049,7 @@ void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
     (D == DP ? launch_args(lora_paged_attention_kernel<T, DP, true>, grid, 64 * kAttnWaves, 0, s, a)          \
              : launch_args(lora_paged_attention_kernel<T, DP, false>, grid, 64 * kAttnWaves, 0, s, a))
     if (D <= 64) LORA_ATTN(64);
+    else if (D <= 96) LORA_ATTN(96);
     else if (D <= 128) LORA_ATTN(128);
     else LORA_ATTN(256);
 #undef LORA_ATTN

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -58,6 +59,10 @@ class CNormArgs(ctypes.Structure):
                 ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("reserved", _I32)]
 
 
+_pack_norm = struct.Struct("4i13q3fi").pack   # the bytes of a CNormArgs, in a fifth of the time
+assert struct.calcsize("4i13q3fi") == ctypes.sizeof(CNormArgs)
+
+
 # ------------------------------------------------------------------ argument checks
 _NAMES = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int32: "i32"}
 
@@ -72,7 +77,10 @@ def _type(t, what):
 def _matrix(t, what, dtype, rows, cols):
     """t: 2-D, of `dtype`, unit column stride, >= rows rows and >= cols columns; its row stride."""
     try:
-        (n, c), (ld, sc) = t.shape, t.stride()
+        n, c = t.shape
+        if t.dtype is dtype and n >= rows and c == cols and t.is_contiguous() and (n > 1 or c % 8 == 0):
+            return c
+        ld, sc = t.stride()
         if t.dtype is dtype and n >= rows and c >= cols and sc == 1 and ld >= cols and (n > 1 or ld % 8 == 0):
             return ld
     except (AttributeError, TypeError, ValueError):
@@ -118,12 +126,13 @@ def _vector(t, what, dtype, n):
 
 def _here(names, *tensors):
     """Every tensor (None: not given) is on the current GPU; its index."""
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != dev:
             break
     else:
-        return dev
+        if dev >= 0 and dev == torch.cuda.current_device():
+            return dev
     for what, t in zip(names.split(), tensors):
         if t is not None and not t.is_cuda:
             raise ValueError(f"{what} must be a GPU tensor (got device {t.device})")
@@ -388,8 +397,7 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
     n, h = res.shape
     dt = res.dtype
     ldr = _matrix(res, "res", dt, n, h)
-    yp = ldy = wp = rp = ldro = xp = ldx = pp = gp = ldg = ip = None
-    n_gates = 0
+    yp = ldy = wp = rp = ldro = xp = ldx = pp = gp = ldg = ip = n_gates = 0
     if y is not None:
         ldy, yp = _matrix(y, "y", dt, n, h), y.data_ptr()
         _vector(w, "w", dt, h)
@@ -409,6 +417,6 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
         _vector(gate_idx, "gate_idx", torch.int32, n)
         ip = gate_idx.data_ptr()
     dev = _here("res y res_out x w post_w gate gate_idx", res, y, res_out, x, w, post_w, gate, gate_idx)
-    a = CNormArgs(ty, n, h, n_gates, yp, ldy or 0, rp, ldro or 0, res.data_ptr(), ldr, xp, ldx or 0, wp, pp, gp,
-                  ldg or 0, ip, alpha, eps, w_offset, 0)
-    _call("lora_residual_norm", _stream(stream, dev), ctypes.byref(a))
+    _call("lora_residual_norm", _stream(stream, dev),
+          _pack_norm(ty, n, h, n_gates, yp, ldy, rp, ldro, res.data_ptr(), ldr, xp, ldx, wp, pp, gp, ldg, ip, alpha, eps,
+                     w_offset, 0))
