@@ -173,7 +173,8 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
  *
  *   out, q       device [n_rows][ld], ld % 8 == 0, ld >= q_heads * head_dim; the cache's type
  *   q_heads      a multiple of kv_heads
- *   block_table  device int32 [n_req][ld_table], ld_table >= max_blocks
+ *   block_table  device int32 [n_req][ld_table], ld_table >= max_blocks;
+ *                max_blocks * page_size <= 2^30
  *   kv_len       device int32 [n_rows] (the query's own token included)
  *   req          device int32 [n_rows] or NULL
  *   scale        any finite value (usually 1/sqrt(head_dim))

@@ -383,13 +383,16 @@ struct AppendArgs {
 
 constexpr int32_t kAppendFill = 1024;  // rows that fill the CUs with one workgroup each
 
-// cos and sin of position * inv_freq: the product is exact in 64 bits (31 + 24 bits), so
-// reducing it to turns in 64 bits leaves the angle right to 2^-22 turns or better at any
-// 32-bit position.
+// cos and sin of position * inv_freq.  The product (31 + 24 bits) is kept as p + e, exactly,
+// and 1 / (2 pi) to twice 53 bits, so the fraction of a turn is right to 2^-50 at any 32-bit
+// position; it is rounded to fp32 only then.
 __device__ inline float2 turn_of(int32_t pos, float inv_freq)
 {
-    const double turns = (double)pos * (double)inv_freq * 0.15915494309189533577;
-    const float half_turns = (float)(2.0 * (turns - rint(turns)));
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    const double p = (double)pos * (double)inv_freq, e = __builtin_fma((double)pos, (double)inv_freq, -p);
+    const double whole = rint(p * kHi);
+    const double part = __builtin_fma(p, kHi, -whole) + __builtin_fma(p, kLo, e * kHi);
+    const float half_turns = (float)(2.0 * part);
     float2 cs;
     cs.y = sinpif(half_turns);
     cs.x = cospif(half_turns);
@@ -507,6 +510,7 @@ constexpr int kAttnRowTiles = 4;     // what starting and finishing a row costs,
 constexpr int kAttnJoin = 16;        // parts joined at a time
 constexpr int kAttnMaxTiles = 4096;  // key/value heads x 16-head tiles of one launch
 constexpr int kAttnCUs = 256;
+constexpr int32_t kAttnMaxSpan = 1 << 30;  // tokens of a table row: positions and steps past them fit 32 bits
 // Wavefronts per SIMD, and so workgroups per CU, that the registers are kept to.
 constexpr int attn_occupancy(int dp) { return dp <= 64 ? 2 : 1; }
 // Arrival counters: two part slots per workgroup, and at most 4 workgroups per CU or one
@@ -514,21 +518,18 @@ constexpr int attn_occupancy(int dp) { return dp <= 64 ? 2 : 1; }
 // different shapes sharing a workspace never put sums where another finds its counters.
 constexpr size_t kAttnCounters = 2 * (4 * kAttnCUs + kAttnMaxTiles);
 
-// Visible tokens [first, first + span) of row i; span -1: the row is not active.
+// Visible tokens [first, first + span) of row i; span -1: the row is not active, or none.
 struct RowSpan {
     int32_t req, first, span;
 };
 
 __device__ inline RowSpan row_span(const AttnArgs &a, int32_t i)
 {
-    RowSpan s{0, 0, -1};
-    if (i >= a.n_rows) return s;
-    const int32_t n = a.kv_len[i];
-    s.req = a.req ? a.req[i] : i;
-    if (n < 0 || n > (int64_t)a.max_blocks << a.shift || s.req < 0 || s.req >= a.n_req) return s;
-    s.first = a.window > 0 && n > a.window ? n - a.window : 0;
-    s.span = n - s.first;
-    return s;
+    const int32_t at = min(i, a.n_rows - 1);  // loads without a branch, so many can be in flight
+    const int32_t n = a.kv_len[at], r = a.req ? a.req[at] : at;
+    const bool on = i < a.n_rows && n >= 0 && n <= a.max_blocks << a.shift && r >= 0 && r < a.n_req;
+    const int32_t first = a.window > 0 && n > a.window ? n - a.window : 0;
+    return RowSpan{r, first, on ? n - first : -1};
 }
 
 // The schedule of a launch, found by every workgroup from the lengths on the device.  Each
@@ -558,39 +559,65 @@ __device__ inline int32_t wave_scan(int32_t v)
     return v;
 }
 
-// The first row with work at or behind position w * share (row n_rows: none), and the
-// share.  Every wavefront finds it for itself, 64 rows at a time, so nothing waits on a
-// barrier; the host has checked that the line fits 32 bits.
-__device__ inline RowWork first_row(const AttnArgs &a, int32_t w, int32_t &share)
+// A wavefront's walk over the rows of a launch, 64 of them in its lanes at a time.
+struct RowWalk {
+    int32_t base;   // the lanes hold rows base .. base + 63
+    RowSpan rs;     // lane's row
+    int32_t tiles;
+
+    __device__ inline void load(const AttnArgs &a, int32_t b)
+    {
+        base = b;
+        rs = row_span(a, b + (int32_t)(threadIdx.x & 63));
+        tiles = row_tiles(rs);
+    }
+    __device__ inline RowWork row(int lane, int32_t tile0) const
+    {
+        return RowWork{base + lane, tile0, __builtin_amdgcn_readlane(tiles, lane),
+                       RowSpan{__builtin_amdgcn_readlane(rs.req, lane), __builtin_amdgcn_readlane(rs.first, lane),
+                               __builtin_amdgcn_readlane(rs.span, lane)}};
+    }
+    // The next active row behind row r, at position tile0 of the line (row n_rows: none).
+    __device__ inline RowWork after(const AttnArgs &a, int32_t r, int32_t tile0)
+    {
+        uint64_t on = r + 1 - base < 64 ? __ballot(tiles > 0) & (~(uint64_t)0 << (r + 1 - base)) : 0;
+        while (!on && base + 64 < a.n_rows) {
+            load(a, base + 64);
+            on = __ballot(tiles > 0);
+        }
+        return on ? row(__builtin_ctzll(on), tile0) : RowWork{a.n_rows, 0, 0, RowSpan{0, 0, -1}};
+    }
+};
+
+// The first row with work at or behind position w * share (row n_rows: none), the share and
+// the line's length.  Every wavefront finds it for itself, so nothing waits on a barrier;
+// the host has checked that the line fits 32 bits.
+__device__ inline RowWork first_row(const AttnArgs &a, int32_t w, RowWalk &walk, int32_t &share, int32_t &total)
 {
     const int lane = threadIdx.x & 63;
-    const RowSpan none{0, 0, -1};
-    RowSpan rs = row_span(a, lane);
-    int32_t tiles = row_tiles(rs), total = tiles > 0 ? tiles + kAttnRowTiles : 0;
-    for (int32_t i = lane + 64; i < a.n_rows; i += 64) {
-        const int32_t t = row_tiles(row_span(a, i));
-        total += t > 0 ? t + kAttnRowTiles : 0;
+    walk.load(a, 0);
+    int32_t sum = walk.tiles > 0 ? walk.tiles + kAttnRowTiles : 0;
+#pragma unroll 8
+    for (int32_t c = 64; c < a.n_rows; c += 64) {
+        const int32_t t = row_tiles(row_span(a, c + lane));
+        sum += t > 0 ? t + kAttnRowTiles : 0;
     }
-    total = __builtin_amdgcn_readlane(wave_scan(total), 63);
+    total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
     share = max((total + a.shares - 1) / a.shares, kAttnMinShare);
     const int64_t begin = (int64_t)w * share;
     int32_t at0 = 0;
-    for (int32_t c = 0; c < a.n_rows && begin < total; c += 64) {
-        if (c > 0) {
-            rs = row_span(a, c + lane);
-            tiles = row_tiles(rs);
-        }
-        const int32_t cost = tiles > 0 ? tiles + kAttnRowTiles : 0, end = at0 + wave_scan(cost);
+    while (begin < total) {
+        const int32_t cost = walk.tiles > 0 ? walk.tiles + kAttnRowTiles : 0, end = at0 + wave_scan(cost);
         const uint64_t here = __ballot(end - cost <= begin && begin < end);
         if (here) {
             const int l = __builtin_ctzll(here);
-            return RowWork{c + l, __builtin_amdgcn_readlane(end - tiles, l), __builtin_amdgcn_readlane(tiles, l),
-                           RowSpan{__builtin_amdgcn_readlane(rs.req, l), __builtin_amdgcn_readlane(rs.first, l),
-                                   __builtin_amdgcn_readlane(rs.span, l)}};
+            return walk.row(l, __builtin_amdgcn_readlane(end - walk.tiles, l));
         }
         at0 = __builtin_amdgcn_readlane(end, 63);
+        if (walk.base + 64 >= a.n_rows) break;
+        walk.load(a, walk.base + 64);
     }
-    return RowWork{a.n_rows, 0, 0, none};
+    return RowWork{a.n_rows, 0, 0, RowSpan{0, 0, -1}};
 }
 
 __device__ inline f4_t mfma(const vec8<F16> &x, const vec8<F16> &y, const f4_t &c)
@@ -604,8 +631,9 @@ __device__ inline f4_t mfma(const vec8<BF16> &x, const vec8<BF16> &y, const f4_t
 
 // A weight p in [0, 2^kBias] as two 16-bit parts, hi + lo, both cut off (never rounded up)
 // and neither 0, so that hi * v + lo * v is what p * v is for an infinite v too.  fp16 keeps
-// 22 bits (the bias keeps weights down to 2^-38 of the largest out of its subnormals), bf16
-// 16 bits: both far below the rounding of the output.
+// 22 bits (the bias lifts weights out of its subnormals, whose step is 2^-38 of the largest
+// weight; a weight of 0 counts as two such steps), bf16 16 bits: both far below the
+// rounding of the output.
 template <typename T>
 struct Weight;
 template <>
@@ -804,10 +832,11 @@ lora_paged_attention_kernel(AttnArgs a)
     const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
     const int32_t in_page = (1 << a.shift) - 1;
-    int32_t share;
-    RowWork rw = first_row(a, wg, share);
+    int32_t share, total;
+    RowWalk walk;
+    RowWork rw = first_row(a, wg, walk, share, total);
     if (rw.row >= a.n_rows) return;
-    const int32_t line0 = wg * share, line1 = (int32_t)min((int64_t)line0 + share, (int64_t)INT32_MAX);
+    const int32_t line0 = wg * share, line1 = (int32_t)min((int64_t)line0 + share, (int64_t)total);
 
     // A row's part in this share: tokens [begin, end); the row has `parts` parts from workgroup w0 on.
     struct Part {
@@ -823,12 +852,8 @@ lora_paged_attention_kernel(AttnArgs a)
                          tile0 < line0 ? tile0 / share : wg, 1, a.table + (int64_t)rw.rs.req * a.ld_table};
             int32_t last = wg;
             if (row_end > line1) last = (row_end - 1) / share;
-            do {
-                rw.rs = row_span(a, ++rw.row);
-                rw.tiles = row_tiles(rw.rs);
-            } while (rw.tiles == 0 && rw.row < a.n_rows);
-            rw.tile0 = row_end + kAttnRowTiles;
-            if (row_end >= line1) rw.row = a.n_rows;
+            if (row_end < line1) rw = walk.after(a, rw.row, row_end + kAttnRowTiles);
+            else rw.row = a.n_rows;
             if (from < to) return Part{p.row, p.begin, p.end, p.w0, last - p.w0 + 1, p.table};
             // else the row's tiles lie in the next workgroup's share
         }
@@ -1181,10 +1206,12 @@ int check_cache(const lora_kv_cache *c)
     if (!c->k || !c->v) return fail(LORA_E_NULL, "cache needs k and v");
     if (!aligned16(c->k) || !aligned16(c->v)) return fail(LORA_E_ALIGN, "cache k and v must be 16-byte aligned");
     for (int64_t s : {c->page_stride, c->token_stride, c->head_stride}) {
-        if (s < c->head_dim || s > (int64_t)1 << 50)
-            return fail(LORA_E_SHAPE, "cache stride %lld < head_dim = %d", (long long)s, c->head_dim);
+        if (s < c->head_dim) return fail(LORA_E_SHAPE, "cache stride %lld < head_dim = %d", (long long)s, c->head_dim);
         if (s % 8) return fail(LORA_E_ALIGN, "cache stride %lld is not a multiple of 8", (long long)s);
     }
+    const __int128 reach = (__int128)(c->num_pages - 1) * c->page_stride + (__int128)(c->page_size - 1) * c->token_stride +
+                           (__int128)(c->kv_heads - 1) * c->head_stride + c->head_dim;
+    if (reach > (__int128)1 << 48) return fail(LORA_E_SHAPE, "the cache's last element is beyond 2^48");
     return LORA_OK;
 }
 
@@ -1365,8 +1392,9 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     if (n_rows < 0 || n_req < 0) return fail(LORA_E_SHAPE, "n_rows = %d, n_req = %d", n_rows, n_req);
     if (q_heads < 1 || q_heads % cache->kv_heads)
         return fail(LORA_E_SHAPE, "q_heads = %d is not a multiple of kv_heads = %d", q_heads, cache->kv_heads);
-    if (max_blocks < 1 || ld_table < max_blocks || (int64_t)max_blocks * cache->page_size > INT32_MAX)
-        return fail(LORA_E_SHAPE, "max_blocks = %d, ld_table = %lld", max_blocks, (long long)ld_table);
+    if (max_blocks < 1 || ld_table < max_blocks || (int64_t)max_blocks * cache->page_size > kAttnMaxSpan)
+        return fail(LORA_E_SHAPE, "max_blocks = %d of %d tokens, ld_table = %lld", max_blocks, cache->page_size,
+                    (long long)ld_table);
     if (window < 0) return fail(LORA_E_SHAPE, "window = %d", window);
     if (!std::isfinite(scale)) return fail(LORA_E_SHAPE, "scale is not finite");
     if ((int64_t)n_rows * q_heads > (int64_t)1 << 30)

@@ -5,7 +5,9 @@ Roundings counted by the tolerances, with u = 2^-24 (half a step of fp32, relati
 half_step(t) = finfo(t).eps / 2 for the output type t:
   rotary   cos and sin are off by at most pi 2^-25 (the reduced angle rounded to fp32) plus
            4 u (two fp32 units of the sine), under 2^-22; a product and a fused
-           multiply-add round twice more: |err| <= half_step |y| + 2^-21 (|a| + |b|).
+           multiply-add round twice more: |err| <= half_step |y| + 2^-21 (|a| + |b|).  The
+           reference's own angle is a 64-bit product, off by 2^-53 of itself: where that is
+           more than 2^-23 (positions beyond 10^9), it is counted too, in (|a| + |b|).
   attention  a score is a sum of D products in fp32, scaled and moved to base 2:
            ds = (D + 8) u |scale| max_t sum_d |q_d k_td|, both for the score and for the
            maximum it is compared with; exp2, the split of p into two 16-bit parts and the
@@ -104,7 +106,7 @@ def rotate(x, pos, inv_freq, axis, n_axes, interleaved):
         c, s = ang.cos()[:, None], ang.sin()[:, None]
         xa, xb = x[:, :, a].to(F64), x[:, :, b].to(F64)
         y[:, :, a], y[:, :, b] = xa * c - xb * s, xa * s + xb * c
-        mag[:, :, a] = mag[:, :, b] = xa.abs() + xb.abs()
+        mag[:, :, a] = mag[:, :, b] = (xa.abs() + xb.abs()) * (1 + ang.abs()[:, None] * 2.0 ** (21 - 53))
     return y, mag
 
 

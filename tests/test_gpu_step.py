@@ -433,6 +433,24 @@ def test_attention_rows_that_are_not_active():
     c.check(out, lse, want, "inactive")
 
 
+@pytest.mark.parametrize("n,every", [(64, 1), (65, 64), (300, 1), (700, 3), (5000, 1111), (5000, 5000)])
+def test_attention_of_many_rows_few_of_them_active(n, every):
+    """A batch padded far beyond its tokens, and rows in more chunks than one wavefront holds."""
+    say(f"case attention-rows {n} every {every}")
+    lens = [(1 + 37 * i % 200) if i % every == every - 1 else -1 for i in range(n)]
+    c = AttnCase(lens, 2, 1, 32, 16, F16, seed=n)
+    out, lse = c.run()
+    for i, w in enumerate(c.want()):
+        if w is not None:
+            close(out[i].view(2, 32), w[0], w[2], f"row {i}")
+            close(lse[i], w[1], w[3], f"row {i} lse")
+    off = torch.tensor([v < 0 for v in lens], device="cuda")
+    assert (out[off] == 7.0).all() and (lse[off] == 9.0).all()
+    want = torch.zeros(n, dtype=torch.bool)
+    want[~off.cpu()] = True
+    assert want.any()
+
+
 def test_attention_rows_that_share_a_request():
     say("case attention-shared")
     req = [0, 0, 0, 2, 2, 1, 0]

@@ -50,7 +50,8 @@ CACHE_FAULTS = [(dict(type=2), B.LORA_E_UNSUPPORTED), (dict(page_size=0), B.LORA
                 (dict(head_dim=60), B.LORA_E_SHAPE), (dict(head_dim=264), B.LORA_E_SHAPE),
                 (dict(reserved=1), B.LORA_E_SHAPE), (dict(k=None), B.LORA_E_NULL), (dict(v=None), B.LORA_E_NULL),
                 (dict(k=PTR + 8), B.LORA_E_ALIGN), (dict(token_stride=32), B.LORA_E_SHAPE),
-                (dict(head_stride=68), B.LORA_E_ALIGN), (dict(page_stride=-2048), B.LORA_E_SHAPE)]
+                (dict(head_stride=68), B.LORA_E_ALIGN), (dict(page_stride=-2048), B.LORA_E_SHAPE),
+                (dict(page_stride=1 << 62), B.LORA_E_SHAPE), (dict(token_stride=(1 << 63) - 8), B.LORA_E_SHAPE)]
 
 
 @pytest.mark.parametrize("kw,code", CACHE_FAULTS, ids=lambda x: str(x))
@@ -79,7 +80,8 @@ def _attn(**kw):
     (dict(heads=0), B.LORA_E_SHAPE), (dict(cache=None), B.LORA_E_NULL), (dict(out=None), B.LORA_E_NULL),
     (dict(q=None), B.LORA_E_NULL), (dict(q=PTR + 4098), B.LORA_E_ALIGN), (dict(ldq=255), B.LORA_E_SHAPE),
     (dict(ldo=260), B.LORA_E_ALIGN), (dict(blocks=0), B.LORA_E_SHAPE), (dict(ldt=3), B.LORA_E_SHAPE),
-    (dict(blocks=1 << 28, ldt=1 << 28), B.LORA_E_SHAPE), (dict(kv_len=None), B.LORA_E_NULL),
+    (dict(blocks=1 << 28, ldt=1 << 28), B.LORA_E_SHAPE), (dict(blocks=(1 << 26) + 1, ldt=1 << 27), B.LORA_E_SHAPE),
+    (dict(n_rows=65536, blocks=1 << 26, ldt=1 << 26, out=PTR + (1 << 40)), B.LORA_E_UNSUPPORTED), (dict(kv_len=None), B.LORA_E_NULL),
     (dict(table=None), B.LORA_E_NULL), (dict(window=-1), B.LORA_E_SHAPE), (dict(scale=float("inf")), B.LORA_E_SHAPE),
     (dict(scale=float("nan")), B.LORA_E_SHAPE), (dict(lse=PTR + 2), B.LORA_E_ALIGN), (dict(work=None), B.LORA_E_NULL),
     (dict(work=PTR + 128), B.LORA_E_ALIGN), (dict(work_bytes=0), B.LORA_E_SHAPE),
