@@ -82,12 +82,13 @@ struct PlanArgs {
     lora_kv_pages pg;
     lora_kv_plan_out out;
     const int32_t *kv_len, *new_len, *req_slot;
-    int32_t shift;     // log2(page_size)
-    int32_t map_here;  // workgroup 0 writes the token maps (else further workgroups, or a second launch)
+    int32_t shift;   // log2(page_size)
+    int32_t move;    // this launch moves the pages and writes the maps
+    int32_t finish;  // this launch writes the lengths, offsets, free top and status
 };
 
-constexpr int kPlanThreads = 1024;   // requests planned at a time
-constexpr int kPlanMapsHere = 4096;  // token rows up to which a launch of one workgroup writes the maps itself
+constexpr int kPlanThreads = 1024;  // requests planned at a time
+constexpr int kPlanGroups = 256;    // workgroups of a launch at most: one per CU
 
 // One request of a plan; `bad` holds its LORA_KV_* bits.
 struct PlanReq {
@@ -204,19 +205,35 @@ __device__ inline void plan_map_row(const PlanArgs &a, int32_t t, int32_t r, int
     if (o.idx) o.idx[t] = r < 0 || !a.req_slot ? -1 : a.req_slot[r];
 }
 
-// The plan, by one workgroup: prefix sums and checks over all requests first (all or
-// nothing), then, THREADS requests at a time, the pages of ended requests onto the free
-// list, and after all of those the pages of growing ones off it.  A chunk's work is spread
-// over the workgroup by page and by token, each found by a binary search in the chunk's
-// prefix sums.  Bound by the latency of its chain of loads (lengths, then ids), so small
-// batches run in one wavefront, where no barrier waits.
-//
-// Where a step has many token rows and one chunk holds all requests, workgroups 1, 2, ...
-// make the same sums for themselves and write the maps of THREADS rows each.  They read
-// only what workgroup 0 does not write: table entries that were there before, and the free
-// list below its old end (a page that an ended request gives back in this step is read
-// from that request's table row).  That needs kv_end and the free top to be other arrays
-// than the ones read.
+// What the sums of all requests allow: LORA_KV_* bits.
+__device__ inline int32_t plan_check(const PlanArgs &a, const PlanSums &s, int32_t top0)
+{
+    int32_t bad = s.bad;
+    if (top0 < 0 || top0 > a.pg.num_pages || top0 + (int64_t)s.all_given > a.pg.num_pages) bad |= LORA_KV_INVALID;
+    if (s.all_grown > top0 + (int64_t)s.all_given) bad |= LORA_KV_NO_PAGES;
+    if ((int64_t)s.all_add > a.out.max_tokens) bad |= LORA_KV_TOO_MANY;
+    return bad;
+}
+
+__device__ inline void plan_status(const PlanArgs &a, const PlanSums &s, int32_t top0, int32_t bad)
+{
+    a.out.status[0] = bad;
+    a.out.status[1] = (int32_t)min(s.all_add, (uint32_t)INT32_MAX);
+    a.out.status[2] = (int32_t)min(s.all_grown, (uint32_t)INT32_MAX);
+    a.out.status[3] = (int32_t)min(s.all_given, (uint32_t)INT32_MAX);
+    a.out.free_top[0] = bad ? top0 : (int32_t)(top0 + (int64_t)s.all_given - s.all_grown);
+    a.out.q_ptr[a.pg.n_req] = bad ? 0 : (int32_t)s.all_add;
+}
+
+// The plan of up to THREADS requests.  Every workgroup makes the prefix sums and checks for
+// itself (all or nothing), then takes its share of the pages given back, the pages taken
+// and the token rows, each found by a binary search in the sums.  Nothing that one thread
+// reads is written by another: the table entries read were there before, and free_pages is
+// read below its old end only -- a page that an ended request gives back in this step is
+// taken from that request's table row.  Lengths and free top are written by workgroup 0,
+// or, where they are updated in place and there are more workgroups, by a second launch.
+// Bound by the latency of its chain of loads (lengths, then ids), so small batches run in
+// few wavefronts, whose barriers are cheap.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void lora_kv_plan_kernel(PlanArgs a)
 {
@@ -224,136 +241,127 @@ __global__ __launch_bounds__(THREADS) void lora_kv_plan_kernel(PlanArgs a)
     __shared__ int32_t off[THREADS], off_given[THREADS], off_tok[THREADS], had_s[THREADS], len_s[THREADS];
     const int tid = threadIdx.x;
     const int32_t n = a.pg.n_req;
-    const bool one = n <= THREADS;  // one chunk holds all requests
     const int32_t top0 = *a.pg.free_top;
-    PlanReq q = plan_req(a, tid);
-    PlanSums s = plan_scan<THREADS>(q, wave_sums);
-    if (!one) {
-        PlanReq sum = q;
-        for (int32_t r = tid + THREADS; r < n; r += THREADS) {
-            const PlanReq x = plan_req(a, r);
-            sum.bad |= x.bad;
-            sum.given = __builtin_elementwise_add_sat(sum.given, x.given);
-            sum.grown = __builtin_elementwise_add_sat(sum.grown, x.grown);
-            sum.add = __builtin_elementwise_add_sat(sum.add, x.add);
+    const PlanReq q = plan_req(a, tid);
+    const PlanSums s = plan_scan<THREADS>(q, wave_sums);
+    const int32_t bad = plan_check(a, s, top0);
+    off[tid] = (int32_t)s.grown;
+    off_given[tid] = (int32_t)s.given;
+    off_tok[tid] = (int32_t)s.add;
+    had_s[tid] = q.had;
+    len_s[tid] = q.len;
+    __syncthreads();  // also: every thread has read its lengths and the free top
+    if (a.finish && blockIdx.x == 0) {
+        if (tid == 0) plan_status(a, s, top0, bad);
+        if (tid < n) {
+            a.out.kv_end[tid] = bad ? q.len : (int32_t)q.end;
+            a.out.q_ptr[tid] = bad ? 0 : (int32_t)s.add;
         }
-        const PlanSums all = plan_scan<THREADS>(sum, wave_sums);
-        s.all_given = all.all_given;
-        s.all_grown = all.all_grown;
-        s.all_add = all.all_add;
-        s.bad = all.bad;
     }
-    const int64_t given = s.all_given, taken = s.all_grown, tokens = s.all_add;
-    int32_t bad = s.bad;
-    if (top0 < 0 || top0 > a.pg.num_pages || top0 + given > a.pg.num_pages) bad |= LORA_KV_INVALID;
-    if (taken > top0 + given) bad |= LORA_KV_NO_PAGES;
-    if (tokens > a.out.max_tokens) bad |= LORA_KV_TOO_MANY;
-    const int32_t top = (int32_t)(top0 + given);
-
-    if (blockIdx.x > 0) {  // the maps of THREADS rows
-        const int32_t t = (blockIdx.x - 1) * THREADS + tid;
-        off[tid] = (int32_t)s.grown;
-        off_given[tid] = (int32_t)s.given;
-        off_tok[tid] = (int32_t)s.add;
-        had_s[tid] = q.had;
-        len_s[tid] = q.len;
-        __syncthreads();
-        if (t >= a.out.max_tokens) return;
-        if (bad || t >= tokens) {
-            plan_map_row(a, t, -1, -1, 0);
-            return;
-        }
-        const int r = last_at_most(off_tok, THREADS, t);
-        const int32_t pos = len_s[r] + (t - off_tok[r]), b = pos >> a.shift;
-        int32_t page;
-        if (b < had_s[r]) {
-            page = a.pg.block_table[(int64_t)r * a.pg.ld_table + b];
-        } else {
-            const int32_t k = top - 1 - (off[r] + b - had_s[r]);
-            if (k < top0) {
-                page = a.pg.free_pages[k];
-            } else {
-                const int e = last_at_most(off_given, THREADS, k - top0);
-                page = a.pg.block_table[(int64_t)e * a.pg.ld_table + (k - top0 - off_given[e])];
+    if (!a.move) return;
+    const int32_t first = blockIdx.x * THREADS + tid, step = gridDim.x * THREADS;
+    const int32_t given = bad ? 0 : (int32_t)s.all_given, taken = bad ? 0 : (int32_t)s.all_grown;
+    const int32_t rows = bad ? 0 : (int32_t)s.all_add, top = top0 + given;
+    auto page_given = [&](int32_t k) {  // k-th page of the ended requests
+        const int r = last_at_most(off_given, THREADS, k);
+        return a.pg.block_table[(int64_t)r * a.pg.ld_table + (k - off_given[r])];
+    };
+    auto page_taken = [&](int32_t k) {  // k-th page from the list's end
+        const int32_t at = top - 1 - k;
+        return at < top0 ? a.pg.free_pages[at] : page_given(at - top0);
+    };
+    // one line of items: token rows, pages taken, pages given back
+    const int64_t n_tok = a.out.max_tokens, n_all = n_tok + taken + given;
+    for (int64_t i = first; i < n_all; i += step) {
+        if (i < n_tok) {
+            const int32_t t = (int32_t)i;
+            if (t >= rows) {
+                plan_map_row(a, t, -1, -1, 0);
+                continue;
             }
+            const int r = last_at_most(off_tok, THREADS, t);
+            const int32_t pos = len_s[r] + (t - off_tok[r]), b = pos >> a.shift;
+            plan_map_row(a, t, r, pos, b < had_s[r] ? a.pg.block_table[(int64_t)r * a.pg.ld_table + b]
+                                                    : page_taken(off[r] + b - had_s[r]));
+        } else if (i < n_tok + taken) {
+            const int32_t k = (int32_t)(i - n_tok);
+            const int r = last_at_most(off, THREADS, k);
+            a.pg.block_table[(int64_t)r * a.pg.ld_table + had_s[r] + (k - off[r])] = page_taken(k);
+        } else {
+            const int32_t k = (int32_t)(i - n_tok - taken);
+            a.pg.free_pages[top0 + k] = page_given(k);
         }
-        plan_map_row(a, t, r, pos, page);
-        return;
     }
+}
 
-    if (tid == 0) {
-        a.out.status[0] = bad;
-        a.out.status[1] = (int32_t)min(tokens, (int64_t)INT32_MAX);
-        a.out.status[2] = (int32_t)min(taken, (int64_t)INT32_MAX);
-        a.out.status[3] = (int32_t)min(given, (int64_t)INT32_MAX);
-        a.out.free_top[0] = bad ? top0 : (int32_t)(top - taken);
-        a.out.q_ptr[n] = bad ? 0 : (int32_t)tokens;
+// The plan of more requests than one chunk holds, by one workgroup: totals and checks first,
+// then, a chunk at a time, the pages of ended requests onto the free list, and after all
+// of those the pages of growing ones off it.
+__global__ __launch_bounds__(kPlanThreads) void lora_kv_plan_chunks_kernel(PlanArgs a)
+{
+    constexpr int THREADS = kPlanThreads;
+    __shared__ uint4 wave_sums[THREADS / 64];
+    __shared__ int32_t off[THREADS], had_s[THREADS];
+    const int tid = threadIdx.x;
+    const int32_t n = a.pg.n_req;
+    const int32_t top0 = *a.pg.free_top;
+    PlanReq sum = plan_req(a, tid);
+    for (int32_t r = tid + THREADS; r < n; r += THREADS) {
+        const PlanReq x = plan_req(a, r);
+        sum.bad |= x.bad;
+        sum.given = __builtin_elementwise_add_sat(sum.given, x.given);
+        sum.grown = __builtin_elementwise_add_sat(sum.grown, x.grown);
+        sum.add = __builtin_elementwise_add_sat(sum.add, x.add);
     }
+    const PlanSums all = plan_scan<THREADS>(sum, wave_sums);
+    const int32_t bad = plan_check(a, all, top0);
+    __syncthreads();  // every thread has read the free top
+    if (tid == 0) plan_status(a, all, top0, bad);
     if (bad) {
         for (int32_t r = tid; r < n; r += THREADS) {
             a.out.kv_end[r] = a.kv_len[r];
             a.out.q_ptr[r] = 0;
         }
-        if (a.map_here)
-            for (int32_t t = tid; t < a.out.max_tokens; t += THREADS) plan_map_row(a, t, -1, -1, 0);
         return;
     }
-    // pages of ended requests go on top of the free list
-    if (given > 0) {
-        int32_t at = top0;
-        for (int32_t c = 0; c < n; c += THREADS) {
-            const PlanSums x = one ? s : plan_scan<THREADS>(plan_req(a, c + tid), wave_sums);
-            off_given[tid] = (int32_t)x.given;
-            __syncthreads();
-            const int32_t here = (int32_t)x.all_given;
-            for (int32_t k = tid; k < here; k += THREADS) {
-                const int i = last_at_most(off_given, THREADS, k);
-                a.pg.free_pages[at + k] = a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + (k - off_given[i])];
-            }
-            at += here;
-            __syncthreads();  // off_given, and below the list, are read by other threads
+    int32_t at = top0;
+    for (int32_t c = 0; c < n && all.all_given > 0; c += THREADS) {
+        const PlanSums s = plan_scan<THREADS>(plan_req(a, c + tid), wave_sums);
+        off[tid] = (int32_t)s.given;
+        __syncthreads();
+        const int32_t here = (int32_t)s.all_given;
+        for (int32_t k = tid; k < here; k += THREADS) {
+            const int i = last_at_most(off, THREADS, k);
+            a.pg.free_pages[at + k] = a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + (k - off[i])];
         }
+        at += here;
+        __syncthreads();  // off, and below the list, are read by other threads
     }
-    // growing requests and the token maps
-    int32_t at = top - 1, row0 = 0;
+    at -= 1;
+    int32_t row0 = 0;
     for (int32_t c = 0; c < n; c += THREADS) {
-        if (!one) {
-            q = plan_req(a, c + tid);
-            s = plan_scan<THREADS>(q, wave_sums);
-        }
-        const int32_t pages = (int32_t)s.all_grown, rows = (int32_t)s.all_add;
+        const PlanReq q = plan_req(a, c + tid);
+        const PlanSums s = plan_scan<THREADS>(q, wave_sums);
         off[tid] = (int32_t)s.grown;
         had_s[tid] = q.had;
-        off_tok[tid] = (int32_t)s.add;
-        len_s[tid] = q.len;
         if (c + tid < n) {
             a.out.q_ptr[c + tid] = row0 + (int32_t)s.add;
             a.out.kv_end[c + tid] = (int32_t)q.end;
         }
         __syncthreads();
-        for (int32_t k = tid; k < pages; k += THREADS) {
+        const int32_t here = (int32_t)s.all_grown;
+        for (int32_t k = tid; k < here; k += THREADS) {
             const int i = last_at_most(off, THREADS, k);
             a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + had_s[i] + (k - off[i])] = a.pg.free_pages[at - k];
         }
-        if (a.map_here) {
-            for (int32_t k = tid; k < rows; k += THREADS) {
-                const int i = last_at_most(off_tok, THREADS, k);
-                const int32_t pos = len_s[i] + (k - off_tok[i]), b = pos >> a.shift;
-                const int32_t page = b < had_s[i] ? a.pg.block_table[(int64_t)(c + i) * a.pg.ld_table + b]
-                                                  : a.pg.free_pages[at - (off[i] + b - had_s[i])];
-                plan_map_row(a, row0 + k, c + i, pos, page);
-            }
-        }
-        at -= pages;
-        row0 += rows;
+        at -= here;
+        row0 += (int32_t)s.all_add;
         __syncthreads();
     }
-    if (a.map_here)
-        for (int32_t t = row0 + tid; t < a.out.max_tokens; t += THREADS) plan_map_row(a, t, -1, -1, 0);
 }
 
-// Token maps of a step with many rows where the plan works in place or in several chunks:
-// one row per thread, from what the plan left: q_ptr (searched), kv_end and the table.
+// Token maps of a step planned in chunks, one row per thread, from what the plan left: q_ptr
+// (searched), kv_end and the table.
 __global__ __launch_bounds__(256) void lora_kv_maps_kernel(PlanArgs a)
 {
     const int32_t t = blockIdx.x * 256 + threadIdx.x;
@@ -1253,7 +1261,7 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
 {
     clear_error();
     if (!pages || !out) return fail(LORA_E_NULL, "pages and out are required");
-    PlanArgs a{*pages, *out, kv_len, new_len, req_slot, 0, 1};
+    PlanArgs a{*pages, *out, kv_len, new_len, req_slot, 0, 1, 1};
     a.shift = page_shift(pages->page_size);
     if (a.shift < 0)
         return fail(LORA_E_SHAPE, "page_size = %d is not a power of two in 1..%d", pages->page_size, LORA_KV_MAX_PAGE);
@@ -1271,20 +1279,37 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     if (out->max_tokens > 0 && (!out->tok_req || !out->tok_pos || !out->slots))
         return fail(LORA_E_NULL, "tok_req, tok_pos and slots are required");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // One workgroup up to kPlanMapsHere token rows; beyond that further workgroups for the
-    // maps, or a second launch where the plan works in place or in several chunks.
-    const bool in_place = out->kv_end == kv_len || out->free_top == pages->free_top;
-    a.map_here = out->max_tokens <= kPlanMapsHere;
-    if (!a.map_here && !in_place && pages->n_req <= kPlanThreads) {
-        const unsigned more = (unsigned)((out->max_tokens + (int64_t)kPlanThreads - 1) / kPlanThreads);
-        launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(1 + more), kPlanThreads, 0, s, a);
+    const int32_t n = pages->n_req;
+    if (n > kPlanThreads) {
+        launch_args(lora_kv_plan_chunks_kernel, dim3(1), kPlanThreads, 0, s, a);
+        if (out->max_tokens > 0)
+            launch_args(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
         return launch_status("step plan");
     }
-    if (a.map_here && pages->n_req <= 64 && out->max_tokens <= 256)
-        launch_args(lora_kv_plan_kernel<64>, dim3(1), 64, 0, s, a);
-    else
-        launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, s, a);
-    if (!a.map_here) launch_args(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
+    // The work there may be: every token row, and every page that the tables can hold.  Up to
+    // two of these a thread, since every workgroup makes its sums at the same time (1000
+    // requests moving 240,000 one-token pages: 125 us in one workgroup, 8.5 in 256).  A plan
+    // in place would need the second launch then; while its token rows are few, so most
+    // likely are its pages, and one workgroup is faster.
+    const int64_t moves = out->max_tokens + std::min<int64_t>(pages->num_pages, (int64_t)n * pages->max_blocks);
+    const bool in_place = out->kv_end == kv_len || out->free_top == pages->free_top;
+    const bool small = n <= 64 && moves <= 1024, medium = n <= 256;
+    const int threads = small ? 64 : medium ? 256 : kPlanThreads;
+    int64_t groups = std::min<int64_t>((moves + 2 * threads - 1) / (2 * threads), kPlanGroups);
+    if (small || (in_place && out->max_tokens <= kPlanThreads)) groups = 1;
+    a.move = 1;
+    a.finish = groups == 1 || !in_place;
+    auto go = [&](unsigned g) {
+        if (small) launch_args(lora_kv_plan_kernel<64>, dim3(g), 64, 0, s, a);
+        else if (medium) launch_args(lora_kv_plan_kernel<256>, dim3(g), 256, 0, s, a);
+        else launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(g), kPlanThreads, 0, s, a);
+    };
+    go((unsigned)std::max<int64_t>(groups, 1));
+    if (!a.finish) {
+        a.finish = 1;
+        a.move = 0;
+        go(1);
+    }
     return launch_status("step plan");
 }
 
@@ -1465,10 +1490,10 @@ int lora_residual_norm(void *stream, const lora_norm_args *args)
     if (a.reserved != 0) return fail(LORA_E_SHAPE, "reserved field must be 0");
     if (!(a.eps >= 0.f) || !std::isfinite(a.eps) || !std::isfinite(a.alpha) || !std::isfinite(a.w_offset))
         return fail(LORA_E_SHAPE, "eps = %g, alpha = %g, w_offset = %g", a.eps, a.alpha, a.w_offset);
+    if (a.n_rows == 0) return LORA_OK;  // whatever the pointers: an empty tensor's is NULL
     if (!a.y && !a.res_out) return fail(LORA_E_NULL, "y and res_out are both NULL");
     if (!a.x && (a.post_w || a.gate)) return fail(LORA_E_NULL, "post_w and gate need x");
     if (!a.gate && a.gate_idx) return fail(LORA_E_NULL, "gate_idx without gate");
-    if (a.n_rows == 0) return LORA_OK;
     if ((st = check_matrix(a.res, a.ldr, a.hidden, "res"))) return st;
     if (a.x && (st = check_matrix(a.x, a.ldx, a.hidden, "x"))) return st;
     if (a.y && (st = check_matrix(a.y, a.ldy, a.hidden, "y"))) return st;

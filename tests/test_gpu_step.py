@@ -97,6 +97,27 @@ def test_plan_equals_its_definition(n, page, seed):
     c.check(plan, want, "second call")
 
 
+@pytest.mark.parametrize("n,page,cap", [(61, 1, 6000), (300, 16, 40000), (700, 8, 60000), (1500, 4, 90000), (40, 16, 900)])
+@pytest.mark.parametrize("fits", [True, False])
+def test_plan_in_place_equals_its_definition(n, page, cap, fits):
+    """kv_end is kv_len and the free top is updated where it is read, in steps of every size."""
+    say(f"case plan-in-place n={n} page={page} cap={cap} fits={fits}")
+    kv, new = _mixed(n, n, page, most=100)
+    c = PlanCase(kv, new, page, max_blocks=-(-300 // page), spare=3, seed=n, max_tokens=cap if fits else 30)
+    plan = S.KVPlan(n, c.max_tokens, kv_end=c.dev_kv, free_top=c.dev_top)
+    want = c.want()
+    assert (want["status"][0] == 0) == fits
+    S.lora_kv_plan(plan, c.pages, c.dev_kv, c.dev_new, req_slot=c.dev_slot)
+    c.check(plan, want, "in place")
+    kv2 = [k if k < 150 else 5 for k in want["kv_end"]]          # and a second step from there
+    if fits and kv2 == want["kv_end"]:
+        new2 = [1 if i % 3 else 0 for i in range(n)]
+        want2 = R.plan(kv2, new2, want["table"], want["free"], want["free_top"], page, cap, c.req_slot)
+        c.dev_new.copy_(ints(new2))
+        S.lora_kv_plan(plan, c.pages, c.dev_kv, c.dev_new, req_slot=c.dev_slot)
+        c.check(plan, want2, "second step")
+
+
 @pytest.mark.parametrize("kv,new,page,max_tokens", [
     ([], [], 16, 5), ([0], [0], 16, 0), ([0], [0], 16, 4), ([0, 0], [1, 0], 1, 1), ([5], [-1], 4, 2),
     ([0] * 7, [-1] * 7, 8, 3), ([16], [16], 16, 16), ([4095], [1], 16, 4096), ([0, 3], [5000, 1], 16, 5100),
@@ -514,6 +535,67 @@ def test_attention_small_weights_add_up():
         c.check(out, lse, c.want(), str(dt))
 
 
+def test_attention_subnormal_keys_and_values():
+    """fp16 keys and values below 2^-14 (its subnormals) count like any others."""
+    say("case attention-subnormal")
+    c = AttnCase([300, 5], 4, 2, 64, 16, F16, seed=12)
+    c.cache.v.mul_(2.0 ** -16)
+    c.cache.k.mul_(2.0 ** -17)
+    c.q = (c.q.float() * 2000).to(F16)          # scores of a few units from subnormal keys
+    c.cache.k[c.cache.k.isnan()] = 0.0
+    c.cache.v[c.cache.v.isnan()] = 0.0
+    out, lse = c.run(scale=2.0)
+    want = c.want(scale=2.0)
+    assert float(want[0][0].abs().max()) < 2.0 ** -14 and float(want[0][1].abs().max()) > 0.5
+    c.check(out, lse, want, "subnormal")
+
+
+def test_attention_reads_a_table_of_wider_rows():
+    say("case attention-wide-table")
+    c = AttnCase([100, 37, 64], 4, 2, 64, 16, F16, seed=13)
+    n, wide = 3, torch.full((3, c.table.shape[1] + 9), 10 ** 9, dtype=torch.int32, device="cuda")
+    wide[:, 4:4 + c.table.shape[1]] = c.table.cuda()
+    view = wide[:, 4:4 + c.table.shape[1]]
+    out, lse = torch.empty(n, 4 * 64, dtype=F16, device="cuda"), torch.empty(n, 4, device="cuda")
+    S.lora_paged_attention(out, c.q.cuda(), c.cache, view, ints(c.lens), S.attention_workspace(n, 4, c.cache), lse=lse)
+    torch.cuda.synchronize()
+    for i, w in enumerate(c.want()):
+        close(out[i].view(4, 64), w[0], w[2], f"row {i}")
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that run at the same time, each split over many workgroups."""
+    say("case attention-two-streams")
+    cases = [AttnCase([20000, 3, 900], 8, 1, 128, 16, F16, seed=20 + i) for i in range(2)]
+    alone = [tuple(t.clone() for t in c.run()) for c in cases]
+    streams, args, outs = [torch.cuda.Stream() for _ in cases], [], []
+    for c in cases:
+        outs.append((torch.zeros(3, 8 * 128, dtype=F16, device="cuda"), torch.zeros(3, 8, device="cuda")))
+        args.append((c.q.cuda(), c.cache, c.table.cuda(), ints(c.lens), S.attention_workspace(3, 8, c.cache)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (o, l), a in zip(streams, outs, args):
+            with torch.cuda.stream(st):
+                S.lora_paged_attention(o, *a, lse=l)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl), a in zip(outs, alone, args):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+        assert not a[4][:2 * (4 * 256 + 4096)].any(), "counters are zero again"
+
+
+def test_calls_on_no_rows():
+    say("case no-rows")
+    cache = _cache(2, 16, 2, 64, F16, "token", 1)
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    e = lambda c: torch.empty(0, c, dtype=F16, device="cuda")
+    S.lora_paged_attention(e(256), e(256), cache, ints([[0]]), ints([]), S.attention_workspace(0, 4, cache))
+    S.lora_rope_append(e(256), e(256), e(128), e(128), cache, ints([]), rope=S.Rope.base(64),
+                       positions=torch.empty(1, 0, dtype=torch.int32, device="cuda"))
+    S.lora_residual_norm(e(64), e(64), torch.ones(64, dtype=F16, device="cuda"), x=e(64), res_out=e(64))
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
+
+
 def test_attention_workspace_is_left_clean_and_may_be_shared():
     say("case attention-workspace")
     big = AttnCase([9000, 3, 0, 512], 8, 1, 128, 16, F16, seed=1)
@@ -638,6 +720,35 @@ def test_norm_of_zeros_and_large_rows():
         S.lora_residual_norm(y, res.cuda(), w.cuda())
         _, wy, _, by = R.residual_norm(res, None, w, None, None, None, 1.0, 1e-5, 0.0)
         close(y, wy, by + R.half_step(dt) * wy.abs() + R.tiny(dt), str(dt))
+
+
+def test_norm_beyond_32_bit_offsets():
+    say("case norm-far-rows")
+    h, ld = 64, (1 << 30) + 72
+    flat = [torch.empty(2 * ld + h, dtype=F16, device="cuda") for _ in range(2)]
+    res, y = (f.as_strided((3, h), (ld, 1)) for f in flat)
+    vals = torch.randn(3, h).half()
+    res.copy_(vals)
+    y.zero_()
+    w = torch.ones(h, dtype=F16)
+    S.lora_residual_norm(y, res, w.cuda())
+    torch.cuda.synchronize()
+    _, wy, _, by = R.residual_norm(vals, None, w, None, None, None, 1.0, 1e-5, 0.0)
+    close(y, wy, by + R.half_step(F16) * wy.abs() + R.tiny(F16), "y")
+
+
+def test_launch_events_time_these_calls_too():
+    say("case launch-events")
+    res, w = torch.randn(4000, 4096, device="cuda").half(), torch.ones(4096, dtype=F16, device="cuda")
+    y = torch.empty_like(res)
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    e1.record()
+    torch.cuda.synchronize()
+    B.lora_set_launch_events(e0.cuda_event, e1.cuda_event)
+    S.lora_residual_norm(y, res, w)
+    torch.cuda.synchronize()
+    assert 0.0 < e0.elapsed_time(e1) < 50.0
 
 
 # ------------------------------------------------------------------ streams
