@@ -14,7 +14,8 @@
  * returned (lora_last_error() describes it).  Device-resident metadata (lengths, slots,
  * page ids) is read without a host check, and an entry outside its documented range
  * makes its row, token or page a no-op instead of an out-of-bounds access.  Every call
- * may be captured into a graph and replayed with new metadata in the same arrays.
+ * may be captured into a graph and replayed with new metadata in the same arrays.  The
+ * diagnostics of lora_sgmv.h (launch events, plans) apply to the add-on's launches only.
  *
  * Types: `type` is LORA_TYPE_F16 (IEEE binary16) or LORA_TYPE_BF16 for all 16-bit data
  * of a call.  Arithmetic is fp32 (sums, softmax statistics, norms), angles are 64-bit;

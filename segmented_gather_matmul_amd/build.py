@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "liblora_sgmv.so")
 SOURCES = [os.path.join(CSRC, "lora_kernels.hip"), os.path.join(CSRC, "lora_pool.hip"),
            os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_host.cpp")]
 HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(INCLUDE, "lora_step.h"),
-           os.path.join(CSRC, "lora_internal.hpp"), os.path.join(CSRC, "lora_launch.hpp")]
+           os.path.join(CSRC, "lora_internal.hpp")]
 ARCH = "gfx950"
 
 

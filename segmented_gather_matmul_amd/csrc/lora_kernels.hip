@@ -39,12 +39,14 @@
 //     move in whole lines, and nothing passes through LDS.
 // The per-row and the segment forms of decode batches also run both steps in one launch,
 // the shrink's workgroups handing v to the expand's (lora_handoff_kernel).
+#include <hip/hip_ext.h>
+#include <hip/hip_runtime.h>
+
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
 
 #include "lora_internal.hpp"
-#include "lora_launch.hpp"
 
 // No floating-point contraction anywhere in the kernels: whether the compiler fused a
 // multiply and an add (or rounded an fp32 product straight to fp16) depended on the
@@ -1892,6 +1894,9 @@ __global__ __launch_bounds__(kThreads) void lora_handoff_kernel(const void *__re
 }
 
 // ------------------------------------------------------------------------ launchers
+// Event pair attached to this thread's next kernel launch (lora_set_launch_events).
+thread_local hipEvent_t t_ev_start = nullptr, t_ev_stop = nullptr;
+
 // Set by lora_set_stream_weights for the calling thread: the per-row calls' rows use
 // distinct adapters, so their dense weights are read with streaming loads.
 thread_local int32_t t_stream_w = 0;
@@ -1901,13 +1906,27 @@ template <typename Kernel>
 void launch_pre(Kernel kernel, dim3 grid, int threads, size_t lds, hipStream_t s, const void *src, int32_t n0,
                 int32_t n1, int32_t n2, const Args &a)
 {
-    launch_args(kernel, grid, threads, lds, s, src, n0, n1, n2, a);
+    const dim3 block(threads);
+    if (t_ev_start || t_ev_stop) {
+        hipEvent_t e0 = t_ev_start, e1 = t_ev_stop;
+        t_ev_start = t_ev_stop = nullptr;
+        hipExtLaunchKernelGGL(kernel, grid, block, lds, s, e0, e1, 0, src, n0, n1, n2, a);
+    } else {
+        hipLaunchKernelGGL(kernel, grid, block, lds, s, src, n0, n1, n2, a);
+    }
 }
 
 template <typename Kernel>
 void launch(Kernel kernel, dim3 grid, int threads, size_t lds, hipStream_t s, const Args &a)
 {
-    launch_args(kernel, grid, threads, lds, s, a);
+    const dim3 block(threads);
+    if (t_ev_start || t_ev_stop) {
+        hipEvent_t e0 = t_ev_start, e1 = t_ev_stop;
+        t_ev_start = t_ev_stop = nullptr;
+        hipExtLaunchKernelGGL(kernel, grid, block, lds, s, e0, e1, 0, a);
+    } else {
+        hipLaunchKernelGGL(kernel, grid, block, lds, s, a);
+    }
 }
 
 WeightsDev to_dev(const lora_weights *w)
@@ -1929,6 +1948,13 @@ WeightsDev to_dev(const lora_weights *w)
     d.a_pt_off = w->a_pt_off;
     d.b_pt_off = w->b_pt_off;
     return d;
+}
+
+int launch_status(const char *what)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(LORA_E_HIP, "%s: launch failed: %s", what, hipGetErrorString(e));
+    return LORA_OK;
 }
 
 int check_rows_arg(const void *p, int64_t ld, int32_t need, int32_t mult, const char *name)
@@ -2311,7 +2337,6 @@ lora_proj one_proj(const lora_weights *w, float *v, int64_t ldv, void *y, int64_
 }  // namespace
 
 thread_local int32_t t_plan_jw = 0, t_plan_nr = 0;
-thread_local hipEvent_t t_ev_start = nullptr, t_ev_stop = nullptr;
 
 int32_t plan_shrink_jw(int32_t work_tiles, int32_t r_max)
 {

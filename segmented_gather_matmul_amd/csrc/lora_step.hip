@@ -1,11 +1,13 @@
 // HIP kernels (gfx950 / CDNA4) and launchers of the decode-step operators beside the
 // add-on: the step plan, rotary positions with the append to the paged cache, attention
 // over that cache, and the residual add with its norms (lora_step.h).
+#include <hip/hip_runtime.h>
+
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
 
-#include "lora_launch.hpp"
+#include "lora_internal.hpp"
 #include "lora_step.h"
 
 // As in the add-on's kernels, every fused multiply-add is an explicit __builtin_fmaf.
@@ -15,6 +17,20 @@ namespace lora {
 namespace {
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------------ launching
+template <typename Kernel, typename... A>
+void launch(Kernel kernel, dim3 grid, int threads, size_t lds, hipStream_t s, const A &...a)
+{
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), lds, s, a...);
+}
+
+int launch_status(const char *what)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(LORA_E_HIP, "%s: launch failed: %s", what, hipGetErrorString(e));
+    return LORA_OK;
+}
 
 // ------------------------------------------------------------------------ 16-bit data
 struct F16 {
@@ -1079,8 +1095,8 @@ void attention_launch(const AttnArgs &a, dim3 grid, hipStream_t s)
 {
     const int D = a.head_dim;
 #define LORA_ATTN(DP)                                                                                         \
-    (D == DP ? launch_args(lora_paged_attention_kernel<T, DP, true>, grid, 64 * kAttnWaves, 0, s, a)          \
-             : launch_args(lora_paged_attention_kernel<T, DP, false>, grid, 64 * kAttnWaves, 0, s, a))
+    (D == DP ? launch(lora_paged_attention_kernel<T, DP, true>, grid, 64 * kAttnWaves, 0, s, a)          \
+             : launch(lora_paged_attention_kernel<T, DP, false>, grid, 64 * kAttnWaves, 0, s, a))
     if (D <= 64) LORA_ATTN(64);
     else if (D <= 96) LORA_ATTN(96);
     else if (D <= 128) LORA_ATTN(128);
@@ -1281,9 +1297,9 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int32_t n = pages->n_req;
     if (n > kPlanThreads) {
-        launch_args(lora_kv_plan_chunks_kernel, dim3(1), kPlanThreads, 0, s, a);
+        launch(lora_kv_plan_chunks_kernel, dim3(1), kPlanThreads, 0, s, a);
         if (out->max_tokens > 0)
-            launch_args(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
+            launch(lora_kv_maps_kernel, dim3((unsigned)((out->max_tokens + 255ll) / 256)), 256, 0, s, a);
         return launch_status("step plan");
     }
     // The work there may be: every token row, and every page that the tables can hold.  Up to
@@ -1300,9 +1316,9 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     a.move = 1;
     a.finish = groups == 1 || !in_place;
     auto go = [&](unsigned g) {
-        if (small) launch_args(lora_kv_plan_kernel<64>, dim3(g), 64, 0, s, a);
-        else if (medium) launch_args(lora_kv_plan_kernel<256>, dim3(g), 256, 0, s, a);
-        else launch_args(lora_kv_plan_kernel<kPlanThreads>, dim3(g), kPlanThreads, 0, s, a);
+        if (small) launch(lora_kv_plan_kernel<64>, dim3(g), 64, 0, s, a);
+        else if (medium) launch(lora_kv_plan_kernel<256>, dim3(g), 256, 0, s, a);
+        else launch(lora_kv_plan_kernel<kPlanThreads>, dim3(g), kPlanThreads, 0, s, a);
     };
     go((unsigned)std::max<int64_t>(groups, 1));
     if (!a.finish) {
@@ -1382,8 +1398,8 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
     const int64_t blocks = n_rows < kAppendFill ? std::min<int64_t>((units + 255) / 256, 64) : 1;
     const dim3 grid((unsigned)n_rows, (unsigned)blocks);
 #define LORA_APPEND(T, INTER)                                                                      \
-    (stream_out ? launch_args(lora_rope_append_kernel<T, INTER, true>, grid, 256, 0, s, a)         \
-                : launch_args(lora_rope_append_kernel<T, INTER, false>, grid, 256, 0, s, a))
+    (stream_out ? launch(lora_rope_append_kernel<T, INTER, true>, grid, 256, 0, s, a)         \
+                : launch(lora_rope_append_kernel<T, INTER, false>, grid, 256, 0, s, a))
     if (rope->interleaved) {
         if (bf) LORA_APPEND(BF16, true);
         else LORA_APPEND(F16, true);
@@ -1523,8 +1539,8 @@ int lora_residual_norm(void *stream, const lora_norm_args *args)
     const dim3 grid((unsigned)a.n_rows);
     const bool bf = a.type == LORA_TYPE_BF16;
 #define LORA_NORM_T(T, NC)                                                                        \
-    (stream_out ? launch_args(lora_residual_norm_kernel<T, NC, true>, grid, threads, 0, s, a)      \
-                : launch_args(lora_residual_norm_kernel<T, NC, false>, grid, threads, 0, s, a))
+    (stream_out ? launch(lora_residual_norm_kernel<T, NC, true>, grid, threads, 0, s, a)      \
+                : launch(lora_residual_norm_kernel<T, NC, false>, grid, threads, 0, s, a))
 #define LORA_NORM(NC) (bf ? LORA_NORM_T(BF16, NC) : LORA_NORM_T(F16, NC))
     if (nc <= 1) LORA_NORM(1);
     else if (nc <= 2) LORA_NORM(2);

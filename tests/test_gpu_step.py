@@ -737,20 +737,6 @@ def test_norm_beyond_32_bit_offsets():
     close(y, wy, by + R.half_step(F16) * wy.abs() + R.tiny(F16), "y")
 
 
-def test_launch_events_time_these_calls_too():
-    say("case launch-events")
-    res, w = torch.randn(4000, 4096, device="cuda").half(), torch.ones(4096, dtype=F16, device="cuda")
-    y = torch.empty_like(res)
-    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-    e0.record()
-    e1.record()
-    torch.cuda.synchronize()
-    B.lora_set_launch_events(e0.cuda_event, e1.cuda_event)
-    S.lora_residual_norm(y, res, w)
-    torch.cuda.synchronize()
-    assert 0.0 < e0.elapsed_time(e1) < 50.0
-
-
 # ------------------------------------------------------------------ streams
 def test_calls_on_a_side_stream():
     say("case side-stream")
