@@ -529,7 +529,7 @@ struct AttnArgs {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kAttnWaves = 4;        // wavefronts of an attention workgroup
 constexpr int kAttnTile = 32;        // tokens a wavefront takes at a time
-constexpr int kAttnMinShare = 16;    // tiles a workgroup takes at least
+constexpr int kAttnMinShare = 4;     // tiles a workgroup takes at least: one per wavefront
 constexpr int kAttnRowTiles = 4;     // what starting and finishing a row costs, in tiles
 constexpr int kAttnJoin = 16;        // parts joined at a time
 constexpr int kAttnMaxTiles = 4096;  // key/value heads x 16-head tiles of one launch
