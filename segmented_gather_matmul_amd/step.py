@@ -74,18 +74,20 @@ def _type(t, what):
     return ty
 
 
+# Every call checks every tensor; the checks that hold are made by a small compiled module
+# (a tenth of a microsecond each).  Where it has not been built, or one does not hold, the
+# same rules below are gone through in Python, which say what is wrong.
+try:
+    from . import _step_args as _fast
+except ImportError:
+    _fast = None
+_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int32: 3}
+
+
 def _matrix(t, what, dtype, rows, cols):
     """t: 2-D, of `dtype`, unit column stride, >= rows rows and >= cols columns; its row stride."""
-    try:
-        n, c = t.shape
-        if t.dtype is dtype and n >= rows and c == cols and t.is_contiguous() and (n > 1 or c % 8 == 0):
-            return c
-        ld, sc = t.stride()
-        if t.dtype is dtype and n >= rows and c >= cols and sc == 1 and ld >= cols and (n > 1 or ld % 8 == 0):
-            return ld
-    except (AttributeError, TypeError, ValueError):
-        pass
-    return _matrix_checked(t, what, dtype, rows, cols)
+    ld = _fast.matrix(t, _CODES[dtype], rows, cols) if _fast else -1
+    return ld if ld >= 0 else _matrix_checked(t, what, dtype, rows, cols)
 
 
 def _matrix_checked(t, what, dtype, rows, cols):
@@ -110,29 +112,23 @@ def _matrix_checked(t, what, dtype, rows, cols):
 
 def _vector(t, what, dtype, n):
     """t: contiguous, of `dtype`, at least n elements."""
-    try:
-        if t.dtype is dtype and t.is_contiguous() and t.numel() >= n:
-            return
-    except AttributeError:
-        pass
+    if _fast and _fast.vector(t, _CODES[dtype], n):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{what} must be a tensor (got {type(t).__name__})")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must have dtype {_NAMES[dtype]} (got {t.dtype})")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    raise ValueError(f"{what} has {t.numel()} elements, needs at least {n}")
+    if t.numel() < n:
+        raise ValueError(f"{what} has {t.numel()} elements, needs at least {n}")
 
 
 def _here(names, *tensors):
     """Every tensor (None: not given) is on the current GPU; its index."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            break
-    else:
-        if dev >= 0 and dev == torch.cuda.current_device():
-            return dev
+    dev = _fast.here(*tensors) if _fast else -1
+    if dev >= 0 and dev == torch.cuda.current_device():
+        return dev
     for what, t in zip(names.split(), tensors):
         if t is not None and not t.is_cuda:
             raise ValueError(f"{what} must be a GPU tensor (got device {t.device})")
@@ -140,6 +136,7 @@ def _here(names, *tensors):
     for what, t in zip(names.split(), tensors):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _call(name, *args):

@@ -209,6 +209,44 @@ def test_binding_rejects_wrong_tensors():
             nrm(**k)
 
 
+def test_compiled_checks_agree_with_the_python_ones():
+    """What the compiled module accepts, the rules in Python accept with the same answer; what
+    they refuse, it refuses (it may leave odd cases to them)."""
+    assert S._fast is not None, "the module is built with the library"
+    base = torch.zeros(6, 40, dtype=torch.float16)
+    tensors = [base, base[:, :24], base[:, 8:32], base[1:2], base[:1, :17], base[:0], base[:, :0], base.t(), base[::2],
+               base[:, ::2], base[0], base.view(2, 3, 40), base.float(), base.bfloat16(), base.int(), base.expand(6, 40),
+               base[:1].expand(6, 40), torch.zeros(40, dtype=torch.float16)[None], torch.zeros(3, 1, dtype=torch.float16),
+               None, 5, "q", [1.0]]
+    agreed = 0
+    for t in tensors:
+        for dt in S._CODES:
+            for rows, cols in ((0, 0), (1, 17), (2, 24), (6, 40), (7, 40), (6, 41), (1, 1)):
+                ld = S._fast.matrix(t, S._CODES[dt], rows, cols)
+                try:
+                    want = S._matrix_checked(t, "t", dt, rows, cols)
+                except ValueError:
+                    want = None
+                if ld >= 0:
+                    assert want == ld, (getattr(t, "shape", t), dt, rows, cols)
+                    agreed += 1
+                elif want is not None:
+                    assert t.shape[0] < 2 or t.numel() == 0, "only rows without a meaningful stride are left to Python"
+            for n in (0, 1, 40, 240, 241):
+                fast, held = S._fast.vector(t, S._CODES[dt], n), S._fast
+                try:
+                    S._fast = None
+                    S._vector(t, "t", dt, n)
+                    ok = True
+                except ValueError:
+                    ok = False
+                finally:
+                    S._fast = held
+                assert fast == ok, (getattr(t, "shape", t), dt, n)
+    assert agreed > 20
+    assert S._fast.here(base, None, base) == -1 and S._fast.here(base, 5) == -1
+
+
 def test_descriptors_reject_wrong_layouts():
     h = torch.float16
     k = torch.zeros(4, 16, 2, 64, dtype=h)
