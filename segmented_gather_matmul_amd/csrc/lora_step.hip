@@ -414,12 +414,11 @@ __device__ inline float2 turn_of(int32_t pos, float inv_freq)
     const double part = __builtin_fma(p, kHi, -whole) + __builtin_fma(p, kLo, e * kHi);
     const float half_turns = (float)(2.0 * part);
     float2 cs;
-    cs.y = sinpif(half_turns);
-    cs.x = cospif(half_turns);
+    sincospif(half_turns, &cs.y, &cs.x);
     return cs;
 }
 
-// Workgroups of 256 threads: blockIdx.x is the token row, and the row's units go round over
+// Workgroups of up to 256 threads: blockIdx.x is the token row, and the row's units go round over
 // the threads of its gridDim.y workgroups.  A unit moves one 16-byte chunk, or the two
 // chunks x[i..], x[i + rot/2..] whose elements turn together (interleaved, one chunk holds
 // whole pairs).  A thread asks for its first chunks first; while they are on their way, the
@@ -434,52 +433,53 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
     __shared__ float2 cs[LORA_KV_MAX_HEAD_DIM / 2];
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x;
-    const int32_t slot = a.slots[t];
-    if (slot < 0 || slot >= (int64_t)a.c.num_pages << a.shift) return;
+    const int32_t slot = a.slots[t];  // waited for only where something is stored
     const int half = a.rot / 2;
-    const int64_t cell = (int64_t)(slot >> a.shift) * a.c.page_stride +
-                         (int64_t)(slot & ((1 << a.shift) - 1)) * a.c.token_stride;
     const int n_qk = (a.q_heads + a.kv_heads) * a.units_rot;
     const int n_all = n_qk + a.kv_heads * a.units_v;
-    // a unit's addresses; turn: first of its frequencies, -1: its chunk passes through
+    enum { kQ, kK, kV };
     struct Unit {
-        const void *src;
-        void *dst;
-        int64_t from, to;
-        int turn;
+        int what, head, col;  // its (first) chunk
+        int turn;             // first of its frequencies, -1: its chunk passes through
     };
     auto unit_of = [&](int u) {
         if (u >= n_qk) {
-            const int h = (u - n_qk) / a.units_v, c = (u - n_qk) - h * a.units_v;
-            return Unit{a.v, a.c.v, t * a.ldv + (int64_t)h * a.head_dim + 8 * c, cell + h * a.c.head_stride + 8 * c, -1};
+            const int h = (u - n_qk) / a.units_v;
+            return Unit{kV, h, 8 * (u - n_qk - h * a.units_v), -1};
         }
-        int h = u / a.units_rot;
+        const int h = u / a.units_rot;
         int d = 8 * (u - h * a.units_rot), turn = -1;
-        const bool is_q = h < a.q_heads;
         if (INTER) turn = d < a.rot ? d / 2 : -1;
         else if (d < half) turn = d;
         else d += half;  // the chunks behind the pairs
-        if (!is_q) h -= a.q_heads;
-        return Unit{is_q ? a.q : a.k, is_q ? a.q_out : a.c.k, t * (is_q ? a.ldq : a.ldk) + (int64_t)h * a.head_dim + d,
-                    is_q ? t * a.ldqo + (int64_t)h * a.head_dim + d : cell + h * a.c.head_stride + d, turn};
+        return h < a.q_heads ? Unit{kQ, h, d, turn} : Unit{kK, h - a.q_heads, d, turn};
     };
-    int u = blockIdx.y * 256 + tid;
+    const int step = blockDim.x * gridDim.y;
+    int u = blockIdx.y * blockDim.x + tid;
     Unit un{};
     uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
     auto fetch = [&]() {
         un = unit_of(u);
-        ra = load16(un.src, un.from);
-        if (!INTER && un.turn >= 0) rb = load16(un.src, un.from + half);
+        const void *src = un.what == kQ ? a.q : un.what == kK ? a.k : a.v;
+        const int64_t ld = un.what == kQ ? a.ldq : un.what == kK ? a.ldk : a.ldv;
+        const int64_t from = t * ld + (int64_t)un.head * a.head_dim + un.col;
+        ra = load16(src, from);
+        if (!INTER && un.turn >= 0) rb = load16(src, from + half);
     };
     if (u < n_all) fetch();
-    for (int i = tid; i < half; i += 256) {
+    for (int i = tid; i < half; i += blockDim.x) {
         const int ax = a.axis ? a.axis[i] : 0;
         cs[i] = ax >= 0 && ax < a.n_axes ? turn_of(a.pos[ax * a.ld_pos + t], a.inv_freq[i]) : make_float2(1.f, 0.f);
     }
+    if (slot < 0 || slot >= (int64_t)a.c.num_pages << a.shift) return;
+    const int64_t cell = (int64_t)(slot >> a.shift) * a.c.page_stride +
+                         (int64_t)(slot & ((1 << a.shift) - 1)) * a.c.token_stride;
     __syncthreads();
     while (u < n_all) {
+        void *const dst = un.what == kQ ? a.q_out : un.what == kK ? a.c.k : a.c.v;
+        const int64_t to = (un.what == kQ ? t * a.ldqo + (int64_t)un.head * a.head_dim : cell + un.head * a.c.head_stride) + un.col;
         if (un.turn < 0) {
-            store16<STREAM>(un.dst, un.to, ra);
+            store16<STREAM>(dst, to, ra);
         } else {
             float x[8], y[8];
             unpack8<T>(ra, x);
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
                     y[2 * e] = __builtin_fmaf(x[2 * e], w.x, -(x[2 * e + 1] * w.y));
                     y[2 * e + 1] = __builtin_fmaf(x[2 * e], w.y, x[2 * e + 1] * w.x);
                 }
-                store16<STREAM>(un.dst, un.to, pack8<T>(y));
+                store16<STREAM>(dst, to, pack8<T>(y));
             } else {
                 float b[8], z[8];
                 unpack8<T>(rb, b);
@@ -500,11 +500,11 @@ __global__ __launch_bounds__(256) void lora_rope_append_kernel(AppendArgs a)
                     y[e] = __builtin_fmaf(x[e], w.x, -(b[e] * w.y));
                     z[e] = __builtin_fmaf(x[e], w.y, b[e] * w.x);
                 }
-                store16<STREAM>(un.dst, un.to, pack8<T>(y));
-                store16<STREAM>(un.dst, un.to + half, pack8<T>(z));
+                store16<STREAM>(dst, to, pack8<T>(y));
+                store16<STREAM>(dst, to + half, pack8<T>(z));
             }
         }
-        u += 256 * gridDim.y;
+        u += step;
         if (u < n_all) fetch();
     }
 }
@@ -1408,9 +1408,11 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
     // units (32 rows of the 7B shape: 4.4 us against 3.0).
     const int64_t blocks = n_rows < kAppendFill ? std::min<int64_t>((units + 255) / 256, 64) : 1;
     const dim3 grid((unsigned)n_rows, (unsigned)blocks);
+    // a row of few units (one GPU's shard of 64/8 heads has 88) in as few wavefronts
+    const int threads = (int)std::min<int64_t>((units + 63) / 64 * 64, 256);
 #define LORA_APPEND(T, INTER)                                                                      \
-    (stream_out ? launch(lora_rope_append_kernel<T, INTER, true>, grid, 256, 0, s, a)         \
-                : launch(lora_rope_append_kernel<T, INTER, false>, grid, 256, 0, s, a))
+    (stream_out ? launch(lora_rope_append_kernel<T, INTER, true>, grid, threads, 0, s, a)         \
+                : launch(lora_rope_append_kernel<T, INTER, false>, grid, threads, 0, s, a))
     if (rope->interleaved) {
         if (bf) LORA_APPEND(BF16, true);
         else LORA_APPEND(F16, true);
