@@ -1141,23 +1141,31 @@ lora_residual_norm_kernel(lora_norm_args a)
     const int tid = threadIdx.x, nt = blockDim.x;
     const int64_t row = blockIdx.x;
     const int chunks = a.hidden / 8;
-    int32_t gi = -1;
-    if (a.gate) {
-        gi = a.gate_idx ? a.gate_idx[row] : 0;
-        if (gi < -1 || gi >= a.n_gates) return;
-    }
-    // everything is asked for before anything waits
+    // Everything is asked for before anything waits; of the longest rows, which fill the
+    // registers, x and res only.
+    constexpr bool kEarly = NC <= 4;
+    constexpr int NE = kEarly ? NC : 1;
+    const int32_t gi = a.gate ? a.gate_idx ? a.gate_idx[row] : 0 : -1;
     const uint4 zero4 = make_uint4(0, 0, 0, 0);
-    uint4 res[NC], x[NC], pw[NC], gate[NC], w[NC];
+    uint4 res[NC], x[NC], pw[NE], gate[NE], w[NE];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = tid + i * nt;
         const bool in = c < chunks;
         res[i] = in ? load16(a.res, row * a.ldr + 8 * c) : zero4;
         x[i] = a.x && in ? load16(a.x, row * a.ldx + 8 * c) : zero4;
-        pw[i] = a.post_w && in ? load16(a.post_w, 8 * c) : zero4;
-        gate[i] = gi >= 0 && in ? load16(a.gate, gi * a.ldg + 8 * c) : zero4;
-        w[i] = a.y && in ? load16(a.w, 8 * c) : zero4;
+        if (kEarly) {
+            pw[i] = a.post_w && in ? load16(a.post_w, 8 * c) : zero4;
+            w[i] = a.y && in ? load16(a.w, 8 * c) : zero4;
+        }
+    }
+    if (gi < -1 || gi >= max(a.n_gates, 1)) return;
+    if (kEarly) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int c = tid + i * nt;
+            gate[i] = gi >= 0 && c < chunks ? load16(a.gate, gi * a.ldg + 8 * c) : zero4;
+        }
     }
     float h[NC][8], p[NC][8];
 #pragma unroll
@@ -1174,8 +1182,10 @@ lora_residual_norm_kernel(lora_norm_args a)
         const float inv = 1.f / __builtin_sqrtf(block_sum(ss, wave_sums) / (float)a.hidden + a.eps);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
+            const int c = tid + i * nt;
+            if (c >= chunks) continue;
             float f[8];
-            unpack8<T>(pw[i], f);
+            unpack8<T>(kEarly ? pw[i % NE] : load16(a.post_w, 8 * c), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[i][e] = p[i][e] * inv * (f[e] + a.w_offset);
         }
@@ -1187,7 +1197,7 @@ lora_residual_norm_kernel(lora_norm_args a)
         if (c >= chunks) continue;
         if (gi >= 0) {
             float g[8];
-            unpack8<T>(gate[i], g);
+            unpack8<T>(kEarly ? gate[i % NE] : load16(a.gate, gi * a.ldg + 8 * c), g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[i][e] *= g[e];
         }
@@ -1205,7 +1215,7 @@ lora_residual_norm_kernel(lora_norm_args a)
         const int c = tid + i * nt;
         if (c >= chunks) continue;
         float f[8], y[8];
-        unpack8<T>(w[i], f);
+        unpack8<T>(kEarly ? w[i % NE] : load16(a.w, 8 * c), f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = h[i][e] * inv * (f[e] + a.w_offset);
         store16<STREAM>(a.y, row * a.ldy + 8 * c, pack8<T>(y));
