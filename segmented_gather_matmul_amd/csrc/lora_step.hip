@@ -859,8 +859,17 @@ lora_paged_attention_kernel(AttnArgs a)
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int per_share = a.kv_heads * a.head_tiles;
-    const int32_t wg = blockIdx.x / per_share, rest = blockIdx.x - wg * per_share;
-    const int kvh = rest / a.head_tiles, ht = rest - kvh * a.head_tiles;
+    // The head tiles of one share and key/value head follow each other on one XCD (workgroups
+    // go to the 8 XCDs in turn), so that its L2 serves K and V to all but the first.
+    // (32 rows of 4000 tokens, 64/1 heads: 49 us without, 42 so.)
+    int32_t pair = blockIdx.x, ht = 0;
+    if (a.head_tiles > 1) {
+        const int32_t eight = blockIdx.x / (8 * a.head_tiles);
+        ht = blockIdx.x / 8 - eight * a.head_tiles;
+        pair = 8 * eight + blockIdx.x % 8;
+    }
+    const int32_t wg = pair / a.kv_heads, kvh = pair - wg * a.kv_heads, rest = kvh * a.head_tiles + ht;
+    if (wg >= a.shares) return;
     const int heads = min(16, a.group - 16 * ht);    // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
     const int32_t in_page = (1 << a.shift) - 1;
@@ -1510,7 +1519,8 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     a.part_o = reinterpret_cast<float *>(a.count + kAttnCounters);
     a.part_ml = a.part_o + slots * cache->head_dim;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)(a.shares * tiles));
+    const int32_t pairs = a.shares * a.kv_heads;
+    const dim3 grid((unsigned)(a.head_tiles > 1 ? (pairs + 7) / 8 * 8 * a.head_tiles : pairs));
     if (cache->type == LORA_TYPE_BF16) attention_launch<BF16>(a, grid, s);
     else attention_launch<F16>(a, grid, s);
     return launch_status("paged attention");

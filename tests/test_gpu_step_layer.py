@@ -200,6 +200,26 @@ def test_captured_step_replays_on_new_lengths(case):
     del g
 
 
+@pytest.mark.parametrize("kw", [dict(overlap=True), dict(handoff=False)])
+def test_the_layers_other_forms_give_the_same_bits(case, kw):
+    """The add-ons' shrinks on a second stream, or in launches of their own."""
+    from segmented_gather_matmul_amd import layer as LY
+    from segmented_gather_matmul_amd import step as S
+    say(f"case step-layer-forms {kw}")
+    T, outs = 24, []
+    for layer in (_layer(case, T), _layer(case, T, **kw)):
+        step = LY.PagedStep(layer.shape, 4, T, 5, 20, 8, rope=S.Rope.base(DH))
+        step.req_slot.copy_(torch.tensor(SLOT, dtype=torch.int32))
+        cache, meta = step.new_cache(), LY.BatchMeta.of_step(step, len(RANKS))
+        for new, hidden in zip(STEPS[:3], _steps(T, 11)):
+            step.begin(torch.tensor(new, dtype=torch.int32, device="cuda"))
+            out = layer.forward_paged(torch.from_numpy(hidden).cuda(), cache, step, meta)
+            outs.append(out[:sum(max(v, 0) for v in new)].clone())
+        torch.cuda.synchronize()
+    for a, b in zip(outs[:3], outs[3:]):
+        assert torch.equal(a, b)
+
+
 def test_a_step_that_does_not_fit_leaves_the_caches(case):
     from segmented_gather_matmul_amd import layer as LY
     from segmented_gather_matmul_amd import step as S
