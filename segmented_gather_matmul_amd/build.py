@@ -64,7 +64,7 @@ def build_args(verbose: bool = False) -> str:
     tmp = ARGS_LIB + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{sysconfig.get_paths()['include']}",
-           "-isystem", inc, ARGS_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-isystem", inc, f"-I{INCLUDE}", ARGS_SOURCE, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
            f"-Wl,-rpath,{lib}"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -81,7 +81,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS) or \
-        os.path.getmtime(ARGS_SOURCE) > os.path.getmtime(ARGS_LIB)
+        any(os.path.getmtime(p) > os.path.getmtime(ARGS_LIB) for p in [ARGS_SOURCE, HEADERS[0], HEADERS[1]])
 
 
 if __name__ == "__main__":

@@ -74,9 +74,9 @@ def _type(t, what):
     return ty
 
 
-# Every call checks every tensor; the checks that hold are made by a small compiled module
-# (a tenth of a microsecond each).  Where it has not been built, or one does not hold, the
-# same rules below are gone through in Python, which say what is wrong.
+# Every call checks every tensor.  A small compiled module makes the checks and the call
+# together (2 to 3 microseconds less than Python takes); where it has not been built, or a
+# check does not hold, the same rules are gone through below, which say what is wrong.
 try:
     from . import _step_args as _fast
 except ImportError:
@@ -145,10 +145,32 @@ def _call(name, *args):
         B._check(code)
 
 
-def _stream(stream, dev):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+_addresses = {}
+
+
+def _address(name):
+    """The library function's address, for the compiled module."""
+    a = _addresses.get(name)
+    if a is None:
+        a = _addresses[name] = ctypes.cast(getattr(B.lib(), name), ctypes.c_void_p).value
+    return a
+
+
+def _done(code):
+    """A call by the compiled module: whether it was made (None: a check does not hold)."""
+    if code:
+        B._check(code)
+    return code is not None
+
+
+def _device(t):
+    """The current GPU's index if t is on it, else -1."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return dev if dev >= 0 and dev == torch.cuda.current_device() else -1
+
+
+def _raw(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _ptr(t):
@@ -186,7 +208,7 @@ class PagedKV:
         self.k, self.v = k, v
         self.dtype, self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.dtype, pages, P, K, D
         self.c = CKVCache(ty, P, pages, K, D, 0, st[0], st[1], st[2], _ptr(k), _ptr(v))
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 def _apart(k, v, reach):
@@ -221,7 +243,7 @@ class KVPages:
         ld = block_table.stride(0) if n > 1 else max(block_table.stride(0), blocks)
         self.c = CKVPages(n, self.page_size, free_pages.numel(), blocks, ld, _ptr(block_table), _ptr(free_pages),
                           _ptr(free_top))
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
 
     @classmethod
     def fresh(cls, n_req, max_blocks, num_pages, page_size, device="cuda"):
@@ -254,7 +276,7 @@ class KVPlan:
         self.tok_req, self.tok_pos, self.slots, self.idx = (new(max_tokens)[:self.max_tokens] for _ in range(4))
         self.c = CKVPlanOut(self.max_tokens, 0, _ptr(self.status), _ptr(self.kv_end), _ptr(self.free_top),
                             _ptr(self.q_ptr), _ptr(self.tok_req), _ptr(self.tok_pos), _ptr(self.slots), _ptr(self.idx))
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 class Rope:
@@ -270,13 +292,19 @@ class Rope:
             raise ValueError(f"{half} frequencies (a multiple of 8), {axes} axes (1..{MAX_AXES})")
         self.inv_freq, self.axis, self.axes, self.rot_dim = inv_freq, axis, int(axes), 2 * half
         self.c = CRope(2 * half, self.axes, 1 if interleaved else 0, 0, _ptr(inv_freq) if half else None, _ptr(axis))
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
 
     @classmethod
     def base(cls, rot_dim, theta=10000.0, axis=None, axes=1, interleaved=False, device="cuda"):
         """inv_freq[i] = theta^(-2i / rot_dim)."""
         f = torch.tensor([theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], dtype=torch.float32, device=device)
         return cls(f, axis, axes, interleaved)
+
+
+class _NoRope:
+    rot_dim, inv_freq, axis = 0, None, None
+    c = CRope(0, 1, 0, 0, None, None)
+    ref, address = ctypes.byref(c), ctypes.addressof(c)
 
 
 def workspace(n_rows, heads, kv_heads, head_dim, device="cuda"):
@@ -300,13 +328,19 @@ def lora_kv_plan(plan: KVPlan, pages: KVPages, kv_len, new_len, req_slot=None, s
     n = pages.n_req
     if n > plan.n_req:
         raise ValueError(f"a plan for {plan.n_req} requests, tables of {n}")
+    if _fast:
+        dev = _device(kv_len)
+        if dev >= 0 and _done(_fast.plan(_address("lora_kv_plan"), _raw(stream, dev), dev, plan.address, pages.address,
+                                         kv_len, new_len, req_slot, pages.block_table, pages.free_pages, pages.free_top,
+                                         plan.status, plan.kv_end, plan.free_top)):
+            return
     _vector(kv_len, "kv_len", torch.int32, n)
     _vector(new_len, "new_len", torch.int32, n)
     if req_slot is not None:
         _vector(req_slot, "req_slot", torch.int32, n)
     dev = _here("kv_len new_len req_slot block_table free_pages free_top status kv_end plan.free_top", kv_len, new_len,
                 req_slot, pages.block_table, pages.free_pages, pages.free_top, plan.status, plan.kv_end, plan.free_top)
-    _call("lora_kv_plan", _stream(stream, dev), pages.ref, kv_len.data_ptr(), new_len.data_ptr(),
+    _call("lora_kv_plan", _raw(stream, dev), pages.ref, kv_len.data_ptr(), new_len.data_ptr(),
                                   _ptr(req_slot), plan.ref)
 
 
@@ -314,6 +348,13 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
     """Rotate q into q_out and k into the cache at `slots`, and append v.  positions int32
     [axes, n_rows] (1-D for one axis); rope None appends without rotation.  q and q_out may
     both be None (k and v only); q_out may be q."""
+    rope = _NoRope if rope is None else rope
+    if _fast:
+        dev = _device(slots)
+        if dev >= 0 and _done(_fast.append(_address("lora_rope_append"), _raw(stream, dev), dev, q_out, q, k, v,
+                                           cache.address, cache.k, slots, rope.address, rope.inv_freq, rope.axis,
+                                           positions)):
+            return
     dt, D = cache.dtype, cache.head_dim
     _vector(slots, "slots", torch.int32, 0)
     n = slots.numel()
@@ -329,10 +370,9 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
     ldk = _matrix(k, "k", dt, n, cache.kv_heads * D)
     ldv = _matrix(v, "v", dt, n, cache.kv_heads * D)
     ldp = n
-    if rope is None:
-        rope = _no_rope()
+    if not rope.rot_dim:
         positions = None
-    elif rope.rot_dim:
+    else:
         if not isinstance(positions, torch.Tensor):
             raise ValueError("positions must be a tensor")
         p2 = positions if positions.dim() == 2 else positions.reshape(1, -1)
@@ -340,18 +380,8 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
         ldp = p2.stride(0) if p2.shape[0] > 1 else max(n, 1)
     dev = _here("slots k v q q_out positions cache.k inv_freq axis", slots, k, v, q, q_out, positions, cache.k,
                 rope.inv_freq, rope.axis)
-    _call("lora_rope_append", _stream(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
+    _call("lora_rope_append", _raw(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
                                       v.data_ptr(), ldv, rope.ref, _ptr(positions), ldp, slots.data_ptr(), cache.ref)
-
-
-class _NoRope:
-    rot_dim, inv_freq, axis = 0, None, None
-    c = CRope(0, 1, 0, 0, None, None)
-    ref = ctypes.byref(c)
-
-
-def _no_rope():
-    return _NoRope
 
 
 def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=None, scale=None, window=0, lse=None,
@@ -360,6 +390,12 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
     int32 [n_req, max_blocks], kv_len int32 [n_rows], req int32 [n_rows] or None (row i reads
     table row i), lse fp32 [n_rows, heads] or None, work from attention_workspace."""
     dt, D = cache.dtype, cache.head_dim
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    if _fast:
+        dev = _device(q)
+        if dev >= 0 and _done(_fast.attention(_address("lora_paged_attention"), _raw(stream, dev), dev, out, q,
+                                              cache.address, cache.k, block_table, kv_len, work, req, scale, window, lse)):
+            return
     if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.shape[1] % D:
         raise ValueError(f"q must be [n_rows, heads * {D}]")
     n, cols = q.shape
@@ -378,9 +414,9 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
         _vector(lse, "lse", torch.float32, n * heads)
     _vector(work, "work", torch.int32, 1)
     dev = _here("q out block_table kv_len req lse work cache.k", q, out, block_table, kv_len, req, lse, work, cache.k)
-    _call("lora_paged_attention", _stream(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
+    _call("lora_paged_attention", _raw(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
                                           cache.ref, n_req, block_table.data_ptr(), ldt, blocks, kv_len.data_ptr(),
-                                          _ptr(req), 1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
+                                          _ptr(req), float(scale), int(window),
                                           _ptr(lse), work.data_ptr(), 4 * work.numel())
 
 
@@ -388,6 +424,11 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
                        w_offset=0.0, stream=None):
     """h = res + alpha * gate * (norm of x with post_w, or x); res_out <- h, y <- norm of h with
     w.  y or res_out may be None; res_out may be res, y may be x; x None adds nothing."""
+    if _fast:
+        dev = _device(res)
+        if dev >= 0 and _done(_fast.norm(_address("lora_residual_norm"), _raw(stream, dev), dev, y, res, w, x, res_out,
+                                         post_w, gate, gate_idx, alpha, eps, w_offset)):
+            return
     ty = _type(res, "res")
     if res.dim() != 2:
         raise ValueError(f"res must be 2-D (got {res.dim()}-D)")
@@ -414,6 +455,6 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
         _vector(gate_idx, "gate_idx", torch.int32, n)
         ip = gate_idx.data_ptr()
     dev = _here("res y res_out x w post_w gate gate_idx", res, y, res_out, x, w, post_w, gate, gate_idx)
-    _call("lora_residual_norm", _stream(stream, dev),
+    _call("lora_residual_norm", _raw(stream, dev),
           _pack_norm(ty, n, h, n_gates, yp, ldy, rp, ldro, res.data_ptr(), ldr, xp, ldx, wp, pp, gp, ldg, ip, alpha, eps,
                      w_offset, 0))

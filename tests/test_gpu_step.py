@@ -737,6 +737,61 @@ def test_norm_beyond_32_bit_offsets():
     close(y, wy, by + R.half_step(F16) * wy.abs() + R.tiny(F16), "y")
 
 
+@pytest.mark.parametrize("lens", [[40, 3, 0, 1000], [17]])
+def test_the_python_and_the_compiled_calls_are_the_same(lens, monkeypatch):
+    say(f"case both-bindings {lens}")
+    assert S._fast is not None
+    n, H, K, D, P = len(lens), 8, 2, 64, 16
+    c = AttnCase(lens, H, K, D, P, F16, seed=31, garbage=False)
+    qkv = torch.randn(n, (H + 2 * K) * D, device="cuda").half()
+    res, w = torch.randn(n, 512, device="cuda").half(), torch.randn(512, device="cuda").half()
+    gate, gi = torch.randn(3, 512, device="cuda").half(), ints([i % 4 - 1 for i in range(n)])
+    rope, pos, slots = S.Rope.base(D), ints([[5 * i for i in range(n)]]), ints([P * i for i in range(n)])
+    table, ln, work = c.table.cuda(), ints(lens), S.attention_workspace(n, H, c.cache)
+
+    def all_calls():
+        kc, vc = c.cache.k.clone(), c.cache.v.clone()
+        cache = S.PagedKV(kc, vc)
+        q_out, out, lse = torch.empty(n, H * D, dtype=F16, device="cuda"), torch.empty(n, H * D, dtype=F16, device="cuda"), torch.empty(n, H, device="cuda")
+        S.lora_rope_append(q_out, qkv[:, :H * D], qkv[:, H * D:(H + K) * D], qkv[:, (H + K) * D:], cache, slots, rope=rope, positions=pos)
+        S.lora_rope_append(None, None, qkv[:, H * D:(H + K) * D], qkv[:, (H + K) * D:], cache, ints([P * i + 1 for i in range(n)]))
+        S.lora_paged_attention(out, q_out, cache, table, ln, work, window=100, lse=lse, req=ints(list(range(n))))
+        y, ro, y2 = torch.empty_like(res), torch.empty_like(res), torch.empty_like(res)
+        S.lora_residual_norm(y, res, w, x=y2.copy_(res).mul_(2), res_out=ro, post_w=w, gate=gate, gate_idx=gi, alpha=0.5, w_offset=1.0)
+        S.lora_residual_norm(y2, res, w)
+        pages = S.KVPages.fresh(n, 70, 80 * n, P)
+        plan = S.KVPlan(n, 64 * n)
+        S.lora_kv_plan(plan, pages, ints([0] * n), ints([3 + i for i in range(n)]), req_slot=gi)
+        torch.cuda.synchronize()
+        return [kc, vc, q_out, out, lse, y, ro, y2, plan.status, plan.slots, plan.idx, pages.block_table]
+
+    fast = all_calls()
+    monkeypatch.setattr(S, "_fast", None)
+    slow = all_calls()
+    for i, (a, b) in enumerate(zip(fast, slow)):
+        assert torch.equal(a, b), i
+
+
+def test_a_refused_call_says_why_either_way(monkeypatch):
+    say("case refusals-on-the-gpu")
+    c = AttnCase([5, 6], 4, 2, 64, 16, F16, seed=1)
+    q, tab, ln, work = c.q.cuda(), c.table.cuda(), ints([5, 6]), S.attention_workspace(2, 4, c.cache)
+    out = torch.zeros_like(q)
+    for again in range(2):
+        for kw, msg in ((dict(kv_len=ln.long()), "dtype"), (dict(out=out[:1]), "at least"), (dict(out=out.cpu()), "GPU tensor"),
+                        (dict(lse=torch.zeros(3, device="cuda")), "elements"), (dict(block_table=tab.cpu()), "GPU tensor")):
+            with pytest.raises(ValueError, match=msg):
+                S.lora_paged_attention(**{**dict(out=out, q=q, cache=c.cache, block_table=tab, kv_len=ln, work=work), **kw})
+        for kw, code in ((dict(out=q), B.LORA_E_SHAPE), (dict(window=-1), B.LORA_E_SHAPE), (dict(work=work[:64]), B.LORA_E_SHAPE),
+                         (dict(scale=float("nan")), B.LORA_E_SHAPE)):
+            with pytest.raises(B.LoraError) as e:
+                S.lora_paged_attention(**{**dict(out=out, q=q, cache=c.cache, block_table=tab, kv_len=ln, work=work), **kw})
+            assert e.value.code == code
+        monkeypatch.setattr(S, "_fast", None)
+    torch.cuda.synchronize()
+    assert not out.any()
+
+
 # ------------------------------------------------------------------ streams
 def test_calls_on_a_side_stream():
     say("case side-stream")
