@@ -423,8 +423,9 @@ __device__ inline float2 turn_of(int32_t pos, float inv_freq)
 // chunks x[i..], x[i + rot/2..] whose elements turn together (interleaved, one chunk holds
 // whole pairs).  A thread asks for its first chunks first; while they are on their way, the
 // row's cos and sin are worked out, once, into LDS.  Bound by reading q, k, v and writing
-// q_out and the cells: 12,907 rows of the 7B layout 114 us (5.57 TB/s), 4001 rows of the
-// 70B layout on three axes 27 us (6.1 TB/s), 32 decode rows 3.3 us.  Four chunks a thread
+// q_out and the cells: 12,907 rows of the 7B layout 114 us (5.55 TB/s), 4001 rows of the
+// 70B layout on three axes 26 us (6.3 TB/s), 12,000 rows of 8/1 heads 13.9 us (4.4 TB/s, a
+// workgroup of two wavefronts a row), 32 decode rows 3.2 us.  Four chunks a thread
 // in flight from the start were slower on the large ones (125.5 and 37 us against 122 and
 // 36, before streaming stores).
 template <typename T, bool INTER, bool STREAM>
@@ -1139,9 +1140,10 @@ __device__ inline float block_sum(float v, float *wave_sums)
 
 // One workgroup per row; a thread keeps its NC chunks of eight elements in registers from
 // the loads to the stores, so x and res are read once and res_out and y written once.
-// Bound by those: 12,907 rows of 4096 71 us (5.95 TB/s); 4001 rows of 8192 with both norms
-// and gates 53 us (4.96 TB/s, two sums over the row one after the other); 32 rows of 4096
-// 2.9 us, a launch and one trip to memory.
+// Bound by those: 12,907 rows of 4096 70.5 us (6.0 TB/s); 4001 rows of 8192 with both norms
+// and gates 51.5 us (5.1 TB/s, two sums over the row one after the other); 500 rows of
+// 65,536 52.6 us (5.0 TB/s; with the weights asked for early too, they spill: 283 us); 32
+// rows of 4096 2.9 us, a launch and one trip to memory.
 template <typename T, int NC, bool STREAM>
 __global__ __launch_bounds__(1024) void
 lora_residual_norm_kernel(lora_norm_args a)
