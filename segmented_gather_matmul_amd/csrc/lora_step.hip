@@ -1336,7 +1336,7 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     }
     // The work there may be: every token row, and every page that the tables can hold.  Up to
     // two of these a thread, since every workgroup makes its sums at the same time (1000
-    // requests moving 240,000 one-token pages: 125 us in one workgroup, 8.5 in 256).  A plan
+    // requests moving 240,000 one-token pages: 125 us in one workgroup, 7 in 256).  A plan
     // in place would need the second launch then; while its token rows are few, so most
     // likely are its pages, and one workgroup is faster.
     const int64_t moves = out->max_tokens + std::min<int64_t>(pages->num_pages, (int64_t)n * pages->max_blocks);

@@ -445,8 +445,7 @@ def test_attention_pages_that_are_none():
 def test_attention_rows_that_are_not_active():
     say("case attention-inactive")
     c = AttnCase([5, 40, 7, 9, 0], 4, 2, 128, 16, F16, req=[0, 1, 1, 0, 1])
-    c.lens = [5, 49, -3, 9, 0]       # 49 > the 3 + 1 pages' 64? no: still inside; see the next line
-    c.lens[1] = c.table.shape[1] * 16 + 1
+    c.lens = [5, c.table.shape[1] * 16 + 1, -3, 9, 0]     # one token more than a table row can hold
     c.req = [0, 1, 1, -1, 2]
     out, lse = c.run()
     want = c.want()
@@ -607,6 +606,29 @@ def test_attention_workspace_is_left_clean_and_may_be_shared():
         big.check(out, lse, wb, "big")
         out, lse = small.run(work=work)
         small.check(out, lse, ws, "small")
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 4096, 4097, 8193])
+def test_attention_joins_of_every_depth(n):
+    """One row cut into 16, 17, 32 and more parts: one join or two, whole and broken groups."""
+    say(f"case attention-parts n={n}")
+    for H, D, dt in ((8, 128, F16), (3, 24, BF16), (20, 80, F16)):
+        c = AttnCase([n], H, 1, D, 64, dt, seed=n % 97)
+        out, lse = c.run()
+        c.check(out, lse, c.want(), f"{H} heads of {D}")
+
+
+def test_calls_of_different_shapes_share_a_workspace():
+    """The counters lie where every shape looks for them: sums of one call never become another's."""
+    say("case attention-shapes-share")
+    cases = [AttnCase([9000, 40], 8, 1, 128, 16, F16, seed=1), AttnCase([700, 3, 2500], 32, 32, 64, 16, BF16, seed=2),
+             AttnCase([5000], 40, 2, 128, 16, F16, seed=3), AttnCase([3000, 1, 0], 6, 3, 256, 16, BF16, seed=4)]
+    work = torch.zeros(max(S.attention_workspace(c.n, c.H, c.cache).numel() for c in cases), dtype=torch.int32, device="cuda")
+    wants = [c.want() for c in cases]
+    for _ in range(3):
+        for c, w in zip(cases, wants):
+            out, lse = c.run(work=work)
+            c.check(out, lse, w, f"{c.H} heads of {c.D}")
 
 
 def test_attention_captured_with_lengths_that_change():
