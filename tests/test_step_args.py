@@ -2,6 +2,7 @@
 checks make before a launch, and the references the GPU tests compare against.  No test
 here launches a kernel."""
 import ctypes
+import importlib
 import os
 import re
 import subprocess
@@ -21,6 +22,9 @@ PTR = 0x10000   # an aligned address that is never followed: every call here is 
 def _lib():
     if build_mod.stale():
         build_mod.build()
+    if S._fast is None:      # built only just now, after the binding was imported
+        importlib.invalidate_caches()
+        S._fast = importlib.import_module("segmented_gather_matmul_amd._step_args")
     return B.lib()
 
 
