@@ -25,11 +25,13 @@ bool has_type(const at::Tensor &t, long code)
     }
 }
 
+bool is_plain(const at::Tensor &t) { return t.layout() == at::kStrided && !t.is_nested(); }
+
 // The row stride of a 2-D tensor of that type with unit column stride, at least rows x cols;
 // -1 otherwise (and for a single row whose stride is no valid leading dimension).
 int64_t matrix_ld(const at::Tensor &t, long code, int64_t rows, int64_t cols)
 {
-    if (t.layout() != at::kStrided || t.dim() != 2 || !has_type(t, code) || t.size(0) < rows || t.size(1) < cols ||
+    if (!is_plain(t) || t.dim() != 2 || !has_type(t, code) || t.size(0) < rows || t.size(1) < cols ||
         (t.size(1) > 1 && t.stride(1) != 1) || t.stride(0) < cols || (t.size(0) < 2 && t.stride(0) % 8))
         return -1;
     return t.stride(0);
@@ -37,7 +39,7 @@ int64_t matrix_ld(const at::Tensor &t, long code, int64_t rows, int64_t cols)
 
 bool is_vector(const at::Tensor &t, long code, int64_t n)
 {
-    return t.layout() == at::kStrided && has_type(t, code) && t.numel() >= n && t.is_contiguous();
+    return is_plain(t) && has_type(t, code) && t.numel() >= n && t.is_contiguous();
 }
 
 // One call's arguments: `ok` falls as soon as one is not what it should be.
@@ -71,7 +73,7 @@ struct Args {
     {
         const at::Tensor *t = tensor(i);
         if (!ok) return nullptr;
-        if (t->layout() != at::kStrided || t->dim() != 2 || !has_type(*t, kI32) || t->size(0) < rows || t->size(1) < cols ||
+        if (!is_plain(*t) || t->dim() != 2 || !has_type(*t, kI32) || t->size(0) < rows || t->size(1) < cols ||
             (t->size(1) > 1 && t->stride(1) != 1) || (t->size(0) > 1 && t->stride(0) < cols)) {
             ok = false;
             return nullptr;
@@ -264,7 +266,24 @@ PyObject *plan(PyObject *, PyObject *const *args, Py_ssize_t n)
                               static_cast<const int32_t *>(slot), out));
 }
 
-#define STEP_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
+// A tensor without plain sizes or memory throws from the accessors above.  No exception may leave a C function: the answer is then that of
+// a check that does not hold.
+typedef PyObject *Function(PyObject *, PyObject *const *, Py_ssize_t);
+template <Function *F>
+PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        return F(self, args, n);
+    } catch (...) {
+        PyErr_Clear();
+    }
+    if (F == matrix || F == here) return PyLong_FromLong(-1);
+    if (F == vector) Py_RETURN_FALSE;
+    Py_RETURN_NONE;
+}
+
+#define STEP_METHOD(name) \
+    {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {STEP_METHOD(matrix), STEP_METHOD(vector), STEP_METHOD(here),
                          STEP_METHOD(attention), STEP_METHOD(append), STEP_METHOD(norm),
                          STEP_METHOD(plan), {nullptr, nullptr, 0, nullptr}};

@@ -95,6 +95,8 @@ def _matrix_checked(t, what, dtype, rows, cols):
         raise ValueError(f"{what} must be a tensor (got {type(t).__name__})")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must have dtype {_NAMES[dtype]} (got {t.dtype})")
+    if t.layout is not torch.strided or t.is_nested:
+        raise ValueError(f"{what} must be a plain strided tensor")
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D (got {t.dim()}-D)")
     n, c = t.shape
@@ -118,6 +120,8 @@ def _vector(t, what, dtype, n):
         raise ValueError(f"{what} must be a tensor (got {type(t).__name__})")
     if t.dtype is not dtype:
         raise ValueError(f"{what} must have dtype {_NAMES[dtype]} (got {t.dtype})")
+    if t.layout is not torch.strided or t.is_nested:
+        raise ValueError(f"{what} must be a plain strided tensor")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     if t.numel() < n:

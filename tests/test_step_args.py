@@ -251,6 +251,25 @@ def test_compiled_checks_agree_with_the_python_ones():
     assert S._fast.here(base, None, base) == -1 and S._fast.here(base, 5) == -1
 
 
+@pytest.mark.parametrize("kind", ["nested", "sparse"])
+def test_tensors_without_plain_memory_are_refused(kind):
+    """They throw from their accessors; the process goes on and the check says what is wrong."""
+    def make(dt):
+        if kind == "sparse":
+            return torch.eye(16, dtype=dt).to_sparse()
+        return torch.nested.nested_tensor([torch.zeros(8, dtype=dt), torch.zeros(16, dtype=dt)])
+
+    for dt in S._CODES:
+        t = make(dt)
+        assert S._fast.matrix(t, S._CODES[dt], 1, 4) == -1
+        assert not S._fast.vector(t, S._CODES[dt], 1)
+        assert S._fast.here(t) == -1
+        with pytest.raises(ValueError, match="strided"):
+            S._matrix(t, "t", dt, 1, 4)
+    with pytest.raises(ValueError, match="strided"):
+        S._vector(make(torch.int32), "t", torch.int32, 1)
+
+
 def test_descriptors_reject_wrong_layouts():
     h = torch.float16
     k = torch.zeros(4, 16, 2, 64, dtype=h)
