@@ -199,6 +199,8 @@ class PagedKV:
         if k.device != v.device:
             raise ValueError(f"k is on {k.device}, v on {v.device}")
         pages, P, K, D = k.shape
+        if not k.numel():
+            raise ValueError(f"k and v are empty ({tuple(k.shape)})")
         # a dimension of one entry may have any stride; give the library a valid one
         st = [s if n > 1 else max(D, 8) for n, s in zip(k.shape[:3], k.stride()[:3])]
         cells = sorted((s, n) for n, s in zip(k.shape[:3], k.stride()[:3]) if n > 1)
@@ -219,7 +221,7 @@ def _apart(k, v, reach):
     """k and v (`reach` elements each) do not overlap, or are taken from one tensor along a
     dimension between theirs (e.g. [pages, 2, ...])."""
     off = abs(v.data_ptr() - k.data_ptr()) // k.element_size()
-    if off >= reach or not k.numel():
+    if off >= reach:
         return True
     dims = sorted(((s, n) for n, s in zip(k.shape, k.stride()) if n > 1), reverse=True)
     for i, (s, n) in enumerate(dims):

@@ -281,6 +281,9 @@ def test_descriptors_reject_wrong_layouts():
                       ((k.expand(4, 16, 2, 64)[:1].expand(4, 16, 2, 64), torch.zeros_like(k)), "strides|overlapping")):
         with pytest.raises(ValueError, match=msg):
             S.PagedKV(*args)
+    for shape in ((0, 16, 2, 64), (4, 0, 2, 64), (4, 16, 0, 64), (4, 16, 2, 0)):  # (heads of 0 columns: a division by 0)
+        with pytest.raises(ValueError, match="empty"):
+            S.PagedKV(torch.zeros(shape, dtype=h), torch.zeros(shape, dtype=h))
     t, f, top = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     S.KVPages(t, f, top, 16)
     for args, msg in (((t, f, top, 12), "power"), ((t.long(), f, top, 16), "dtype"), ((t[0], f, top, 16), "block_table"),
