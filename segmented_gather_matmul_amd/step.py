@@ -381,7 +381,9 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
     else:
         if not isinstance(positions, torch.Tensor):
             raise ValueError("positions must be a tensor")
-        p2 = positions if positions.dim() == 2 else positions.reshape(1, -1)
+        if positions.dim() not in (1, 2):
+            raise ValueError(f"positions must be [axes, n_rows] or, for one axis, [n_rows] (got {positions.dim()}-D)")
+        p2 = positions if positions.dim() == 2 else positions[None]
         ldp = _matrix(p2, "positions", torch.int32, rope.axes, n)
         ldp = p2.stride(0) if p2.shape[0] > 1 else max(n, 1)
     dev = _here("slots k v q q_out positions cache.k inv_freq axis", slots, k, v, q, q_out, positions, cache.k,

@@ -202,7 +202,9 @@ def test_binding_rejects_wrong_tensors():
                                                     positions=torch.zeros(1, 2, dtype=torch.int32)), **k})
     for k, msg in ((dict(q_out=None), "together"), (dict(k=k2.bfloat16()), "dtype"), (dict(positions=None), "tensor"),
                    (dict(positions=torch.zeros(1, 1, dtype=torch.int32)), "at least"), (dict(v=k2[:, :64]), "at least"),
-                   (dict(slots=n.long()), "dtype"), (dict(), "GPU tensor")):
+                   (dict(slots=n.long()), "dtype"), (dict(), "GPU tensor"),
+                   (dict(positions=torch.zeros(2, 3, 2, dtype=torch.int32)[:, :1]), "3-D"),   # not a view of one row
+                   (dict(positions=torch.zeros(4, dtype=torch.int32)[::2]), "stride")):
         with pytest.raises(ValueError, match=msg):
             app(**k)
     r = torch.zeros(2, 64, dtype=h)
