@@ -115,8 +115,9 @@ typedef struct lora_kv_plan_out {
  * All or nothing: if any LORA_KV_* bit is set, the tables and the free list stay as they
  * were, kv_end = kv_len, the free top is copied, q_ptr is all 0 and the maps are all -1
  * (the step's other calls then do nothing); status[1..3] still give what the step asked
- * for (clamped to 2^31 - 1).  Page ids are moved, never followed.  Two plans of one free
- * list or table must be ordered on one stream.
+ * for (clamped to 2^31 - 1).  Page ids are moved, never followed.  The arrays written share
+ * no entry with each other or with those read, other than kv_end and free_top as said.
+ * Two plans of one free list or table must be ordered on one stream.
  */
 int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len, const int32_t *new_len,
                  const int32_t *req_slot, const lora_kv_plan_out *out);

@@ -1297,6 +1297,35 @@ int check_apart(const void *out, int64_t ldo, int64_t cols_o, const void *in, in
     return fail(LORA_E_SHAPE, "%s overlap", what);
 }
 
+// The arrays that a plan writes share no entry with each other or with those it reads, but
+// that kv_end may be kv_len and free_top the pages' own: its workgroups each read all the
+// lengths, at times of their own.
+int check_plan_arrays(const lora_kv_pages &pg, const int32_t *kv_len, const int32_t *new_len, const int32_t *req_slot,
+                      const lora_kv_plan_out &o)
+{
+    struct Range {
+        const int32_t *p;
+        int64_t n;
+        const char *name;
+    };
+    const int64_t n = pg.n_req, t = o.max_tokens;
+    const Range all[] = {{o.kv_end, n, "kv_end"}, {o.free_top, 1, "out free_top"}, {o.status, 4, "status"},
+                         {o.q_ptr, n + 1, "q_ptr"}, {o.tok_req, t, "tok_req"}, {o.tok_pos, t, "tok_pos"},
+                         {o.slots, t, "slots"}, {o.idx, t, "idx"}, {pg.free_pages, pg.num_pages, "free_pages"},
+                         {kv_len, n, "kv_len"}, {new_len, n, "new_len"}, {req_slot, n, "req_slot"},
+                         {pg.free_top, 1, "free_top"}};
+    constexpr int kKvEnd = 0, kTop = 1, kWritten = 9, kLen = 9, kOldTop = 12, kAll = 13;
+    for (int i = 0; i < kWritten; ++i)
+        for (int j = i + 1; j < kAll; ++j) {
+            const Range &w = all[i], &x = all[j];
+            const auto a = reinterpret_cast<uintptr_t>(w.p), b = reinterpret_cast<uintptr_t>(x.p);
+            if (!a || !b || a >= b + 4 * x.n || b >= a + 4 * w.n || !w.n || !x.n) continue;
+            if (a == b && ((i == kKvEnd && j == kLen) || (i == kTop && j == kOldTop))) continue;
+            return fail(LORA_E_SHAPE, "%s and %s overlap", w.name, x.name);
+        }
+    return LORA_OK;
+}
+
 }  // namespace
 }  // namespace lora
 
@@ -1326,6 +1355,7 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
         return fail(LORA_E_NULL, "block_table, kv_len, new_len and kv_end are required");
     if (out->max_tokens > 0 && (!out->tok_req || !out->tok_pos || !out->slots))
         return fail(LORA_E_NULL, "tok_req, tok_pos and slots are required");
+    if (const int st = check_plan_arrays(*pages, kv_len, new_len, req_slot, *out)) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int32_t n = pages->n_req;
     if (n > kPlanThreads) {

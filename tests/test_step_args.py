@@ -145,6 +145,24 @@ def test_plan_refusals(pages, out, code):
     assert _plan(pages, out) == code
 
 
+def test_plan_arrays_must_be_apart():
+    """Only kv_end over kv_len and the free top over itself, entry for entry, are taken."""
+    names = ["status", "kv_end", "free_top", "q_ptr", "tok_req", "tok_pos", "slots", "idx"]
+    at = {x: PTR + 4096 * i for i, x in enumerate(names + ["kv", "new", "old_top", "free_pages", "table"])}
+
+    def plan(**kw):
+        a = {**at, **kw}
+        return _plan(dict(free_pages=a["free_pages"], free_top=a["old_top"], block_table=a["table"]),
+                     {x: a[x] for x in names}, a["kv"], a["new"])
+
+    for kw, what in ((dict(kv_end=at["new"]), "kv_end and new_len"), (dict(kv_end=at["kv"] + 4), "kv_end and kv_len"),
+                     (dict(kv_end=at["kv"] - 8), "kv_end and kv_len"), (dict(q_ptr=at["kv"]), "q_ptr and kv_len"),
+                     (dict(free_top=at["kv_end"]), "kv_end and out free_top"), (dict(free_top=at["free_pages"] + 28), "free_pages"),
+                     (dict(old_top=at["status"] + 12), "status and free_top"), (dict(idx=at["slots"] + 12), "slots and idx"),
+                     (dict(tok_pos=at["new"] + 8), "tok_pos and new_len"), (dict(new=at["free_pages"] + 8), "free_pages and new_len")):
+        assert plan(**kw) == B.LORA_E_SHAPE and what in B.last_error(), (kw, B.last_error())
+
+
 def test_plan_needs_its_lengths():
     assert _plan(kv=None) == B.LORA_E_NULL and _plan(new=None) == B.LORA_E_NULL
 
