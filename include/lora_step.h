@@ -71,7 +71,7 @@ typedef struct lora_kv_pages {
     int32_t n_req;         /* rows of the batch's tables (>= 0) */
     int32_t page_size;     /* a power of two, 1..LORA_KV_MAX_PAGE */
     int32_t num_pages;     /* capacity of free_pages (>= 1) */
-    int32_t max_blocks;    /* entries of a table row (>= 1) */
+    int32_t max_blocks;    /* entries of a table row (>= 1); max_blocks * page_size <= 2^31 - 1 */
     int64_t ld_table;      /* >= max_blocks */
     int32_t *block_table;  /* device [n_req][ld_table], updated in place */
     int32_t *free_pages;   /* device [num_pages], updated in place */

@@ -1345,7 +1345,11 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     if (pages->n_req < 0 || pages->num_pages < 1 || (int64_t)pages->num_pages * pages->page_size > INT32_MAX)
         return fail(LORA_E_SHAPE, "n_req = %d, num_pages = %d of %d tokens", pages->n_req, pages->num_pages,
                     pages->page_size);
-    if (pages->max_blocks < 1 || pages->ld_table < pages->max_blocks)
+    // no request that fits its row then ends beyond a 32-bit position
+    if (pages->max_blocks < 1 || (int64_t)pages->max_blocks * pages->page_size > INT32_MAX)
+        return fail(LORA_E_SHAPE, "max_blocks = %d of %d tokens (1 page to 2^31 - 1 tokens)", pages->max_blocks,
+                    pages->page_size);
+    if (pages->ld_table < pages->max_blocks)
         return fail(LORA_E_SHAPE, "max_blocks = %d, ld_table = %lld", pages->max_blocks, (long long)pages->ld_table);
     if (out->max_tokens < 0 || out->reserved != 0)
         return fail(LORA_E_SHAPE, "max_tokens = %d, reserved = %d", out->max_tokens, out->reserved);

@@ -163,6 +163,23 @@ def test_plan_arrays_must_be_apart():
         assert plan(**kw) == B.LORA_E_SHAPE and what in B.last_error(), (kw, B.last_error())
 
 
+def _apart_plan(pages=None, **kw):
+    """A plan over arrays that lie apart; kw moves some of them."""
+    names = ["status", "kv_end", "free_top", "q_ptr", "tok_req", "tok_pos", "slots", "idx"]
+    at = {x: PTR + (i << 16) for i, x in enumerate(names + ["kv", "new", "old_top", "free_pages", "table"])}
+    at.update(kw)
+    return _plan(dict(free_pages=at["free_pages"], free_top=at["old_top"], block_table=at["table"], **(pages or {})),
+                 {x: at[x] for x in names}, at["kv"], at["new"])
+
+
+def test_plan_tables_wider_than_a_position_are_refused():
+    """A position is 32 bits: a table row of 2^31 tokens or more would plan requests that end
+    behind it, whose positions wrap to negative ones and read the table far before its row."""
+    for page, blocks in ((1024, 1 << 21), (1024, (1 << 21) + 1), (2, 1 << 30), (16, 2 ** 31 - 1)):
+        code = _apart_plan(dict(page_size=page, max_blocks=blocks, ld_table=blocks, n_req=1, num_pages=1))
+        assert code == B.LORA_E_SHAPE and "max_blocks" in B.last_error(), (page, blocks, code, B.last_error())
+
+
 def test_plan_needs_its_lengths():
     assert _plan(kv=None) == B.LORA_E_NULL and _plan(new=None) == B.LORA_E_NULL
 
