@@ -1315,6 +1315,15 @@ int check_plan_arrays(const lora_kv_pages &pg, const int32_t *kv_len, const int3
                          {kv_len, n, "kv_len"}, {new_len, n, "new_len"}, {req_slot, n, "req_slot"},
                          {pg.free_top, 1, "free_top"}};
     constexpr int kKvEnd = 0, kTop = 1, kWritten = 9, kLen = 9, kOldTop = 12, kAll = 13;
+    // The table: n rows of max_blocks entries, ld_table apart; what lies between them is none.
+    const __int128 ld = 4 * (__int128)pg.ld_table, row = 4 * (__int128)pg.max_blocks;
+    for (const Range &x : all) {
+        if (!x.p || !x.n || !n) continue;
+        const __int128 from = (__int128)reinterpret_cast<uintptr_t>(x.p) - reinterpret_cast<uintptr_t>(pg.block_table);
+        const __int128 to = from + 4 * x.n, r = from > 0 ? from / ld : 0;  // in bytes; the row that `from` is in or behind
+        const bool here = r < n && from < r * ld + row && to > r * ld, next = r + 1 < n && to > (r + 1) * ld;
+        if (here || next) return fail(LORA_E_SHAPE, "block_table and %s overlap", x.name);
+    }
     for (int i = 0; i < kWritten; ++i)
         for (int j = i + 1; j < kAll; ++j) {
             const Range &w = all[i], &x = all[j];

@@ -180,6 +180,33 @@ def test_plan_tables_wider_than_a_position_are_refused():
         assert code == B.LORA_E_SHAPE and "max_blocks" in B.last_error(), (page, blocks, code, B.last_error())
 
 
+def test_plan_tables_lie_apart_from_the_other_arrays():
+    """The table is written too: no other array may hold one of its entries.  What lies between
+    its rows, behind max_blocks, is no entry."""
+    table = PTR + (64 << 16)
+    sizes = dict(status=4, kv_end=3, free_top=1, q_ptr=4, tok_req=4, tok_pos=4, slots=4, idx=4, kv=3, new=3, old_top=1,
+                 free_pages=8)
+    named = dict(kv="kv_len", new="new_len", old_top="free_top")
+
+    def meets(at, what, ld):
+        """Whether an array `at` entries from the table's first is refused for it.  (Two other
+        arrays overlap in every call, so that none of them goes on to a launch.)"""
+        pair = ("slots", "idx") if what not in ("slots", "idx") else ("tok_req", "tok_pos")
+        kw = {x: PTR + (65 << 16) for x in pair}
+        assert _apart_plan(dict(ld_table=ld), **{**kw, "table": table, what: table + 4 * at}) == B.LORA_E_SHAPE
+        if "block_table" in B.last_error():
+            assert named.get(what, what) in B.last_error()
+            return True
+        assert B.last_error() == f"{pair[0]} and {pair[1]} overlap"
+        return False
+
+    for what, n in sizes.items():
+        for ld in (4, 7, 8):          # three rows of four entries
+            entries = {ld * r + c for r in range(3) for c in range(4)}
+            for at in range(-9, 3 * ld + 2):
+                assert meets(at, what, ld) == bool(entries & set(range(at, at + n))), (what, ld, at, B.last_error())
+
+
 def test_plan_needs_its_lengths():
     assert _plan(kv=None) == B.LORA_E_NULL and _plan(new=None) == B.LORA_E_NULL
 
