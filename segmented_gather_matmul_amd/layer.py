@@ -287,7 +287,8 @@ class LoraDecoderLayer:
     def forward_paged(self, hidden, cache, step: PagedStep, meta: BatchMeta | None, trace: dict | None = None):
         """hidden [step.max_tokens, h] fp16 -> the same, for the token rows of the step planned
         last; rows behind the last token are not read by any other row.  cache: this layer's
-        step.PagedKV.  meta and trace as for forward (meta: BatchMeta.of_step)."""
+        step.PagedKV, of the step's page size and heads and at least its number of pages.
+        meta and trace as for forward (meta: BatchMeta.of_step)."""
         import torch
         import torch.nn.functional as F
         from . import step as S
@@ -296,6 +297,12 @@ class LoraDecoderLayer:
         n = hidden.shape[0]
         if n > self.max_rows or n != step.max_tokens or step.shape != s:
             raise ValueError(f"batch of {n} rows does not fit this layer or step")
+        # the operators read pages and heads off the cache, slots and tables off the step
+        P, pages = step.pages.page_size, step.pages.free_pages.numel()
+        if (cache.page_size, cache.kv_heads, cache.head_dim) != (P, kv // s.head_dim, s.head_dim) or cache.num_pages < pages:
+            raise ValueError(f"a cache of {cache.num_pages} pages of {cache.page_size} tokens, {cache.kv_heads} heads of "
+                             f"{cache.head_dim} does not fit a step of {pages} pages of {P}, {kv // s.head_dim} heads of "
+                             f"{s.head_dim}")
         if meta is not None and meta.n != n:
             raise ValueError(f"metadata for {meta.n} rows, batch of {n}")
 
