@@ -118,6 +118,35 @@ def test_plan_in_place_equals_its_definition(n, page, cap, fits):
         c.check(plan, want2, "second step")
 
 
+@pytest.mark.parametrize("n,page,cap", [(40, 16, 900), (300, 16, 40000), (700, 8, 60000), (1024, 8, 500), (1500, 4, 90000)])
+def test_plan_in_place_in_chained_steps(n, page, cap):
+    """Step after step over the same arrays in place, whatever the lengths have become: each from
+    what the one before left, with requests that end and ones that start in their rows again."""
+    say(f"case plan-in-place-chained n={n} page={page} cap={cap}")
+    rng = random.Random(n)
+    kv, new = _mixed(n, n, page, most=min(100, cap // 40))
+    mb = -(-300 // page)
+    c = PlanCase(kv, new, page, max_blocks=mb, spare=6 * n, seed=n, max_tokens=cap)
+    plan = S.KVPlan(n, cap, kv_end=c.dev_kv, free_top=c.dev_top)
+    for it in range(4):
+        want = R.plan(c.kv, c.new, c.table, c.free, c.top, page, cap, c.req_slot)
+        assert want["status"][0] in ((0, 4) if it == 0 else (0,)), (it, want["status"])   # (1024 requests: the first has too many rows)
+        S.lora_kv_plan(plan, c.pages, c.dev_kv, c.dev_new, req_slot=c.dev_slot)
+        c.check(plan, want, f"step {it}")
+        c.kv, c.table, c.free, c.top = want["kv_end"], want["table"], want["free"], want["free_top"]
+        left, room = c.top, cap
+        c.new = []
+        for have in c.kv:          # what the table, the free pages and the rows still hold
+            m = rng.choice([-1, 0, 1, 1, 1, 5, 2 * page])
+            grow = -(-(have + max(m, 0)) // page) - -(-have // page)
+            if m > 0 and (have + m > mb * page or grow > left or m > room):
+                m = 0
+            if m > 0:
+                left, room = left - grow, room - m
+            c.new.append(m)
+        c.dev_new.copy_(ints(c.new))
+
+
 @pytest.mark.parametrize("kv,new,page,max_tokens", [
     ([], [], 16, 5), ([0], [0], 16, 0), ([0], [0], 16, 4), ([0, 0], [1, 0], 1, 1), ([5], [-1], 4, 2),
     ([0] * 7, [-1] * 7, 8, 3), ([16], [16], 16, 16), ([4095], [1], 16, 4096), ([0, 3], [5000, 1], 16, 5100),
