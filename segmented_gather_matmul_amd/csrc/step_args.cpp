@@ -68,11 +68,17 @@ struct Args {
         if (ld < 0) ok = false;
         return t->data_ptr();
     }
-    // A matrix of int32 metadata, whose row stride needs no alignment.
-    const int32_t *ints(int i, int64_t rows, int64_t cols, int64_t &ld)
+    // A matrix of int32 metadata, whose row stride needs no alignment; with `row_ok`, one row
+    // of it may be 1-D.
+    const int32_t *ints(int i, int64_t rows, int64_t cols, int64_t &ld, bool row_ok = false)
     {
         const at::Tensor *t = tensor(i);
         if (!ok) return nullptr;
+        if (row_ok && rows <= 1 && is_plain(*t) && t->dim() == 1) {
+            if (!has_type(*t, kI32) || t->size(0) < cols || (t->size(0) > 1 && t->stride(0) != 1)) ok = false;
+            ld = std::max<int64_t>(cols, 1);
+            return ok ? static_cast<const int32_t *>(t->data_ptr()) : nullptr;
+        }
         if (!is_plain(*t) || t->dim() != 2 || !has_type(*t, kI32) || t->size(0) < rows || t->size(1) < cols ||
             (t->size(1) > 1 && t->stride(1) != 1) || (t->size(0) > 1 && t->stride(0) < cols)) {
             ok = false;
@@ -205,7 +211,7 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
     g.tensor(12, true);
     const int32_t *pos = nullptr;
     ldp = std::max<int64_t>(rows, 1);
-    if (rope->rot_dim > 0) pos = g.ints(13, rope->n_axes, rows, ldp);
+    if (rope->rot_dim > 0) pos = g.ints(13, rope->n_axes, rows, ldp, true);
     if (!g.ok || rows > INT32_MAX || heads > INT32_MAX) Py_RETURN_NONE;
     return PyLong_FromLong(fn(stream, (int32_t)rows, (int32_t)heads, qo, ldqo, qp, ldq, k, ldk, v, ldv, rope, pos, ldp,
                               static_cast<const int32_t *>(sp), c));

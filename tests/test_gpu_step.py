@@ -860,3 +860,74 @@ def test_calls_on_a_side_stream():
     S.lora_paged_attention(out2, *args, stream=side)
     side.synchronize()
     assert torch.equal(out2, out)
+
+
+class Compiled:
+    """The compiled module, keeping what each of its calls answered."""
+
+    def __init__(self):
+        self.answers, self.module = [], S._fast
+
+    def __getattr__(self, name):
+        fn = getattr(self.module, name)
+        if name not in ("append", "attention", "norm", "plan"):
+            return fn
+
+        def call(*args):
+            self.answers.append((name, fn(*args)))
+            return self.answers[-1][1]
+
+        return call
+
+
+@pytest.mark.parametrize("n", [1, 5, 64])
+def test_one_axis_positions_take_the_compiled_call(n, monkeypatch):
+    """Positions [n_rows] and [1, n_rows] of one axis are one call, made by the compiled module, also
+    for a longer array and a view of one; what it leaves to Python is refused there."""
+    say(f"case compiled-append n={n}")
+    H, K, D, P = 4, 2, 64, 16
+    rope, slots = S.Rope.base(D), ints([3 * i for i in range(n)])
+    qkv = torch.randn(n, (H + 2 * K) * D, device="cuda").half()
+    q, k, v = qkv[:, :H * D], qkv[:, H * D:(H + K) * D], qkv[:, (H + K) * D:]
+    pos = ints([7 * i + 1 for i in range(n + 3)])
+    seen = Compiled()
+    monkeypatch.setattr(S, "_fast", seen)
+
+    def call(positions, axes=rope):
+        cache = S.PagedKV(torch.zeros(3 * n // P + 1, P, K, D, dtype=F16, device="cuda"),
+                          torch.zeros(3 * n // P + 1, P, K, D, dtype=F16, device="cuda"))
+        q_out = torch.zeros(n, H * D, dtype=F16, device="cuda")
+        S.lora_rope_append(q_out, q, k, v, cache, slots, rope=axes, positions=positions)
+        torch.cuda.synchronize()
+        return q_out, cache.k, cache.v
+
+    want = call(pos[None, :n])
+    assert want[0].any() and want[1].any()
+    later = torch.cat([pos.new_full((2,), 99), pos])
+    for p in (pos[:n], pos, later[2:], later[2:2 + n]):
+        for a, b in zip(call(p), want):
+            assert torch.equal(a, b)
+    assert seen.answers == [("append", 0)] * 5, seen.answers
+    if n > 1:
+        for bad, msg in ((pos[:n - 1], "at least"), (later.repeat(2)[::2], "stride"), (pos[:n].long(), "dtype"),
+                         (pos.cpu(), "GPU tensor")):
+            with pytest.raises(ValueError, match=msg):
+                call(bad)
+    with pytest.raises(ValueError, match="at least"):
+        call(pos, S.Rope(rope.inv_freq, axes=2))
+
+
+def test_the_layers_append_takes_the_compiled_call(monkeypatch):
+    """Every call of the decoder layer's paged step is made by the compiled module."""
+    from segmented_gather_matmul_amd import layer as LY
+    say("case compiled-layer")
+    shape = LY.LlamaShape("case", 256, 512, 4, 64, kv_heads=2)
+    layer = LY.random_layer(shape, 2, 8, 8, torch.Generator(device="cuda").manual_seed(0))
+    step = LY.PagedStep(shape, 2, 8, 3, 6, 8, rope=S.Rope.base(64))
+    cache, meta = step.new_cache(), LY.BatchMeta.of_step(step, 2)
+    seen = Compiled()
+    monkeypatch.setattr(S, "_fast", seen)
+    step.begin(ints([5, 2]))
+    layer.forward_paged(torch.randn(8, 256, device="cuda").half(), cache, step, meta)
+    torch.cuda.synchronize()
+    assert seen.answers == [(c, 0) for c in ("plan", "norm", "append", "attention", "norm", "norm")], seen.answers
