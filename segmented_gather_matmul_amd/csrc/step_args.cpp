@@ -119,6 +119,22 @@ struct Args {
     }
 };
 
+// The library's status.  A launch may wait for room in its queue, so other Python threads run
+// meanwhile; the call's own references keep its tensors.
+template <typename Fn, typename... A>
+PyObject *status_of(Fn fn, A... a)
+{
+    struct Unlocked {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    };
+    const int code = [&] {
+        const Unlocked unlocked;
+        return fn(a...);
+    }();
+    return PyLong_FromLong(code);
+}
+
 #define STEP_ARGS(count)                                                                   \
     if (n != count) return PyErr_Format(PyExc_TypeError, "%s takes %d arguments", __func__, count); \
     Args g{args, 0};                                                                          \
@@ -183,10 +199,10 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
         window > INT32_MAX)
         Py_RETURN_NONE;
     const size_t bytes = 4 * static_cast<size_t>(THPVariable_Unpack(args[9]).numel());
-    return PyLong_FromLong(fn(stream, (int32_t)rows, (int32_t)heads, out, ldo, qp, ldq, c, (int32_t)n_req,
-                              tp, ldt, (int32_t)blocks, static_cast<const int32_t *>(len),
-                              static_cast<const int32_t *>(req), scale, (int32_t)window, static_cast<float *>(lse),
-                              work, bytes));
+    return status_of(fn, stream, (int32_t)rows, (int32_t)heads, out, ldo, qp, ldq, c, (int32_t)n_req,
+                     tp, ldt, (int32_t)blocks, static_cast<const int32_t *>(len),
+                     static_cast<const int32_t *>(req), scale, (int32_t)window, static_cast<float *>(lse),
+                     work, bytes);
 }
 
 // append(function, stream, device, q_out, q, k, v, cache, cache k, slots, rope, inv_freq, axis, positions)
@@ -213,8 +229,8 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
     ldp = std::max<int64_t>(rows, 1);
     if (rope->rot_dim > 0) pos = g.ints(13, rope->n_axes, rows, ldp, true);
     if (!g.ok || rows > INT32_MAX || heads > INT32_MAX) Py_RETURN_NONE;
-    return PyLong_FromLong(fn(stream, (int32_t)rows, (int32_t)heads, qo, ldqo, qp, ldq, k, ldk, v, ldv, rope, pos, ldp,
-                              static_cast<const int32_t *>(sp), c));
+    return status_of(fn, stream, (int32_t)rows, (int32_t)heads, qo, ldqo, qp, ldq, k, ldk, v, ldv, rope, pos, ldp,
+                     static_cast<const int32_t *>(sp), c);
 }
 
 // norm(function, stream, device, y, res, w, x, res_out, post_w, gate, gate_idx, alpha, eps, w_offset)
@@ -249,7 +265,7 @@ PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
     a.eps = g.real(12);
     a.w_offset = g.real(13);
     if (!g.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(fn(stream, &a));
+    return status_of(fn, stream, &a);
 }
 
 // plan(function, stream, device, plan, pages, kv_len, new_len, req_slot, tensor, ...): the
@@ -268,8 +284,8 @@ PyObject *plan(PyObject *, PyObject *const *args, Py_ssize_t n)
     const void *slot = g.vector(7, kI32, pages->n_req, true);
     for (Py_ssize_t i = 8; i < n; ++i) g.tensor((int)i);
     if (!g.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(fn(stream, pages, static_cast<const int32_t *>(len), static_cast<const int32_t *>(add),
-                              static_cast<const int32_t *>(slot), out));
+    return status_of(fn, stream, pages, static_cast<const int32_t *>(len), static_cast<const int32_t *>(add),
+                     static_cast<const int32_t *>(slot), out);
 }
 
 // A tensor without plain sizes or memory throws from the accessors above.  No exception may leave a C function: the answer is then that of

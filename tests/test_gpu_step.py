@@ -931,3 +931,46 @@ def test_the_layers_append_takes_the_compiled_call(monkeypatch):
     layer.forward_paged(torch.randn(8, 256, device="cuda").half(), cache, step, meta)
     torch.cuda.synchronize()
     assert seen.answers == [(c, 0) for c in ("plan", "norm", "append", "attention", "norm", "norm")], seen.answers
+
+
+def test_other_threads_run_while_a_compiled_call_waits():
+    """The library's call may wait for room in the launch queue: it is made without the
+    interpreter's lock.  In its place here the C library's sleep, whose argument takes the
+    stream's and which answers 0, from each compiled call."""
+    import ctypes
+    import threading
+    import time
+    say("case compiled-lock")
+    sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    c = AttnCase([5, 6], 4, 2, 64, 16, F16, seed=1)
+    q, tab, ln, work = c.q.cuda(), c.table.cuda(), ints([5, 6]), S.attention_workspace(2, 4, c.cache)
+    kv, none = torch.zeros(2, 128, dtype=F16, device="cuda"), S._NoRope
+    pages, plan = S.KVPages.fresh(2, 3, 6, 16), S.KVPlan(2, 8)
+    us, dev = 200000, torch.cuda.current_device()
+    calls = dict(norm=lambda: S._fast.norm(sleep, us, dev, None, q, None, None, torch.empty_like(q), None, None, None, 1.0, 1e-5, 0.0),
+                 attention=lambda: S._fast.attention(sleep, us, dev, torch.empty_like(q), q, c.cache.address, c.cache.k, tab, ln, work,
+                                                     None, 1.0, 0, None),
+                 append=lambda: S._fast.append(sleep, us, dev, None, None, kv, kv, c.cache.address, c.cache.k, ln, none.address,
+                                               None, None, None),
+                 plan=lambda: S._fast.plan(sleep, us, dev, plan.address, pages.address, ln, ln, None))
+    torch.cuda.synchronize()
+    for name, call in calls.items():
+        ticks, stop = [], threading.Event()
+
+        def count():
+            while not stop.is_set():
+                ticks.append(time.perf_counter())
+                time.sleep(0.002)
+
+        other = threading.Thread(target=count)
+        other.start()
+        while not ticks:
+            time.sleep(0.001)
+        begin = time.perf_counter()
+        assert call() == 0, name
+        end = time.perf_counter()
+        stop.set()
+        other.join()
+        assert end - begin > us * 0.9e-6, name
+        inside = [t for t in ticks if begin + 0.02 < t < end - 0.02]
+        assert len(inside) >= 5, (name, len(inside))
