@@ -74,6 +74,13 @@ def _type(t, what):
     return ty
 
 
+def _count(n, what):
+    """n, which the library takes as 32 bits (ctypes would cut a larger one off)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{what} = {n} does not fit 32 bits")
+    return n
+
+
 # Every call checks every tensor.  A small compiled module makes the checks and the call
 # together (2 to 3 microseconds less than Python takes); where it has not been built, or a
 # check does not hold, the same rules are gone through below, which say what is wrong.
@@ -201,6 +208,8 @@ class PagedKV:
         pages, P, K, D = k.shape
         if not k.numel():
             raise ValueError(f"k and v are empty ({tuple(k.shape)})")
+        for n, what in zip(k.shape, ("num_pages", "page_size", "kv_heads", "head_dim")):
+            _count(n, what)
         # a dimension of one entry may have any stride; give the library a valid one
         st = [s if n > 1 else max(D, 8) for n, s in zip(k.shape[:3], k.stride()[:3])]
         cells = sorted((s, n) for n, s in zip(k.shape[:3], k.stride()[:3]) if n > 1)
@@ -238,7 +247,7 @@ class KVPages:
     def __init__(self, block_table, free_pages, free_top, page_size):
         if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[1] < 1:
             raise ValueError("block_table must be int32 [n_req, max_blocks >= 1]")
-        n, blocks = block_table.shape
+        n, blocks = _count(block_table.shape[0], "n_req"), _count(block_table.shape[1], "max_blocks")
         _matrix(block_table, "block_table", torch.int32, n, blocks)
         _vector(free_pages, "free_pages", torch.int32, 1)
         _vector(free_top, "free_top", torch.int32, 1)
@@ -247,7 +256,7 @@ class KVPages:
         self.block_table, self.free_pages, self.free_top = block_table, free_pages, free_top
         self.n_req, self.max_blocks, self.page_size = n, blocks, int(page_size)
         ld = block_table.stride(0) if n > 1 else max(block_table.stride(0), blocks)
-        self.c = CKVPages(n, self.page_size, free_pages.numel(), blocks, ld, _ptr(block_table), _ptr(free_pages),
+        self.c = CKVPages(n, self.page_size, _count(free_pages.numel(), "num_pages"), blocks, ld, _ptr(block_table), _ptr(free_pages),
                           _ptr(free_top))
         self.ref, self.address = ctypes.byref(self.c), ctypes.addressof(self.c)
 
@@ -268,7 +277,7 @@ class KVPlan:
         def new(n):
             return torch.zeros(max(int(n), 1), dtype=torch.int32, device=device)
 
-        self.n_req, self.max_tokens = int(n_req), int(max_tokens)
+        self.n_req, self.max_tokens = _count(int(n_req), "n_req"), _count(int(max_tokens), "max_tokens")
         if self.n_req < 0 or self.max_tokens < 0:
             raise ValueError(f"n_req = {n_req}, max_tokens = {max_tokens}")
         if kv_end is not None:
@@ -292,6 +301,7 @@ class Rope:
     def __init__(self, inv_freq, axis=None, axes=1, interleaved=False):
         _vector(inv_freq, "inv_freq", torch.float32, 0)
         half = inv_freq.numel()
+        _count(2 * half, "rot_dim")
         if axis is not None:
             _vector(axis, "axis", torch.int32, half)
         if half % 8 or not 1 <= axes <= MAX_AXES:
@@ -316,7 +326,8 @@ class _NoRope:
 def workspace(n_rows, heads, kv_heads, head_dim, device="cuda"):
     """A zeroed workspace for lora_paged_attention calls of up to n_rows rows and this head
     layout (the library leaves its counters zero after every call)."""
-    n = int(B.lib().lora_paged_attention_bytes(int(n_rows), int(heads), int(kv_heads), int(head_dim)))
+    n = int(B.lib().lora_paged_attention_bytes(_count(int(n_rows), "n_rows"), _count(int(heads), "heads"),
+                                               _count(int(kv_heads), "kv_heads"), _count(int(head_dim), "head_dim")))
     if n == 0:
         raise ValueError(f"{heads} query heads over {kv_heads} key/value heads of {head_dim}, {n_rows} rows")
     return torch.zeros(n // 4, dtype=torch.int32, device=device)
@@ -363,14 +374,14 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
             return
     dt, D = cache.dtype, cache.head_dim
     _vector(slots, "slots", torch.int32, 0)
-    n = slots.numel()
+    n = _count(slots.numel(), "n_rows")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     heads = ldq = ldqo = 0
     if q is not None:
         if q.dim() != 2 or q.shape[1] % D:
             raise ValueError(f"q is {tuple(q.shape)}, its columns must be heads of {D}")
-        heads = q.shape[1] // D
+        heads = _count(q.shape[1] // D, "heads")
         ldq = _matrix(q, "q", dt, n, heads * D)
         ldqo = _matrix(q_out, "q_out", dt, n, heads * D)
     ldk = _matrix(k, "k", dt, n, cache.kv_heads * D)
@@ -407,12 +418,14 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
     if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.shape[1] % D:
         raise ValueError(f"q must be [n_rows, heads * {D}]")
     n, cols = q.shape
-    heads = cols // D
+    heads = _count(cols // D, "heads")
+    _count(n, "n_rows")
+    window = _count(int(window), "window")
     ldq = _matrix(q, "q", dt, n, cols)
     ldo = _matrix(out, "out", dt, n, cols)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [n_req, max_blocks]")
-    n_req, blocks = block_table.shape
+    n_req, blocks = _count(block_table.shape[0], "n_req"), _count(block_table.shape[1], "max_blocks")
     _matrix(block_table, "block_table", torch.int32, n_req, blocks)
     ldt = block_table.stride(0) if n_req > 1 else max(blocks, 1)
     _vector(kv_len, "kv_len", torch.int32, n)
@@ -424,7 +437,7 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
     dev = _here("q out block_table kv_len req lse work cache.k", q, out, block_table, kv_len, req, lse, work, cache.k)
     _call("lora_paged_attention", _raw(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
                                           cache.ref, n_req, block_table.data_ptr(), ldt, blocks, kv_len.data_ptr(),
-                                          _ptr(req), float(scale), int(window),
+                                          _ptr(req), float(scale), window,
                                           _ptr(lse), work.data_ptr(), 4 * work.numel())
 
 
@@ -440,7 +453,7 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
     ty = _type(res, "res")
     if res.dim() != 2:
         raise ValueError(f"res must be 2-D (got {res.dim()}-D)")
-    n, h = res.shape
+    n, h = _count(res.shape[0], "n_rows"), _count(res.shape[1], "hidden")
     dt = res.dtype
     ldr = _matrix(res, "res", dt, n, h)
     yp = ldy = wp = rp = ldro = xp = ldx = pp = gp = ldg = ip = n_gates = 0
@@ -458,7 +471,7 @@ def lora_residual_norm(y, res, w=None, x=None, res_out=None, post_w=None, gate=N
         _vector(post_w, "post_w", dt, h)
         pp = post_w.data_ptr()
     if gate is not None:
-        ldg, gp, n_gates = _matrix(gate, "gate", dt, 1, h), gate.data_ptr(), gate.shape[0]
+        ldg, gp, n_gates = _matrix(gate, "gate", dt, 1, h), gate.data_ptr(), _count(gate.shape[0], "n_gates")
     if gate_idx is not None:
         _vector(gate_idx, "gate_idx", torch.int32, n)
         ip = gate_idx.data_ptr()

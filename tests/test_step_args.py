@@ -360,6 +360,48 @@ def test_descriptors_reject_wrong_layouts():
         S.Rope(torch.ones(16), axes=5)
 
 
+def test_counts_that_pass_32_bits_are_refused(monkeypatch):
+    """The library's counts are 32 bits, and ctypes would cut a larger one off: 2^32 + 8 rows would
+    be a call on 8 of them.  (Tensors without memory; nothing is called.)"""
+    far, h, i32 = 2 ** 32 + 8, torch.float16, torch.int32
+    monkeypatch.setattr(S, "_here", lambda *a: 0)
+    monkeypatch.setattr(S, "_raw", lambda *a: None)
+    calls = []
+    monkeypatch.setattr(S, "_call", lambda *a: calls.append(a))
+    e = lambda *shape, dt=i32: torch.empty(shape, dtype=dt, device="meta")
+    cache = S.PagedKV(torch.zeros(4, 16, 2, 64, dtype=h), torch.zeros(4, 16, 2, 64, dtype=h))
+    for make, what in ((lambda: S.PagedKV(e(far, 1, 1, 8, dt=h), e(far, 1, 1, 8, dt=h)), "num_pages"),
+                       (lambda: S.PagedKV(e(1, 1, far, 8, dt=h), e(1, 1, far, 8, dt=h)), "kv_heads"),
+                       (lambda: S.KVPages(e(2, 4), e(far), e(1), 16), "num_pages"),
+                       (lambda: S.KVPages(e(far, 4), e(8), e(1), 16), "n_req"),
+                       (lambda: S.KVPages(e(2, far), e(8), e(1), 16), "max_blocks"),
+                       (lambda: S.KVPlan(4, far, device="meta"), "max_tokens"),
+                       (lambda: S.KVPlan(far, 4, device="meta"), "n_req"),
+                       (lambda: S.Rope(e(far, dt=torch.float32)), "rot_dim"),
+                       (lambda: S.workspace(far, 4, 2, 64, device="meta"), "n_rows"),
+                       (lambda: S.workspace(4, 4, 2, far, device="meta"), "head_dim")):
+        with pytest.raises(ValueError, match=what):
+            make()
+    attn = dict(out=e(far, 256, dt=h), q=e(far, 256, dt=h), cache=cache, block_table=e(far, 4), kv_len=e(far), work=e(64))
+    for kw, what in ((attn, "n_rows"), ({**attn, "q": e(2, 256, dt=h)}, "n_req"),
+                     ({**attn, "q": e(2, 256, dt=h), "block_table": e(2, far)}, "max_blocks"),
+                     ({**attn, "q": e(2, 256, dt=h), "block_table": e(2, 4), "window": far}, "window"),
+                     ({**attn, "q": e(2, 64 * far, dt=h), "out": e(2, 64 * far, dt=h), "block_table": e(2, 4)}, "heads")):
+        with pytest.raises(ValueError, match=what):
+            S.lora_paged_attention(**kw)
+    kv = dict(k=e(far, 128, dt=h), v=e(far, 128, dt=h), cache=cache, slots=e(far))
+    for kw, what in (({**kv, "q_out": None, "q": None}, "n_rows"),
+                     ({**kv, "slots": e(2), "q_out": e(2, 64 * far, dt=h), "q": e(2, 64 * far, dt=h)}, "heads")):
+        with pytest.raises(ValueError, match=what):
+            S.lora_rope_append(**kw)
+    for res, what in ((e(far, 64, dt=h), "n_rows"), (e(2, far, dt=h), "hidden")):
+        with pytest.raises(ValueError, match=what):
+            S.lora_residual_norm(res, res, w=e(res.shape[1], dt=h))
+    with pytest.raises(ValueError, match="n_gates"):
+        S.lora_residual_norm(e(2, 64, dt=h), e(2, 64, dt=h), w=e(64, dt=h), x=e(2, 64, dt=h), gate=e(far, 64, dt=h), gate_idx=e(2))
+    assert not calls
+
+
 # ------------------------------------------------------------------ the references
 def test_plan_reference_on_a_worked_example():
     # pages of 4 tokens; request 0 grows from 3 to 5, request 1 (6 tokens) ends, request 2 starts with 2
