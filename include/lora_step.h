@@ -16,6 +16,9 @@
  * makes its row, token or page a no-op instead of an out-of-bounds access.  Every call
  * may be captured into a graph and replayed with new metadata in the same arrays.  The
  * diagnostics of lora_sgmv.h (launch events, plans) apply to the add-on's launches only.
+ * A launch has at most 2^32 - 1 threads: the calls with a workgroup of 64 to 1024 threads
+ * per row (lora_rope_append, lora_residual_norm) refuse more rows than that holds, which is
+ * never fewer than 2^22 - 1.
  *
  * Types: `type` is LORA_TYPE_F16 (IEEE binary16) or LORA_TYPE_BF16 for all 16-bit data
  * of a call.  Arithmetic is fp32 (sums, softmax statistics, norms), angles are 64-bit;

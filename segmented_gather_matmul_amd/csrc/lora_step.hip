@@ -1297,6 +1297,14 @@ int check_apart(const void *out, int64_t ldo, int64_t cols_o, const void *in, in
     return fail(LORA_E_SHAPE, "%s overlap", what);
 }
 
+// A launch of one workgroup per row has at most 2^32 - 1 threads along its rows.
+int check_rows(int32_t n_rows, int threads)
+{
+    if ((int64_t)n_rows * threads > UINT32_MAX)
+        return fail(LORA_E_UNSUPPORTED, "%d rows of %d threads are too many for one launch", n_rows, threads);
+    return LORA_OK;
+}
+
 // The arrays that a plan writes share no entry with each other or with those it reads, but
 // that kv_end may be kv_len and free_top the pages' own: its workgroups each read all the
 // lengths, at times of their own.
@@ -1474,6 +1482,7 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
     const dim3 grid((unsigned)n_rows, (unsigned)blocks);
     // a row of few units (one GPU's shard of 64/8 heads has 88) in as few wavefronts
     const int threads = (int)std::min<int64_t>((units + 63) / 64 * 64, 256);
+    if ((st = check_rows(n_rows, threads))) return st;
 #define LORA_APPEND(T, INTER)                                                                      \
     (stream_out ? launch(lora_rope_append_kernel<T, INTER, true>, grid, threads, 0, s, a)         \
                 : launch(lora_rope_append_kernel<T, INTER, false>, grid, threads, 0, s, a))
@@ -1612,6 +1621,7 @@ int lora_residual_norm(void *stream, const lora_norm_args *args)
     // gate: 64 us against 54).
     int threads = 64;
     while (threads < 1024 && (threads < 512 ? threads : 2 * threads) < chunks) threads *= 2;
+    if ((st = check_rows(a.n_rows, threads))) return st;
     const int nc = (chunks + threads - 1) / threads;
     const bool stream_out = 2 * (int64_t)a.n_rows * a.hidden * ((a.y ? 1 : 0) + (a.res_out ? 1 : 0)) > kStreamBytes;
     const dim3 grid((unsigned)a.n_rows);

@@ -236,6 +236,20 @@ def test_norm_refusals(kw, code):
     assert _norm(n_rows=0) == B.LORA_OK
 
 
+def test_launches_of_more_threads_than_a_grid_holds_are_refused():
+    """A launch has at most 2^32 - 1 threads along its rows."""
+    far, n = PTR + (1 << 45), 1 << 22      # rows of more than 8192 columns take 1024 threads each
+    for rows, hidden in ((n, 8200), (n, 65536), (1 << 23, 4104), (2 ** 31 - 1, 4096), (1 << 26, 8)):
+        ld = hidden
+        assert _norm(n_rows=rows, hidden=hidden, y=None, res_out=far, x=None, ldro=ld, ldr=ld) == B.LORA_E_UNSUPPORTED
+        assert str(rows) in B.last_error()
+    cache = _cache(num_pages=1, kv_heads=32, head_dim=128, token_stride=4096, head_stride=128, page_stride=65536)
+    for rows, heads in ((1 << 24, 0), (2 ** 31 - 1, 0), (1 << 24, 32)):
+        assert _append(n=rows, heads=heads, qo=far, ldqo=4096, q=PTR, ldq=4096, k=2 * far, ldk=4096, v=3 * far, ldv=4096,
+                       cache=cache, rope=S.CRope(0, 1, 0, 0, None, None)) == B.LORA_E_UNSUPPORTED
+        assert str(rows) in B.last_error()
+
+
 def test_null_descriptors():
     assert _code("lora_residual_norm", None, None) == B.LORA_E_NULL
     assert _code("lora_kv_plan", None, None, PTR, PTR, None, None) == B.LORA_E_NULL
