@@ -193,6 +193,10 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int32_t *tp = g.ints(7, n_req, blocks, ldt);
     const void *len = g.vector(8, kI32, rows), *req = g.vector(10, kI32, rows, true);
     void *lse = g.vector(13, kF32, rows * heads, true), *work = g.vector(9, kI32, 1);
+    if (g.ok && lse && rows > 1) {  // written as [rows, heads]
+        const at::Tensor &l = THPVariable_Unpack(args[13]);
+        if (l.dim() > 1 && l.numel() != l.size(0) * heads) Py_RETURN_NONE;
+    }
     const float scale = g.real(11);
     const int64_t window = g.number(12);
     if (!g.ok || rows > INT32_MAX || heads > INT32_MAX || n_req > INT32_MAX || blocks > INT32_MAX || window < 0 ||

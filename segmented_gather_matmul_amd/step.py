@@ -433,6 +433,8 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
         _vector(req, "req", torch.int32, n)
     if lse is not None:
         _vector(lse, "lse", torch.float32, n * heads)
+        if n > 1 and lse.dim() > 1 and lse.numel() != lse.shape[0] * heads:
+            raise ValueError(f"lse is {tuple(lse.shape)}, its rows must be of {heads} heads")
     _vector(work, "work", torch.int32, 1)
     dev = _here("q out block_table kv_len req lse work cache.k", q, out, block_table, kv_len, req, lse, work, cache.k)
     _call("lora_paged_attention", _raw(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,

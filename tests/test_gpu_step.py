@@ -974,3 +974,20 @@ def test_other_threads_run_while_a_compiled_call_waits():
         assert end - begin > us * 0.9e-6, name
         inside = [t for t in ticks if begin + 0.02 < t < end - 0.02]
         assert len(inside) >= 5, (name, len(inside))
+
+
+def test_an_lse_of_other_columns_is_refused_either_way(monkeypatch):
+    say("case lse-columns")
+    c = AttnCase([5, 6], 4, 2, 64, 16, F16, seed=1, garbage=False)
+    q, tab, ln, work = c.q.cuda(), c.table.cuda(), ints([5, 6]), S.attention_workspace(2, 4, c.cache)
+    out, lse = torch.zeros_like(q), torch.zeros(2, 4, device="cuda")
+    S.lora_paged_attention(out, q, c.cache, tab, ln, work, lse=lse)
+    for again in range(2):
+        for shape in ((3, 4), (8,), (2, 2, 2)):
+            got = torch.zeros(shape, device="cuda")
+            S.lora_paged_attention(out, q, c.cache, tab, ln, work, lse=got)
+            assert torch.equal(got.flatten()[:8], lse.flatten())
+        for shape in ((2, 8), (4, 2), (1, 8)):
+            with pytest.raises(ValueError, match="lse is"):
+                S.lora_paged_attention(out, q, c.cache, tab, ln, work, lse=torch.zeros(shape, device="cuda"))
+        monkeypatch.setattr(S, "_fast", None)

@@ -374,6 +374,22 @@ def test_descriptors_reject_wrong_layouts():
         S.Rope(torch.ones(16), axes=5)
 
 
+def test_an_lse_of_other_columns_is_refused():
+    """It is written as [n_rows, heads]: in a wider array the rows would not be where they are read."""
+    h = torch.float16
+    cache = S.PagedKV(torch.zeros(4, 16, 2, 64, dtype=h), torch.zeros(4, 16, 2, 64, dtype=h))
+    q, tab, n, w = torch.zeros(2, 256, dtype=h), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(64, dtype=torch.int32)
+    call = lambda lse: S.lora_paged_attention(q.clone(), q, cache, tab, n, w, lse=lse)
+    for shape in ((2, 8), (4, 2), (2, 5), (1, 8), (2, 2, 4)):
+        with pytest.raises(ValueError, match="lse is"):
+            call(torch.zeros(shape))
+    for shape in ((2, 4), (3, 4), (8,), (9,), (2, 2, 2), (2, 4, 1)):     # rows of one head after another
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call(torch.zeros(shape))
+    with pytest.raises(ValueError, match="GPU tensor"):                   # (one row begins where the array does)
+        S.lora_paged_attention(q[:1].clone(), q[:1], cache, tab, n, w, lse=torch.zeros(1, 9))
+
+
 def test_counts_that_pass_32_bits_are_refused(monkeypatch):
     """The library's counts are 32 bits, and ctypes would cut a larger one off: 2^32 + 8 rows would
     be a call on 8 of them.  (Tensors without memory; nothing is called.)"""
