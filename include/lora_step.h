@@ -71,7 +71,7 @@ typedef struct lora_kv_cache {
  * [0, *free_top) are the free ids, the last one is taken first.
  */
 typedef struct lora_kv_pages {
-    int32_t n_req;         /* rows of the batch's tables (>= 0) */
+    int32_t n_req;         /* rows of the batch's tables: 0..2^30 */
     int32_t page_size;     /* a power of two, 1..LORA_KV_MAX_PAGE */
     int32_t num_pages;     /* capacity of free_pages (>= 1) */
     int32_t max_blocks;    /* entries of a table row (>= 1); max_blocks * page_size <= 2^31 - 1 */

@@ -100,6 +100,7 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;  // requests planned at a time
 constexpr int kPlanGroups = 256;    // workgroups of a launch at most: one per CU
+constexpr int32_t kPlanMaxReq = 1 << 30;  // requests: the sum of two of their numbers fits 32 bits
 
 // One request of a plan; `bad` holds its LORA_KV_* bits.
 struct PlanReq {
@@ -1359,7 +1360,8 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
     a.shift = page_shift(pages->page_size);
     if (a.shift < 0)
         return fail(LORA_E_SHAPE, "page_size = %d is not a power of two in 1..%d", pages->page_size, LORA_KV_MAX_PAGE);
-    if (pages->n_req < 0 || pages->num_pages < 1 || (int64_t)pages->num_pages * pages->page_size > INT32_MAX)
+    if (pages->n_req < 0 || pages->n_req > kPlanMaxReq || pages->num_pages < 1 ||
+        (int64_t)pages->num_pages * pages->page_size > INT32_MAX)
         return fail(LORA_E_SHAPE, "n_req = %d, num_pages = %d of %d tokens", pages->n_req, pages->num_pages,
                     pages->page_size);
     // no request that fits its row then ends beyond a 32-bit position

@@ -207,6 +207,15 @@ def test_plan_tables_lie_apart_from_the_other_arrays():
                 assert meets(at, what, ld) == bool(entries & set(range(at, at + n))), (what, ld, at, B.last_error())
 
 
+def test_plans_of_more_requests_than_an_index_can_halve_are_refused():
+    """The search of q_ptr adds two request numbers, and the walk of the requests steps past the last
+    one: both are 32 bits."""
+    far = {x: PTR + ((i + 1) << 40) for i, x in enumerate(["status", "kv_end", "free_top", "q_ptr", "tok_req", "tok_pos", "slots",
+                                                            "idx", "kv", "new", "old_top", "free_pages", "table"])}
+    for n in ((1 << 30) + 1, 2 ** 31 - 1025, 2 ** 31 - 1):
+        assert _apart_plan(dict(n_req=n), **far) == B.LORA_E_SHAPE and "n_req" in B.last_error(), (n, B.last_error())
+
+
 def test_plan_needs_its_lengths():
     assert _plan(kv=None) == B.LORA_E_NULL and _plan(new=None) == B.LORA_E_NULL
 
