@@ -1556,7 +1556,7 @@ int lora_paged_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
     // no row is longer than its table or the window, and no share shorter than kAttnMinShare
     const int64_t span = std::min<int64_t>((int64_t)max_blocks * cache->page_size, window > 0 ? window : INT32_MAX);
     const int64_t line = n_rows * ((span + kAttnTile - 1) / kAttnTile + kAttnRowTiles);
-    if (line > INT32_MAX)
+    if (line > INT32_MAX - most)  // (rounded up to whole shares)
         return fail(LORA_E_UNSUPPORTED, "%d rows of up to %lld tokens", n_rows, (long long)span);
     a.shares = (int32_t)std::min<int64_t>(most, (line + kAttnMinShare - 1) / kAttnMinShare);
     a.scale = scale;

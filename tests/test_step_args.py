@@ -95,6 +95,14 @@ def test_attention_refusals(kw, code):
     assert _attn(**kw) == code
 
 
+def test_attention_lines_that_pass_32_bits_are_refused():
+    """The rows' tiles and four more each lie on one line of 32-bit positions, and its length is
+    rounded up to whole shares of it: there is room for that too."""
+    for rows, tiles in ((66, 32537627), (66, 32537628), (64, 1 << 25), (66, 32537627 - 3)):   # 2^31 - 2, past it; 200 short of it with 256 shares
+        code = _attn(n_rows=rows, cache=_cache(page_size=1), blocks=32 * tiles, ldt=32 * tiles, out=PTR + (1 << 40))
+        assert code == B.LORA_E_UNSUPPORTED, (rows, tiles, code, B.last_error())
+
+
 def test_attention_of_no_rows_is_nothing():
     assert _attn(n_rows=0, q=None, out=None, kv_len=None, work=None) == B.LORA_OK
 
