@@ -110,7 +110,8 @@ class PagedStep:
     """The serving state that every layer's paged step shares: up to n_req requests, their
     cached lengths (kv_len), adapter slots (req_slot, -1 = none), pages (of page_size tokens,
     num_pages of them, at most max_blocks a request) and the plan of the current step over at
-    most max_tokens token rows.  rope: a step.Rope or None.
+    most max_tokens token rows.  rope: a step.Rope of one axis (a row's position is its place in
+    its request) or None.  A step and its layers belong on one stream: they share a workspace.
 
     begin(new_len) plans a step on the device: new_len (int32 [n_req], on the device) tokens
     for each request, -1 for one that has ended.  Token rows are in request order
@@ -121,6 +122,9 @@ class PagedStep:
                  device="cuda"):
         import torch
         from . import step as S
+        if rope is not None and (rope.axes != 1 or rope.rot_dim > shape.head_dim):
+            raise ValueError(f"a rope of {rope.axes} axes over {rope.rot_dim} columns: the rows have one position, the "
+                             f"heads {shape.head_dim} columns")
         self.shape, self.n_req, self.max_tokens, self.rope = shape, int(n_req), int(max_tokens), rope
         self.pages = S.KVPages.fresh(n_req, max_blocks, num_pages, page_size, device)
         self.kv_len = torch.zeros(max(self.n_req, 1), dtype=torch.int32, device=device)

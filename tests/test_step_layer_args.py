@@ -39,3 +39,15 @@ def test_a_cache_of_another_geometry_is_refused(layer, kw):
     for fits in (_cache(), _cache(pages=7), step.new_cache(device="cpu")):
         with pytest.raises(ValueError, match="GPU tensor"):       # goes on to the first operator
             layer.forward_paged(hidden, fits, step, None)
+
+
+def test_a_step_refuses_a_rope_it_has_no_positions_for():
+    """A step's rows have one position each (plan.tok_pos), and heads of head_dim columns: refused
+    where the step is made, not in a layer after a plan has moved pages."""
+    make = lambda rope: LY.PagedStep(SHAPE, 2, T, 3, 6, 8, rope=rope, device="cpu")
+    for rope in (None, S.Rope.base(D, device="cpu"), S.Rope.base(D // 2, interleaved=True, device="cpu"),
+                 S.Rope.base(D, axis=torch.zeros(D // 2, dtype=torch.int32), device="cpu")):
+        assert make(rope).rope is rope
+    for rope, msg in ((S.Rope.base(D, axes=2, device="cpu"), "axes"), (S.Rope.base(2 * D, device="cpu"), "columns")):
+        with pytest.raises(ValueError, match=msg):
+            make(rope)
