@@ -9,9 +9,9 @@
  *
  * The conventions of lora_sgmv.h hold: the caller owns every buffer; calls are
  * asynchronous on `stream`, allocate nothing, never synchronise and keep no state; all
- * device pointers to 16- and 32-bit floating data are 16-byte aligned; arguments are
- * checked on the host before any launch, and LORA_OK or a negative LORA_E_* code is
- * returned (lora_last_error() describes it).  Device-resident metadata (lengths, slots,
+ * device pointers to 16-bit data are 16-byte aligned (lse, inv_freq and the int32 arrays 4);
+ * arguments are checked on the host before any launch, and LORA_OK or a negative LORA_E_*
+ * code is returned (lora_last_error() describes it).  Device-resident metadata (lengths, slots,
  * page ids) is read without a host check, and an entry outside its documented range
  * makes its row, token or page a no-op instead of an out-of-bounds access.  Every call
  * may be captured into a graph and replayed with new metadata in the same arrays.  The
@@ -152,9 +152,9 @@ typedef struct lora_rope {
  * Rows with another slot (-1: no token) leave q_out and the cache as they were.
  * q, k, v: device [n_rows][ld*], ld % 8 == 0 (column slices of one product are fine);
  * q_out may be q itself (same leading dimension), and must not overlap the inputs
- * otherwise.  q and q_out may both be NULL with q_heads 0.  positions: device int32
- * [n_axes][ld_pos], ld_pos >= n_rows (NULL allowed when rot_dim is 0).  Two rows of one
- * call must not name the same slot.
+ * otherwise; none of the four may overlap the cache.  q and q_out may both be NULL with
+ * q_heads 0.  positions: device int32 [n_axes][ld_pos], ld_pos >= n_rows (NULL allowed when
+ * rot_dim is 0).  Two rows of one call must not name the same slot.
  */
 int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out, int64_t ldqo, const void *q,
                      int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv, const lora_rope *rope,
@@ -174,7 +174,14 @@ int lora_rope_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out,
  * or every s_t = -inf) gets out = 0 and lse = -inf.  Rows with n < 0, n > max_blocks *
  * page_size or r outside [0, n_req) are not active: out and lse stay as they were there.
  * Several rows may name one request (each with its own n), e.g. the tokens of a guess
- * that is being verified.
+ * that is being verified; each row reads its tokens for itself.
+ * Softmax weights multiply v as two 16-bit parts: bf16 keeps 16 bits of a weight, fp16 22 bits
+ * and never less than 2^-37 of the row's largest one, so that beside the rounding of the
+ * output, n visible tokens put an fp16 row off by up to n 2^-37 max_t |v_t| (half an fp16
+ * step of that maximum at n = 2^26).
+ * n_rows times the tiles of the longest row that max_blocks (or the window) allows, 32 tokens
+ * each and four more a row, stays 512 below 2^31, or the call is refused
+ * (LORA_E_UNSUPPORTED): 63 rows at 2^30 tokens, 65,000 at 2^20.
  *
  *   out, q       device [n_rows][ld], ld % 8 == 0, ld >= q_heads * head_dim; the cache's type
  *   q_heads      a multiple of kv_heads

@@ -1,6 +1,11 @@
 // HIP kernels (gfx950 / CDNA4) and launchers of the decode-step operators beside the
 // add-on: the step plan, rotary positions with the append to the paged cache, attention
 // over that cache, and the residual add with its norms (lora_step.h).
+//
+// Times in comments: what a kernel takes now is the median of its kernel trace; figures with
+// an alternative or an earlier form beside them were taken together, as launches of a
+// captured graph (the two ways differ by up to 0.5 us for the smallest kernels and by 5 %
+// for the others).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -245,8 +250,8 @@ __device__ inline void plan_status(const PlanArgs &a, const PlanSums &s, int32_t
 // taken from that request's table row.  Lengths and free top are written by workgroup 0,
 // or, where they are updated in place and there are more workgroups, by a second launch.
 // Bound by the latency of its chain of loads (lengths, then ids), so small batches run in
-// few wavefronts, whose barriers are cheap: 32 decoding requests 3.9 us (1024 threads: 5.2),
-// 509 requests with 9,000 token rows 6.6 us.
+// few wavefronts, whose barriers are cheap: 32 decoding requests 3.7 us (in a graph 3.9, with
+// 1024 threads 5.2), 509 requests with 9,400 token rows 6.4 us.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void lora_kv_plan_kernel(PlanArgs a)
 {
@@ -309,7 +314,8 @@ __global__ __launch_bounds__(THREADS) void lora_kv_plan_kernel(PlanArgs a)
 
 // The plan of more requests than one chunk holds, by one workgroup: totals and checks first,
 // then, a chunk at a time, the pages of ended requests onto the free list, and after all
-// of those the pages of growing ones off it.
+// of those the pages of growing ones off it.  4096 requests, 13,400 pages and 6,850 token rows:
+// 33 us, and 5.6 for the maps.
 __global__ __launch_bounds__(kPlanThreads) void lora_kv_plan_chunks_kernel(PlanArgs a)
 {
     constexpr int THREADS = kPlanThreads;
@@ -425,8 +431,9 @@ __device__ inline float2 turn_of(int32_t pos, float inv_freq)
 // whole pairs).  A thread asks for its first chunks first; while they are on their way, the
 // row's cos and sin are worked out, once, into LDS.  Bound by reading q, k, v and writing
 // q_out and the cells: 12,907 rows of the 7B layout 114 us (5.55 TB/s), 4001 rows of the
-// 70B layout on three axes 26 us (6.3 TB/s), 12,000 rows of 8/1 heads 13.9 us (4.4 TB/s, a
-// workgroup of two wavefronts a row), 32 decode rows 3.2 us.  Four chunks a thread
+// 70B layout on three axes 25.7 us (6.4 TB/s: 82 MB in and 82 out, part of which stays in the
+// 256 MB cache beside the memory), 12,000 rows of 8/1 heads 14.4 us (4.3 TB/s, a
+// workgroup of two wavefronts a row), 32 decode rows 3.5 us.  Four chunks a thread
 // in flight from the start were slower on the large ones (125.5 and 37 us against 122 and
 // 36, before streaming stores).
 template <typename T, bool INTER, bool STREAM>
@@ -658,7 +665,9 @@ __device__ inline f4_t mfma(const vec8<BF16> &x, const vec8<BF16> &y, const f4_t
 // and neither 0, so that hi * v + lo * v is what p * v is for an infinite v too.  fp16 keeps
 // 22 bits (the bias lifts weights out of its subnormals, whose step is 2^-38 of the largest
 // weight; a weight of 0 counts as two such steps), bf16 16 bits: both far below the
-// rounding of the output.
+// rounding of the output.  The steps add up: n tokens of weights near or below them put an
+// fp16 output off by up to n 2^-37 max |v|, 2^-20 max |v| at 131,072 tokens, half an fp16
+// step of it (2^-11) at 2^26.
 template <typename T>
 struct Weight;
 template <>
@@ -835,11 +844,12 @@ __device__ inline void join_row(const AttnArgs &a, int32_t row, int32_t w0, int3
 //
 // Bound by reading K and V once; every head of a group shares the read, and 16 columns of
 // heads cost the same matrix instructions as one.  Measured (fp16, 128 columns): 32 rows of
-// 8192 tokens x 32 heads 711 us, 6.04 TB/s, what a plain read of the bytes reaches; 32 rows
-// of 64 to 4096 tokens 98 us, 5.2 TB/s; one row of 131,071 tokens, one key/value head 24 us
-// (13 us beyond the read: lengths, table and first K one after another, then two joins);
-// one row of 17 tokens 6.2 us.  Slower on those (98 / 24 / 6.2): two workgroups per CU 104 /
-// 24.4 / 6.4, three 145 / 37 / 9.2 (what is in flight queues up, and every row's first loads
+// 8192 tokens x 32 heads 724 us, 5.93 TB/s (a plain read of the bytes reaches 6.05); 32 rows
+// of 64 to 4096 tokens 97 us, 5.2 TB/s; one row of 131,071 tokens, one key/value head 23.7 us
+// (12.6 us beyond the read: the launch and lengths, table and first K one after another, which
+// are all of the 6.5 us that one row of 17 tokens takes, and two joins; other joins than of
+// kAttnJoin parts are not measured).  In a graph, slower than 98 / 24 / 6.2 us on the last
+// three: two workgroups per CU 104 / 24.4 / 6.4, three 145 / 37 / 9.2 (what is in flight queues up, and every row's first loads
 // wait behind it); eight wavefronts 105 / 27 / 9; 64-token tiles 104 / 26 / 8.2; one part
 // per row and workgroup, a dynamic grid and a second launch to join 122 / 104 / 13.9;
 // streaming loads 125 / 25 / 5.8 on that grid's successor (64-byte pieces of a row miss
@@ -1141,10 +1151,11 @@ __device__ inline float block_sum(float v, float *wave_sums)
 
 // One workgroup per row; a thread keeps its NC chunks of eight elements in registers from
 // the loads to the stores, so x and res are read once and res_out and y written once.
-// Bound by those: 12,907 rows of 4096 70.5 us (6.0 TB/s); 4001 rows of 8192 with both norms
-// and gates 51.5 us (5.1 TB/s, two sums over the row one after the other); 500 rows of
-// 65,536 52.6 us (5.0 TB/s; with the weights asked for early too, they spill: 283 us); 32
-// rows of 4096 2.9 us, a launch and one trip to memory.
+// Bound by those: 12,907 rows of 4096 70 us (6.0 TB/s); 4001 rows of 8192 with both norms
+// and gates 50 us (5.3 TB/s, two sums over the row one after the other); 500 rows of
+// 65,536 with both 57 us (4.6 TB/s; in a graph 53, and 283 with the weights asked for early
+// too, which spill); 32 rows of 4096 3.1 us, a launch and one trip to memory.  A row of fewer
+// than 512 columns leaves lanes of its wavefront idle (seven in eight at 64).
 template <typename T, int NC, bool STREAM>
 __global__ __launch_bounds__(1024) void
 lora_residual_norm_kernel(lora_norm_args a)
@@ -1388,10 +1399,11 @@ int lora_kv_plan(void *stream, const lora_kv_pages *pages, const int32_t *kv_len
         return launch_status("step plan");
     }
     // The work there may be: every token row, and every page that the tables can hold.  Up to
-    // two of these a thread, since every workgroup makes its sums at the same time (1000
-    // requests moving 240,000 one-token pages: 125 us in one workgroup, 7 in 256).  A plan
-    // in place would need the second launch then; while its token rows are few, so most
-    // likely are its pages, and one workgroup is faster.
+    // two of these a thread, since every workgroup makes its sums at the same time.  A plan
+    // in place would need the second launch then (2.9 us); while its token rows are few, so
+    // most likely are its pages, and one workgroup is faster.  Where they are not it is far
+    // slower: 1000 requests giving back 240,000 one-token pages, 504 token rows, 260 us in
+    // place against 7.2 with arrays of their own.
     const int64_t moves = out->max_tokens + std::min<int64_t>(pages->num_pages, (int64_t)n * pages->max_blocks);
     const bool in_place = out->kv_end == kv_len || out->free_top == pages->free_top;
     const bool small = n <= 64 && moves <= 1024, medium = n <= 256;
