@@ -124,6 +124,11 @@ def lib() -> ctypes.CDLL:
             "lora_paged_attention": [P, I32, I32, P, I64, P, I64, P, I32, P, I64, I32, P, P, ctypes.c_float, I32, P, P,
                                      ctypes.c_size_t],
             "lora_residual_norm": [P, P],
+            # lora_quant.h (marshalled by quant.py)
+            "lora_quant_append": [P, I32, I32, P, I64, P, I64, P, I64, P, I64, P, P, I64, P, P],
+            "lora_quant_read": [P, I32, P, I64, P, I64, P, P],
+            "lora_quant_attention": [P, I32, I32, P, I64, P, I64, P, I32, P, I64, I32, P, P, ctypes.c_float, I32, P, P,
+                                     ctypes.c_size_t],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -135,7 +140,8 @@ def lib() -> ctypes.CDLL:
                                 ("lora_pool_pages_for", [I32, I32, I32, I32], I64),
                                 ("lora_pool_load_header_bytes", [I32], ctypes.c_size_t),
                                 ("lora_handoff_bytes", [I32], ctypes.c_size_t),
-                                ("lora_paged_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t)):
+                                ("lora_paged_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t),
+                                ("lora_quant_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         L.lora_pick_tile_rows.restype = ctypes.c_int32

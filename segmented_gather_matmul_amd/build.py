@@ -9,6 +9,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,9 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
 SOURCES = [os.path.join(CSRC, "lora_kernels.hip"), os.path.join(CSRC, "lora_pool.hip"),
-           os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_host.cpp")]
-HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(INCLUDE, "lora_step.h"),
-           os.path.join(CSRC, "lora_internal.hpp")]
+           os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_quant.hip"), os.path.join(CSRC, "lora_host.cpp")]
+PUBLIC_HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(INCLUDE, "lora_step.h"),
+                  os.path.join(INCLUDE, "lora_quant.h")]
+HEADERS = PUBLIC_HEADERS + [os.path.join(CSRC, "lora_internal.hpp"), os.path.join(CSRC, "step_device.hpp")]
 ARCH = "gfx950"
 ARGS_LIB = os.path.join(PKG, "_step_args.so")
 ARGS_SOURCE = os.path.join(CSRC, "step_args.cpp")
@@ -32,7 +35,7 @@ def hipcc() -> str:
 
 
 def flags() -> list[str]:
-    return ["-O3", "-std=c++17", "-fPIC", "-shared", f"--offload-arch={ARCH}",
+    return ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
             # Packed FP32 instructions stay off: plain float code is compiled to scalar FP32 ops.
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             # Leading scalar kernel arguments (up to four; only the hand-off kernel has any
@@ -41,15 +44,23 @@ def flags() -> list[str]:
             "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *flags(), *SOURCES, "-o", tmp]
+def _hipcc(args, verbose):
+    cmd = [hipcc(), *flags(), *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("hipcc failed building liblora_sgmv.so")
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles the sources side by side, every one of them every time, and links them."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as work, ThreadPoolExecutor(4) as pool:
+        objects = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+        list(pool.map(lambda so: _hipcc(["-c", so[0], "-o", so[1]], verbose), zip(SOURCES, objects)))
+        _hipcc(["-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     build_args(verbose)
     return LIB
@@ -81,7 +92,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS) or \
-        any(os.path.getmtime(p) > os.path.getmtime(ARGS_LIB) for p in [ARGS_SOURCE, HEADERS[0], HEADERS[1]])
+        any(os.path.getmtime(p) > os.path.getmtime(ARGS_LIB) for p in [ARGS_SOURCE, *PUBLIC_HEADERS])
 
 
 if __name__ == "__main__":

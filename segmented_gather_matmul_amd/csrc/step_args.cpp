@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "lora_quant.h"
 #include "lora_step.h"
 
 namespace {
@@ -135,8 +136,8 @@ PyObject *status_of(Fn fn, A... a)
     return PyLong_FromLong(code);
 }
 
-#define STEP_ARGS(count)                                                                   \
-    if (n != count) return PyErr_Format(PyExc_TypeError, "%s takes %d arguments", __func__, count); \
+#define STEP_ARGS(name, count)                                                                   \
+    if (n != count) return PyErr_Format(PyExc_TypeError, "%s takes %d arguments", name, count); \
     Args g{args, 0};                                                                          \
     g.dev = g.number(2)
 
@@ -176,12 +177,13 @@ PyObject *here(PyObject *, PyObject *const *args, Py_ssize_t n)
 }
 
 // attention(function, stream, device, out, q, cache, cache k, block_table, kv_len, work, req, scale, window, lse)
-PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
+template <typename Fn, typename Cache>
+PyObject *attention_over(const char *name, PyObject *const *args, Py_ssize_t n)
 {
-    STEP_ARGS(14);
-    const auto fn = g.address<decltype(&lora_paged_attention)>(0);
+    STEP_ARGS(name, 14);
+    const auto fn = g.address<Fn>(0);
     void *const stream = g.address<void *>(1);
-    const auto *c = g.address<const lora_kv_cache *>(5);
+    const auto *c = g.address<const Cache *>(5);
     const at::Tensor *q = g.tensor(4), *table = g.tensor(7);
     if (!g.ok || q->dim() != 2 || table->dim() != 2 || q->size(1) % c->head_dim) Py_RETURN_NONE;
     const int64_t rows = q->size(0), cols = q->size(1), n_req = table->size(0), blocks = table->size(1);
@@ -209,13 +211,23 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
                      work, bytes);
 }
 
-// append(function, stream, device, q_out, q, k, v, cache, cache k, slots, rope, inv_freq, axis, positions)
-PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
+PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
-    STEP_ARGS(14);
-    const auto fn = g.address<decltype(&lora_rope_append)>(0);
+    return attention_over<decltype(&lora_paged_attention), lora_kv_cache>("attention", args, n);
+}
+PyObject *quant_attention(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return attention_over<decltype(&lora_quant_attention), lora_quant_cache>("quant_attention", args, n);
+}
+
+// append(function, stream, device, q_out, q, k, v, cache, cache k, slots, rope, inv_freq, axis, positions)
+template <typename Fn, typename Cache>
+PyObject *append_to(const char *name, PyObject *const *args, Py_ssize_t n)
+{
+    STEP_ARGS(name, 14);
+    const auto fn = g.address<Fn>(0);
     void *const stream = g.address<void *>(1);
-    const auto *c = g.address<const lora_kv_cache *>(7);
+    const auto *c = g.address<const Cache *>(7);
     const auto *rope = g.address<const lora_rope *>(10);
     const at::Tensor *slots = g.tensor(9), *q = g.tensor(4, true);
     if (!g.ok || (q == nullptr) != (args[3] == Py_None) || (q && (q->dim() != 2 || q->size(1) % c->head_dim))) Py_RETURN_NONE;
@@ -237,10 +249,37 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
                      static_cast<const int32_t *>(sp), c);
 }
 
+PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return append_to<decltype(&lora_rope_append), lora_kv_cache>("append", args, n);
+}
+PyObject *quant_append(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return append_to<decltype(&lora_quant_append), lora_quant_cache>("quant_append", args, n);
+}
+
+// quant_read(function, stream, device, k_out, v_out, slots, cache, cache k)
+PyObject *quant_read(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    STEP_ARGS("quant_read", 8);
+    const auto fn = g.address<decltype(&lora_quant_read)>(0);
+    void *const stream = g.address<void *>(1);
+    const auto *c = g.address<const lora_quant_cache *>(6);
+    const at::Tensor *slots = g.tensor(5);
+    g.tensor(7);
+    if (!g.ok) Py_RETURN_NONE;
+    const int64_t rows = slots->numel(), cols = (int64_t)c->kv_heads * c->head_dim;
+    int64_t ldk, ldv;
+    void *k = g.matrix(3, c->type, rows, cols, ldk, true), *v = g.matrix(4, c->type, rows, cols, ldv, true);
+    const void *sp = g.vector(5, kI32, rows);
+    if (!g.ok || rows > INT32_MAX) Py_RETURN_NONE;
+    return status_of(fn, stream, (int32_t)rows, k, ldk, v, ldv, static_cast<const int32_t *>(sp), c);
+}
+
 // norm(function, stream, device, y, res, w, x, res_out, post_w, gate, gate_idx, alpha, eps, w_offset)
 PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
-    STEP_ARGS(14);
+    STEP_ARGS("norm", 14);
     const auto fn = g.address<decltype(&lora_residual_norm)>(0);
     void *const stream = g.address<void *>(1);
     const at::Tensor *res = g.tensor(4);
@@ -312,7 +351,8 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n)
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {STEP_METHOD(matrix), STEP_METHOD(vector), STEP_METHOD(here),
                          STEP_METHOD(attention), STEP_METHOD(append), STEP_METHOD(norm),
-                         STEP_METHOD(plan), {nullptr, nullptr, 0, nullptr}};
+                         STEP_METHOD(plan), STEP_METHOD(quant_attention), STEP_METHOD(quant_append),
+                         STEP_METHOD(quant_read), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -111,7 +111,8 @@ class PagedStep:
     cached lengths (kv_len), adapter slots (req_slot, -1 = none), pages (of page_size tokens,
     num_pages of them, at most max_blocks a request) and the plan of the current step over at
     most max_tokens token rows.  rope: a step.Rope of one axis (a row's position is its place in
-    its request) or None.  A step and its layers belong on one stream: they share a workspace.
+    its request) or None.  kv_bits: 16 (caches of step.PagedKV), or 8 or 4 (quant.QuantKV, which
+    holds k and v quantised).  A step and its layers belong on one stream: they share a workspace.
 
     begin(new_len) plans a step on the device: new_len (int32 [n_req], on the device) tokens
     for each request, -1 for one that has ended.  Token rows are in request order
@@ -119,27 +120,36 @@ class PagedStep:
     the step does not fit; then nothing changes and the layers leave every cache as it is."""
 
     def __init__(self, shape: LlamaShape, n_req, max_tokens, max_blocks, num_pages, page_size=16, rope=None,
-                 device="cuda"):
+                 device="cuda", kv_bits=16):
         import torch
+        from . import quant as Q
         from . import step as S
+        if kv_bits not in (16, 8, 4):
+            raise ValueError(f"kv_bits = {kv_bits} is not 16, 8 or 4")
         if rope is not None and (rope.axes != 1 or rope.rot_dim > shape.head_dim):
             raise ValueError(f"a rope of {rope.axes} axes over {rope.rot_dim} columns: the rows have one position, the "
                              f"heads {shape.head_dim} columns")
         self.shape, self.n_req, self.max_tokens, self.rope = shape, int(n_req), int(max_tokens), rope
+        self.kv_bits = kv_bits
         self.pages = S.KVPages.fresh(n_req, max_blocks, num_pages, page_size, device)
         self.kv_len = torch.zeros(max(self.n_req, 1), dtype=torch.int32, device=device)
         self.req_slot = torch.full((self.n_req,), -1, dtype=torch.int32, device=device)
         self.plan = S.KVPlan(n_req, max_tokens, device, kv_end=self.kv_len, free_top=self.pages.free_top)
         self.row_len = torch.zeros(self.max_tokens, dtype=torch.int32, device=device)
-        self.work = S.workspace(max_tokens, shape.heads, shape.kv_heads or shape.heads, shape.head_dim, device)
+        workspace = S.workspace if kv_bits == 16 else Q.workspace
+        self.work = workspace(max_tokens, shape.heads, shape.kv_heads or shape.heads, shape.head_dim, device)
 
     def new_cache(self, dtype=None, device="cuda"):
         """An empty cache for one layer."""
         import torch
+        from . import quant as Q
         from . import step as S
         size = (self.pages.free_pages.numel(), self.pages.page_size, self.shape.kv_heads or self.shape.heads,
                 self.shape.head_dim)
-        zeros = lambda: torch.zeros(size, dtype=torch.float16 if dtype is None else dtype, device=device)
+        dtype = torch.float16 if dtype is None else dtype
+        if self.kv_bits != 16:
+            return Q.QuantKV.zeros(*size, dtype, self.kv_bits, device)
+        zeros = lambda: torch.zeros(size, dtype=dtype, device=device)
         return S.PagedKV(zeros(), zeros())
 
     def begin(self, new_len):
@@ -291,10 +301,12 @@ class LoraDecoderLayer:
     def forward_paged(self, hidden, cache, step: PagedStep, meta: BatchMeta | None, trace: dict | None = None):
         """hidden [step.max_tokens, h] fp16 -> the same, for the token rows of the step planned
         last; rows behind the last token are not read by any other row.  cache: this layer's
-        step.PagedKV, of the step's page size and heads and at least its number of pages.
+        step.PagedKV, or quant.QuantKV where the step's kv_bits is 8 or 4, of the step's page size and heads
+        and at least its number of pages.
         meta and trace as for forward (meta: BatchMeta.of_step)."""
         import torch
         import torch.nn.functional as F
+        from . import quant as Q
         from . import step as S
         s, bb = self.shape, self.bb
         h, f, kv = s.hidden, s.ffn, s.kv_width
@@ -307,16 +319,19 @@ class LoraDecoderLayer:
             raise ValueError(f"a cache of {cache.num_pages} pages of {cache.page_size} tokens, {cache.kv_heads} heads of "
                              f"{cache.head_dim} does not fit a step of {pages} pages of {P}, {kv // s.head_dim} heads of "
                              f"{s.head_dim}")
+        if (cache.bits if isinstance(cache, Q.QuantKV) else 16) != step.kv_bits:
+            raise ValueError(f"a {type(cache).__name__} does not fit a step of {step.kv_bits} bits")
         if meta is not None and meta.n != n:
             raise ValueError(f"metadata for {meta.n} rows, batch of {n}")
+        append, attention = ((S.lora_rope_append, S.lora_paged_attention) if step.kv_bits == 16
+                             else (Q.lora_quant_append, Q.lora_quant_attention))
 
         a = torch.empty_like(hidden)
         S.lora_residual_norm(a, hidden, bb["norm1"], eps=s.eps)
         q, k, v = self._project(meta, a, bb["w_qkv"], ("q", "k", "v"), (h, kv, kv))
         q_rot, attn = torch.empty_like(hidden), torch.zeros_like(hidden)   # zeros: rows of no request
-        S.lora_rope_append(q_rot, q, k, v, cache, step.plan.slots, rope=step.rope, positions=step.plan.tok_pos)
-        S.lora_paged_attention(attn, q_rot, cache, step.pages.block_table, step.row_len, step.work,
-                               req=step.plan.tok_req)
+        append(q_rot, q, k, v, cache, step.plan.slots, rope=step.rope, positions=step.plan.tok_pos)
+        attention(attn, q_rot, cache, step.pages.block_table, step.row_len, step.work, req=step.plan.tok_req)
         (o,) = self._project(meta, attn, bb["w_o"], ("o",), (h,))
         h1, a2 = torch.empty_like(hidden), torch.empty_like(hidden)
         S.lora_residual_norm(a2, hidden, bb["norm2"], x=o, res_out=h1, eps=s.eps)

@@ -372,6 +372,10 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
                                            cache.address, cache.k, slots, rope.address, rope.inv_freq, rope.axis,
                                            positions)):
             return
+    _append_checked("lora_rope_append", q_out, q, k, v, cache, slots, rope, positions, stream)
+
+
+def _append_checked(entry, q_out, q, k, v, cache, slots, rope, positions, stream):
     dt, D = cache.dtype, cache.head_dim
     _vector(slots, "slots", torch.int32, 0)
     n = _count(slots.numel(), "n_rows")
@@ -399,7 +403,7 @@ def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = 
         ldp = p2.stride(0) if p2.shape[0] > 1 else max(n, 1)
     dev = _here("slots k v q q_out positions cache.k inv_freq axis", slots, k, v, q, q_out, positions, cache.k,
                 rope.inv_freq, rope.axis)
-    _call("lora_rope_append", _raw(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
+    _call(entry, _raw(stream, dev), n, heads, _ptr(q_out), ldqo, _ptr(q), ldq, k.data_ptr(), ldk,
                                       v.data_ptr(), ldv, rope.ref, _ptr(positions), ldp, slots.data_ptr(), cache.ref)
 
 
@@ -408,13 +412,17 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
     """Attention of one query token per row: q and out [n_rows, heads * head_dim], block_table
     int32 [n_req, max_blocks], kv_len int32 [n_rows], req int32 [n_rows] or None (row i reads
     table row i), lse fp32 [n_rows, heads] or None, work from attention_workspace."""
-    dt, D = cache.dtype, cache.head_dim
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
     if _fast:
         dev = _device(q)
         if dev >= 0 and _done(_fast.attention(_address("lora_paged_attention"), _raw(stream, dev), dev, out, q,
                                               cache.address, cache.k, block_table, kv_len, work, req, scale, window, lse)):
             return
+    _attention_checked("lora_paged_attention", out, q, cache, block_table, kv_len, work, req, scale, window, lse, stream)
+
+
+def _attention_checked(entry, out, q, cache, block_table, kv_len, work, req, scale, window, lse, stream):
+    dt, D = cache.dtype, cache.head_dim
     if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.shape[1] % D:
         raise ValueError(f"q must be [n_rows, heads * {D}]")
     n, cols = q.shape
@@ -437,7 +445,7 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
             raise ValueError(f"lse is {tuple(lse.shape)}, its rows must be of {heads} heads")
     _vector(work, "work", torch.int32, 1)
     dev = _here("q out block_table kv_len req lse work cache.k", q, out, block_table, kv_len, req, lse, work, cache.k)
-    _call("lora_paged_attention", _raw(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
+    _call(entry, _raw(stream, dev), n, heads, out.data_ptr(), ldo, q.data_ptr(), ldq,
                                           cache.ref, n_req, block_table.data_ptr(), ldt, blocks, kv_len.data_ptr(),
                                           _ptr(req), float(scale), window,
                                           _ptr(lse), work.data_ptr(), 4 * work.numel())

@@ -1,0 +1,302 @@
+"""CPU: the quantised cache's C ABI and binding -- exports, every refusal that the host checks make before a launch,
+and the references the GPU tests compare against.  No test here launches a kernel."""
+import ctypes
+import importlib
+import math
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from segmented_gather_matmul_amd import binding as B
+from segmented_gather_matmul_amd import build as build_mod
+from segmented_gather_matmul_amd import layer as LY
+from segmented_gather_matmul_amd import quant as Q
+from segmented_gather_matmul_amd import step as S
+from tests import quant_ref as QR
+
+PTR = 0x10000   # an aligned address that is never followed: every call here is refused
+U8, F16 = torch.uint8, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if build_mod.stale():
+        build_mod.build()
+    if S._fast is None:
+        importlib.invalidate_caches()
+        S._fast = importlib.import_module("segmented_gather_matmul_amd._step_args")
+    return B.lib()
+
+
+def test_exports():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(build_mod.INCLUDE, "lora_quant.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(lora_[a-z0-9_]+)\s*\(", text))
+    assert names == set(Q.EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", build_mod.LIB], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (lora_\w+)", out))
+
+
+def test_the_descriptor_is_laid_out_as_in_the_header(tmp_path):
+    fields = [f[0] for f in Q.CQuantCache._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "lora_quant.h"\nint main(void) {\n'
+                   + "".join(f'printf("%zu ", offsetof(lora_quant_cache, {f}));\n' for f in fields)
+                   + 'printf("%zu\\n", sizeof(lora_quant_cache)); return 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", f"-I{build_mod.INCLUDE}", str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [getattr(Q.CQuantCache, f).offset for f in fields] + [ctypes.sizeof(Q.CQuantCache)]
+
+
+def _cache(**kw):
+    d = dict(type=0, bits=4, page_size=16, num_pages=8, kv_heads=2, head_dim=64, page_stride=1024, token_stride=64,
+             head_stride=32, exp_page_stride=64, exp_token_stride=4, exp_head_stride=2, k=PTR, v=PTR, k_exp=PTR, v_exp=PTR)
+    d.update(kw)
+    return Q.CQuantCache(*[d[f[0]] for f in Q.CQuantCache._fields_])
+
+
+def _code(fn, *args):
+    return getattr(B.lib(), fn)(*args)
+
+
+CACHE_FAULTS = [(dict(type=2), B.LORA_E_UNSUPPORTED), (dict(bits=16), B.LORA_E_UNSUPPORTED), (dict(bits=0), B.LORA_E_UNSUPPORTED),
+                (dict(page_size=0), B.LORA_E_SHAPE), (dict(page_size=12), B.LORA_E_SHAPE), (dict(page_size=2048), B.LORA_E_SHAPE),
+                (dict(num_pages=0), B.LORA_E_SHAPE), (dict(num_pages=1 << 28), B.LORA_E_SHAPE), (dict(kv_heads=0), B.LORA_E_SHAPE),
+                (dict(head_dim=0), B.LORA_E_SHAPE), (dict(head_dim=60), B.LORA_E_SHAPE), (dict(head_dim=264), B.LORA_E_SHAPE),
+                (dict(k=None), B.LORA_E_NULL), (dict(v=None), B.LORA_E_NULL), (dict(k_exp=None), B.LORA_E_NULL),
+                (dict(v_exp=None), B.LORA_E_NULL), (dict(k=PTR + 8), B.LORA_E_ALIGN), (dict(v=PTR + 1), B.LORA_E_ALIGN),
+                (dict(token_stride=16), B.LORA_E_SHAPE), (dict(bits=8, head_stride=32), B.LORA_E_SHAPE),
+                (dict(head_stride=40), B.LORA_E_ALIGN), (dict(page_stride=-1024), B.LORA_E_SHAPE),
+                (dict(exp_head_stride=1), B.LORA_E_SHAPE), (dict(exp_page_stride=-64), B.LORA_E_SHAPE),
+                (dict(page_stride=1 << 62), B.LORA_E_SHAPE), (dict(exp_token_stride=1 << 62), B.LORA_E_SHAPE),
+                (dict(exp_page_stride=(1 << 63) - 1), B.LORA_E_SHAPE)]
+
+
+@pytest.mark.parametrize("kw,code", CACHE_FAULTS, ids=lambda x: str(x))
+def test_bad_caches_are_refused(kw, code):
+    c, rope = _cache(**kw), S.CRope(0, 1, 0, 0, None, None)
+    assert _code("lora_quant_append", None, 1, 0, None, 0, None, 0, PTR, 128, PTR, 128, ctypes.byref(rope), None, 0, PTR,
+                 ctypes.byref(c)) == code
+    assert _code("lora_quant_read", None, 1, PTR, 128, PTR + 4096, 128, PTR, ctypes.byref(c)) == code
+    assert _code("lora_quant_attention", None, 1, 2, PTR, 128, PTR + 4096, 128, ctypes.byref(c), 1, PTR, 4, 4, PTR, None,
+                 1.0, 0, None, PTR, 1 << 30) == code
+    assert B.last_error()
+
+
+def _attn(**kw):
+    d = dict(n_rows=2, heads=4, out=PTR, ldo=256, q=PTR + 4096, ldq=256, cache=_cache(), n_req=2, table=PTR, ldt=4,
+             blocks=4, kv_len=PTR, req=None, scale=1.0, window=0, lse=None, work=PTR, work_bytes=1 << 30)
+    d.update(kw)
+    c = d["cache"]
+    return _code("lora_quant_attention", None, d["n_rows"], d["heads"], d["out"], d["ldo"], d["q"], d["ldq"],
+                 ctypes.byref(c) if c else None, d["n_req"], d["table"], d["ldt"], d["blocks"], d["kv_len"], d["req"],
+                 d["scale"], d["window"], d["lse"], d["work"], d["work_bytes"])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_rows=-1), B.LORA_E_SHAPE), (dict(n_req=-1), B.LORA_E_SHAPE), (dict(heads=3), B.LORA_E_SHAPE),
+    (dict(heads=0), B.LORA_E_SHAPE), (dict(cache=None), B.LORA_E_NULL), (dict(out=None), B.LORA_E_NULL),
+    (dict(q=None), B.LORA_E_NULL), (dict(q=PTR + 4098), B.LORA_E_ALIGN), (dict(ldq=255), B.LORA_E_SHAPE),
+    (dict(ldo=260), B.LORA_E_ALIGN), (dict(blocks=0), B.LORA_E_SHAPE), (dict(ldt=3), B.LORA_E_SHAPE),
+    (dict(blocks=(1 << 26) + 1, ldt=1 << 27), B.LORA_E_SHAPE), (dict(kv_len=None), B.LORA_E_NULL),
+    (dict(n_rows=1 << 17, blocks=1 << 26, ldt=1 << 26, out=PTR + (1 << 40)), B.LORA_E_UNSUPPORTED),
+    (dict(table=None), B.LORA_E_NULL), (dict(window=-1), B.LORA_E_SHAPE), (dict(scale=float("inf")), B.LORA_E_SHAPE),
+    (dict(scale=float("nan")), B.LORA_E_SHAPE), (dict(lse=PTR + 2), B.LORA_E_ALIGN), (dict(work=None), B.LORA_E_NULL),
+    (dict(work=PTR + 128), B.LORA_E_ALIGN), (dict(work_bytes=0), B.LORA_E_SHAPE), (dict(q=PTR + 16), B.LORA_E_SHAPE),
+    (dict(q=PTR), B.LORA_E_SHAPE), (dict(n_rows=1 << 29), B.LORA_E_SHAPE)], ids=lambda x: str(x))
+def test_attention_refusals(kw, code):
+    assert _attn(**kw) == code
+
+
+def test_calls_of_no_rows_are_nothing():
+    c, rope = _cache(), S.CRope(0, 1, 0, 0, None, None)
+    assert _attn(n_rows=0, q=None, out=None, kv_len=None, work=None) == B.LORA_OK
+    assert _code("lora_quant_read", None, 0, None, 0, None, 0, None, ctypes.byref(c)) == B.LORA_OK
+    assert _code("lora_quant_append", None, 0, 0, None, 0, None, 0, None, 0, None, 0, ctypes.byref(rope), None, 0, None,
+                 ctypes.byref(c)) == B.LORA_OK
+    assert B.lib().lora_quant_attention_bytes(-1, 4, 2, 64) == 0 and B.lib().lora_quant_attention_bytes(2, 3, 2, 64) == 0
+    assert B.lib().lora_quant_attention_bytes(2, 4, 2, 60) == 0 and B.lib().lora_quant_attention_bytes(2, 4, 2, 64) > 0
+
+
+def _append(**kw):
+    d = dict(n=2, heads=4, qo=PTR, ldqo=256, q=PTR + 4096, ldq=256, k=PTR + 8192, ldk=128, v=PTR + 16384, ldv=128,
+             rope=S.CRope(64, 1, 0, 0, PTR, None), pos=PTR, ldp=2, slots=PTR, cache=_cache())
+    d.update(kw)
+    r, c = d["rope"], d["cache"]
+    return _code("lora_quant_append", None, d["n"], d["heads"], d["qo"], d["ldqo"], d["q"], d["ldq"], d["k"], d["ldk"],
+                 d["v"], d["ldv"], ctypes.byref(r) if r else None, d["pos"], d["ldp"], d["slots"], ctypes.byref(c))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), B.LORA_E_SHAPE), (dict(heads=-1), B.LORA_E_SHAPE), (dict(rope=None), B.LORA_E_NULL),
+    (dict(rope=S.CRope(72, 1, 0, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(80, 1, 0, 0, PTR, None)), B.LORA_E_SHAPE),
+    (dict(rope=S.CRope(64, 0, 0, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(64, 5, 0, 0, PTR, None)), B.LORA_E_SHAPE),
+    (dict(rope=S.CRope(64, 1, 2, 0, PTR, None)), B.LORA_E_SHAPE), (dict(rope=S.CRope(64, 1, 0, 0, None, None)), B.LORA_E_NULL),
+    (dict(pos=None), B.LORA_E_NULL), (dict(ldp=1), B.LORA_E_SHAPE), (dict(slots=None), B.LORA_E_NULL),
+    (dict(q=None), B.LORA_E_NULL), (dict(qo=None), B.LORA_E_NULL), (dict(k=None), B.LORA_E_NULL),
+    (dict(v=PTR + 4), B.LORA_E_ALIGN), (dict(ldk=120), B.LORA_E_SHAPE), (dict(ldv=132), B.LORA_E_ALIGN),
+    (dict(qo=PTR + 4096, ldqo=264), B.LORA_E_SHAPE), (dict(qo=PTR + 8192 - 16), B.LORA_E_SHAPE),
+    (dict(qo=PTR + 16384), B.LORA_E_SHAPE), (dict(heads=1 << 20), B.LORA_E_UNSUPPORTED)], ids=lambda x: str(x))
+def test_append_refusals(kw, code):
+    assert _append(**kw) == code
+
+
+def _read(**kw):
+    d = dict(n=2, k=PTR, ldk=128, v=PTR + 8192, ldv=128, slots=PTR, cache=_cache())
+    d.update(kw)
+    return _code("lora_quant_read", None, d["n"], d["k"], d["ldk"], d["v"], d["ldv"], d["slots"], ctypes.byref(d["cache"]))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), B.LORA_E_SHAPE), (dict(k=None, v=None), B.LORA_E_NULL), (dict(slots=None), B.LORA_E_NULL),
+    (dict(ldk=120), B.LORA_E_SHAPE), (dict(ldv=132), B.LORA_E_ALIGN), (dict(k=PTR + 2), B.LORA_E_ALIGN),
+    (dict(v=PTR), B.LORA_E_SHAPE), (dict(v=PTR + 256), B.LORA_E_SHAPE), (dict(v=PTR + 128, ldk=136, ldv=136), B.LORA_E_SHAPE),
+    (dict(cache=_cache(kv_heads=1 << 23)), B.LORA_E_UNSUPPORTED)], ids=lambda x: str(x))
+def test_read_refusals(kw, code):
+    assert _read(**kw) == code
+
+
+def test_launches_of_more_threads_than_a_grid_holds_are_refused():
+    far = PTR + (1 << 45)
+    cache = _cache(num_pages=1, kv_heads=32, head_dim=128, token_stride=2048, head_stride=64, page_stride=32768,
+                   exp_head_stride=4, exp_token_stride=128, exp_page_stride=2048)
+    for rows, heads in ((1 << 24, 0), (2 ** 31 - 1, 0), (1 << 24, 32)):
+        assert _append(n=rows, heads=heads, qo=far, ldqo=4096, q=PTR, ldq=4096, k=2 * far, ldk=4096, v=3 * far, ldv=4096,
+                       cache=cache, rope=S.CRope(0, 1, 0, 0, None, None)) == B.LORA_E_UNSUPPORTED
+        assert str(rows) in B.last_error()
+        assert _read(n=rows, k=far, ldk=4096, v=2 * far, ldv=4096, cache=cache) == B.LORA_E_UNSUPPORTED
+        assert str(rows) in B.last_error()
+
+
+def test_null_descriptors():
+    rope = S.CRope(0, 1, 0, 0, None, None)
+    assert _code("lora_quant_append", None, 1, 0, None, 0, None, 0, PTR, 128, PTR, 128, ctypes.byref(rope), None, 0, PTR, None) == B.LORA_E_NULL
+    assert _code("lora_quant_read", None, 1, PTR, 128, None, 0, PTR, None) == B.LORA_E_NULL
+
+
+# ------------------------------------------------------------------ the binding
+def test_descriptors_reject_wrong_layouts():
+    z = lambda *s: torch.zeros(s, dtype=U8)
+    k, e = z(4, 16, 2, 32), z(4, 16, 2, 2)
+    make = lambda k=k, v=None, ke=e, ve=None, D=64, dt=F16: Q.QuantKV(k, k.clone() if v is None else v, ke,
+                                                                     ke.clone() if ve is None else ve, D, dt)
+    c = make()
+    assert (c.bits, c.num_pages, c.page_size, c.kv_heads, c.head_dim) == (4, 4, 16, 2, 64)
+    assert make(k=z(4, 16, 2, 64)).bits == 8 and make(D=40).head_dim == 40
+    for kw, msg in ((dict(dt=torch.float32), "dtype"), (dict(k=z(4, 16, 2, 48)), "blocks"), (dict(D=60), "head_dim"),
+                    (dict(D=264), "head_dim"), (dict(D=0), "head_dim"), (dict(D=96), "blocks"), (dict(k=k[0]), "k must"),
+                    (dict(k=k.short()), "uint8"), (dict(ke=z(4, 16, 2, 1)), "k_exp is"), (dict(ke=z(4, 16, 1, 2)), "k_exp is"),
+                    (dict(v=z(4, 16, 2, 64)), "v is"), (dict(v=k), "overlap"), (dict(ve=e), "overlap"), (dict(v="v"), "uint8"),
+                    (dict(v=z(4, 2, 16, 32).transpose(1, 2)), "strides"), (dict(ve=z(4, 2, 16, 2).transpose(1, 2)), "strides"),
+                    (dict(k=z(4, 16, 2, 64)[..., ::2]), "unit"), (dict(k=k[:1].expand(4, 16, 2, 32)), "overlapping"),
+                    (dict(k=z(0, 16, 2, 32), ke=z(0, 16, 2, 2)), "empty"), (dict(k=z(4, 16, 0, 32), ke=z(4, 16, 0, 2)), "empty")):
+        with pytest.raises(ValueError, match=msg):
+            make(**kw)
+    # all four in records of one buffer, page after page; a record too small for them is refused
+    def records(shift, size=2 * 16 * 2 * 34):
+        one = z(4, size)
+        cut = lambda at, n: one[:, at:at + 32 * n].view(4, 16, 2, n)
+        return Q.QuantKV(cut(0, 32), cut(1024, 32), cut(2048 - shift, 2), cut(2112 - shift, 2), 64, F16)
+    records(0)
+    with pytest.raises(ValueError, match="v and k_exp overlap"):
+        records(16)
+    for bits in (4, 8):
+        c = Q.QuantKV.zeros(3, 8, 2, 80, torch.bfloat16, bits, device="cpu")
+        assert c.bits == bits and tuple(c.k.shape) == (3, 8, 2, 12 * bits) and c.k.stride()[1] < c.k.stride()[2]
+    with pytest.raises(ValueError, match="bits"):
+        Q.QuantKV.zeros(3, 8, 2, 80, bits=6, device="cpu")
+    one = Q.QuantKV.zeros(1, 1, 1, 64, device="cpu")      # sizes of one: any stride
+    assert one.c.token_stride >= 32
+
+
+def test_binding_rejects_wrong_tensors(monkeypatch):
+    c = Q.QuantKV.zeros(4, 16, 2, 64, device="cpu")
+    q, k2 = torch.zeros(2, 256, dtype=F16), torch.zeros(2, 128, dtype=F16)
+    tab, n, w = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(64, dtype=torch.int32)
+    attn = lambda **k: Q.lora_quant_attention(**{**dict(out=q.clone(), q=q, cache=c, block_table=tab, kv_len=n, work=w), **k})
+    app = lambda **k: Q.lora_quant_append(**{**dict(q_out=q.clone(), q=q, k=k2, v=k2.clone(), cache=c, slots=n,
+                                                    rope=S.Rope(torch.ones(32)), positions=torch.zeros(1, 2, dtype=torch.int32)), **k})
+    read = lambda **k: Q.lora_quant_read(**{**dict(k_out=k2, v_out=k2.clone(), cache=c, slots=n), **k})
+    for fast in (S._fast, None):
+        monkeypatch.setattr(S, "_fast", fast)
+        for k, msg in ((dict(q=q.float()), "dtype"), (dict(q=q[:, :200]), "heads"), (dict(out=q[:1]), "at least"),
+                       (dict(kv_len=n.long()), "dtype"), (dict(kv_len=n[:1]), "elements"), (dict(block_table=tab.long()), "dtype"),
+                       (dict(lse=torch.zeros(3)), "elements"), (dict(lse=torch.zeros(2, 8)), "lse is"), (dict(req=n.float()), "dtype"),
+                       (dict(), "GPU tensor")):
+            with pytest.raises(ValueError, match=msg):
+                attn(**k)
+        for k, msg in ((dict(q_out=None), "together"), (dict(k=k2.bfloat16()), "dtype"), (dict(positions=None), "tensor"),
+                       (dict(v=k2[:, :64]), "at least"), (dict(slots=n.long()), "dtype"), (dict(), "GPU tensor")):
+            with pytest.raises(ValueError, match=msg):
+                app(**k)
+        for k, msg in ((dict(k_out=k2.bfloat16()), "dtype"), (dict(v_out=k2[:, :120]), "at least"), (dict(k_out=k2[:1]), "at least"),
+                       (dict(slots=n.long()), "dtype"), (dict(slots=None), "tensor"), (dict(k_out=k2.t()), "stride|at least"),
+                       (dict(), "GPU tensor")):
+            with pytest.raises(ValueError, match=msg):
+                read(**k)
+
+
+def test_counts_that_pass_32_bits_are_refused(monkeypatch):
+    far, i32 = 2 ** 32 + 8, torch.int32
+    monkeypatch.setattr(S, "_here", lambda *a: 0)
+    monkeypatch.setattr(S, "_raw", lambda *a: None)
+    calls = []
+    monkeypatch.setattr(S, "_call", lambda *a: calls.append(a))
+    e = lambda *shape, dt=i32: torch.empty(shape, dtype=dt, device="meta")
+    c = Q.QuantKV.zeros(4, 16, 2, 64, device="cpu")
+    m = lambda *s: torch.empty(s, dtype=U8, device="meta")
+    for make, what in ((lambda: Q.QuantKV(m(far, 1, 1, 16), m(far, 1, 1, 16), m(far, 1, 1, 1), m(far, 1, 1, 1), 8, F16), "num_pages"),
+                       (lambda: Q.QuantKV(m(1, 1, far, 16), m(1, 1, far, 16), m(1, 1, far, 1), m(1, 1, far, 1), 8, F16), "kv_heads"),
+                       (lambda: Q.workspace(far, 4, 2, 64, device="meta"), "n_rows")):
+        with pytest.raises(ValueError, match=what):
+            make()
+    attn = dict(out=e(far, 256, dt=F16), q=e(far, 256, dt=F16), cache=c, block_table=e(far, 4), kv_len=e(far), work=e(64))
+    for kw, what in ((attn, "n_rows"), ({**attn, "q": e(2, 256, dt=F16)}, "n_req")):
+        with pytest.raises(ValueError, match=what):
+            Q.lora_quant_attention(**kw)
+    with pytest.raises(ValueError, match="n_rows"):
+        Q.lora_quant_append(None, None, e(far, 128, dt=F16), e(far, 128, dt=F16), c, e(far))
+    with pytest.raises(ValueError, match="n_rows"):
+        Q.lora_quant_read(e(far, 128, dt=F16), None, c, e(far))
+    assert not calls
+
+
+# ------------------------------------------------------------------ the layer
+def test_a_layer_takes_the_cache_of_its_step():
+    H, KV, D, T = 4, 2, 64, 8
+    shape = LY.LlamaShape("case", H * D, 512, H, D, kv_heads=KV)
+    layer = LY.random_layer(shape, 2, 8, T, torch.Generator().manual_seed(0), device="cpu")
+    hidden = torch.zeros(T, H * D, dtype=F16)
+    with pytest.raises(ValueError, match="kv_bits"):
+        LY.PagedStep(shape, 2, T, 3, 6, 8, device="cpu", kv_bits=3)
+    steps = {b: LY.PagedStep(shape, 2, T, 3, 6, 8, device="cpu", kv_bits=b) for b in (16, 8, 4)}
+    for b, step in steps.items():
+        for c, other in steps.items():
+            with pytest.raises(ValueError, match="GPU tensor" if b == c else "bits"):
+                layer.forward_paged(hidden, other.new_cache(device="cpu"), step, None)
+    assert steps[4].new_cache(torch.bfloat16, "cpu").dtype is torch.bfloat16
+
+
+# ------------------------------------------------------------------ the references
+def test_reference_on_worked_blocks():
+    x = torch.zeros(1, 32, dtype=torch.float64)
+    x[0, :8] = torch.tensor([6.9, -0.25, 0.75, 2.5, 3.5, 5.0, 1.1, -0.1])
+    y, e = QR.quantise(x, 4, F16)
+    assert e.tolist() == [[127.0]] and y[0, :8].tolist() == [6.0, -0.0, 1.0, 2.0, 4.0, 4.0, 1.0, -0.0]
+    y, e = QR.quantise(x * 8.0, 4, F16)
+    assert e.tolist() == [[130.0]]
+    x[0, 0] = 7.0
+    y, e = QR.quantise(x, 4, F16)
+    assert e.tolist() == [[128.0]] and y[0, :4].tolist() == [8.0, -0.0, 1.0, 2.0]
+    y, e = QR.quantise(x, 8, F16)          # 7 is below 464 / 64 and not below 464 / 128
+    assert e.tolist() == [[121.0]] and y[0, 0] == 7.0 and y[0, 6] == 1.125
+    x[0, 3] = math.inf
+    y, e = QR.quantise(x, 8, F16)
+    assert e.tolist() == [[255.0]] and bool(y.isnan().all())
+    big, _ = QR.quantise(torch.full((1, 32), 65504.0, dtype=torch.float64), 4, F16)
+    assert big[0, 0] == 49152.0
+    code = QR.pack(*[t for t in QR.quantise(torch.arange(32, dtype=torch.float64)[None], 4, F16)], 4)
+    assert code.shape == (1, 16)
