@@ -129,6 +129,8 @@ def lib() -> ctypes.CDLL:
             "lora_quant_read": [P, I32, P, I64, P, I64, P, P],
             "lora_quant_attention": [P, I32, I32, P, I64, P, I64, P, I32, P, I64, I32, P, P, ctypes.c_float, I32, P, P,
                                      ctypes.c_size_t],
+            # lora_sample.h (marshalled by sample.py)
+            "lora_sample": [P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -141,7 +143,8 @@ def lib() -> ctypes.CDLL:
                                 ("lora_pool_load_header_bytes", [I32], ctypes.c_size_t),
                                 ("lora_handoff_bytes", [I32], ctypes.c_size_t),
                                 ("lora_paged_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t),
-                                ("lora_quant_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t)):
+                                ("lora_quant_attention_bytes", [I32, I32, I32, I32], ctypes.c_size_t),
+                                ("lora_sample_bytes", [I32, I32], ctypes.c_size_t)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         L.lora_pick_tile_rows.restype = ctypes.c_int32

@@ -18,9 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblora_sgmv.so")
 SOURCES = [os.path.join(CSRC, "lora_kernels.hip"), os.path.join(CSRC, "lora_pool.hip"),
-           os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_quant.hip"), os.path.join(CSRC, "lora_host.cpp")]
+           os.path.join(CSRC, "lora_step.hip"), os.path.join(CSRC, "lora_quant.hip"), os.path.join(CSRC, "lora_sample.hip"),
+           os.path.join(CSRC, "lora_host.cpp")]
 PUBLIC_HEADERS = [os.path.join(INCLUDE, "lora_sgmv.h"), os.path.join(INCLUDE, "lora_step.h"),
-                  os.path.join(INCLUDE, "lora_quant.h")]
+                  os.path.join(INCLUDE, "lora_quant.h"), os.path.join(INCLUDE, "lora_sample.h")]
 HEADERS = PUBLIC_HEADERS + [os.path.join(CSRC, "lora_internal.hpp"), os.path.join(CSRC, "step_device.hpp")]
 ARCH = "gfx950"
 ARGS_LIB = os.path.join(PKG, "_step_args.so")

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "lora_quant.h"
+#include "lora_sample.h"
 #include "lora_step.h"
 
 namespace {
@@ -276,6 +277,39 @@ PyObject *quant_read(PyObject *, PyObject *const *args, Py_ssize_t n)
     return status_of(fn, stream, (int32_t)rows, k, ldk, v, ldv, static_cast<const int32_t *>(sp), c);
 }
 
+// sample(function, stream, device, token, logits, u, work, temperature, top_k, top_p, min_p, rows, logprob)
+PyObject *sample(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    STEP_ARGS("sample", 13);
+    const auto fn = g.address<decltype(&lora_sample)>(0);
+    void *const stream = g.address<void *>(1);
+    const at::Tensor *token = g.tensor(3), *x = g.tensor(4), *work = g.tensor(6);
+    if (!g.ok || !is_plain(*x) || x->dim() != 2 || x->size(0) > INT32_MAX || x->size(1) > INT32_MAX) Py_RETURN_NONE;
+    const long type = has_type(*x, kF16) ? kF16 : has_type(*x, kBF16) ? kBF16 : kF32;  // the library's codes too
+    if (!has_type(*x, type) || (x->size(1) > 1 && x->stride(1) != 1) || (x->size(0) > 1 && x->stride(0) < x->size(1)))
+        Py_RETURN_NONE;
+    const int64_t rows = token->numel();
+    lora_sample_args a{};
+    a.type = (int32_t)type;
+    a.n_rows = (int32_t)rows;
+    a.vocab = (int32_t)x->size(1);
+    a.n_logits = (int32_t)x->size(0);
+    a.logits = x->data_ptr();
+    a.ld = x->size(0) > 1 ? x->stride(0) : x->size(1);
+    a.token = static_cast<int32_t *>(g.vector(3, kI32, rows));
+    a.u = static_cast<const float *>(g.vector(5, kF32, rows));
+    a.work = g.vector(6, kI32, 1);
+    a.work_bytes = 4 * static_cast<size_t>(work->numel());
+    a.temperature = static_cast<const float *>(g.vector(7, kF32, rows, true));
+    a.top_k = static_cast<const int32_t *>(g.vector(8, kI32, rows, true));
+    a.top_p = static_cast<const float *>(g.vector(9, kF32, rows, true));
+    a.min_p = static_cast<const float *>(g.vector(10, kF32, rows, true));
+    a.rows = static_cast<const int32_t *>(g.vector(11, kI32, rows, true));
+    a.logprob = static_cast<float *>(g.vector(12, kF32, rows, true));
+    if (!g.ok || rows > INT32_MAX) Py_RETURN_NONE;
+    return status_of(fn, stream, &a);
+}
+
 // norm(function, stream, device, y, res, w, x, res_out, post_w, gate, gate_idx, alpha, eps, w_offset)
 PyObject *norm(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -352,7 +386,7 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n)
 PyMethodDef methods[] = {STEP_METHOD(matrix), STEP_METHOD(vector), STEP_METHOD(here),
                          STEP_METHOD(attention), STEP_METHOD(append), STEP_METHOD(norm),
                          STEP_METHOD(plan), STEP_METHOD(quant_attention), STEP_METHOD(quant_append),
-                         STEP_METHOD(quant_read), {nullptr, nullptr, 0, nullptr}};
+                         STEP_METHOD(quant_read), STEP_METHOD(sample), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

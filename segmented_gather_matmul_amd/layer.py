@@ -16,8 +16,7 @@ form, for tiles of fewer than 8 rows).  Optionally each shrink runs on a second 
 while the backbone GEMM of the same input runs, so only the expands stay on the layer's
 critical path.
 
-Left out of the step on purpose: sampling, and, in the dense step, rotary position
-embedding.  In the dense step (LoraDecoderLayer.forward) the current token's k and v are
+Left out of the dense step on purpose: rotary position embedding.  In the dense step (LoraDecoderLayer.forward) the current token's k and v are
 written into the last position of the cache, so attention spans `seq_len` positions
 including it.
 
@@ -25,7 +24,8 @@ The paged step (forward_paged) serves requests of any lengths, new tokens of pro
 decoding requests in one batch, over a paged cache: PagedStep plans the step on the
 device from the requests' lengths once for all layers (pages, cache slots, the rows'
 adapter ids), and each layer runs the residual adds with their norms, rotary positions
-with the append to the cache, and attention over it in this library's kernels too.
+with the append to the cache, and attention over it in this library's kernels too.  The cache holds
+16-bit values, or (kv_bits) 8- or 4-bit ones; PagedStep.sample draws the requests' next tokens.
 """
 from __future__ import annotations
 
@@ -157,6 +157,20 @@ class PagedStep:
         from . import step as S
         S.lora_kv_plan(self.plan, self.pages, self.kv_len, new_len, req_slot=self.req_slot)
         torch.add(self.plan.tok_pos, 1, out=self.row_len)   # each row sees its request up to itself
+
+    def sample(self, token, logits, u, work, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None):
+        """Draw the next token of every request that had tokens in the step planned last, from the logits of its last
+        row: token int32 [n_req] (entries of other requests stay as they were), logits [max_tokens, vocab] of
+        the step's token rows; u and the settings are per request, work from sample.sample_workspace(n_req, vocab)
+        (sample.lora_sample)."""
+        import torch
+        from . import sample as SA
+        if logits.shape[0] != self.max_tokens or token.numel() != self.n_req:
+            raise ValueError(f"logits of {logits.shape[0]} rows and {token.numel()} tokens do not fit a step of "
+                             f"{self.max_tokens} rows and {self.n_req} requests")
+        end = self.plan.q_ptr[1:self.n_req + 1]
+        rows = torch.where(end > self.plan.q_ptr[:self.n_req], end - 1, -1)
+        SA.lora_sample(token, logits, u, work, temperature, top_k, top_p, min_p, rows=rows, logprob=logprob)
 
 
 class KVCache:
