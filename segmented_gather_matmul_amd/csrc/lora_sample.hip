@@ -1,6 +1,8 @@
 // HIP kernels (gfx950 / CDNA4) and launchers of sampling (lora_sample.h).
 #include "lora_sample.h"
 
+#include <type_traits>
+
 #include "step_device.hpp"
 
 namespace lora {
@@ -16,186 +18,317 @@ struct F32 {
     typedef float elem;
 };
 
-// Logits as whole numbers in the same order (equal ones equal, -0 taken as 0 before): the sign folded into the bits of
-// the 32-bit value, without the bits that the type never sets.  0 is below all of them: no token.
+// How a logit's bits are read.
 template <typename T>
-struct Key;
+struct Bits;
 template <>
-struct Key<F16> {
-    static constexpr int kDrop = 13;
+struct Bits<F16> {
+    static constexpr uint32_t kInf = 0x7c00, kSign = 0x8000;
+    static constexpr int kDrop = 13;  // low bits of its values in 32 bits that are never set
 };
 template <>
-struct Key<BF16> {
+struct Bits<BF16> {
+    static constexpr uint32_t kInf = 0x7f80, kSign = 0x8000;
     static constexpr int kDrop = 16;
 };
 template <>
-struct Key<F32> {
+struct Bits<F32> {
+    static constexpr uint32_t kInf = 0x7f800000, kSign = 0x80000000;
     static constexpr int kDrop = 0;
 };
+
+// Whole numbers in the order of the values (0 and -0 equal): the magnitude's bits, negated where the sign is set; without
+// the bits that the type never sets, so that neighbours differ by 1.
 template <typename T>
-__device__ inline uint32_t key_of(float f)
+__device__ inline int32_t key_of(float v)
 {
-    const uint32_t b = __builtin_bit_cast(uint32_t, f);
-    return (b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) >> Key<T>::kDrop;
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const int32_t mag = (int32_t)((b & 0x7fffffffu) >> Bits<T>::kDrop);
+    return (int32_t)b < 0 ? -mag : mag;
 }
 template <typename T>
-__device__ inline float value_of(uint32_t key)
+__device__ inline float value_of(int32_t key)
 {
-    constexpr uint32_t low = (1u << Key<T>::kDrop) - 1;
-    const uint32_t s = key << Key<T>::kDrop;
-    return __builtin_bit_cast(float, s & 0x80000000u ? s & 0x7fffffffu : ~(s | low));
+    const float v = __builtin_bit_cast(float, (uint32_t)(key < 0 ? -key : key) << Bits<T>::kDrop);
+    return key < 0 ? -v : v;
 }
 
-// A row in chunks of eight logits, one lane's load, whose first begins at a 16-byte boundary at or before the row.
+// Eight neighbouring logits, what one lane loads at a time; 16-bit ones two in a word.
+template <typename T>
+struct alignas(16) Chunk {
+    static constexpr bool kHalf = sizeof(typename T::elem) == 2;
+    static constexpr int kWords = kHalf ? 4 : 8;
+    static constexpr uint32_t kNone = Bits<T>::kSign | Bits<T>::kInf;
+    typedef short s2_t __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+    uint32_t w[kWords];
+
+    // Logit e of the first four.
+    __device__ inline float value(int e) const
+    {
+        if constexpr (std::is_same_v<T, F16>) return (float)__builtin_bit_cast(h2_t, w[e / 2])[e % 2];
+        else if constexpr (kHalf) return __builtin_bit_cast(float, e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        else return __builtin_bit_cast(float, w[e]);
+    }
+    // The last four in the place of the first: loops over the logits take two rounds of four, for little code.
+    __device__ inline void swap()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords / 2; ++i) {
+            const uint32_t x = w[i];
+            w[i] = w[i + kWords / 2];
+            w[i + kWords / 2] = x;
+        }
+    }
+    // The second logit in the place of the first, and one behind the last.
+    __device__ inline void put(uint32_t bits)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint32_t after = i + 1 < kWords ? w[i + 1] : bits;
+            w[i] = kHalf ? w[i] >> 16 | after << 16 : after;
+        }
+    }
+    __device__ inline float largest() const
+    {
+        if constexpr (std::is_same_v<T, F16>) {
+            h2_t m = __builtin_bit_cast(h2_t, w[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(h2_t, w[i]));
+            return __builtin_fmaxf((float)m[0], (float)m[1]);
+        } else {
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (kHalf)
+                    m = __builtin_fmaxf(m, __builtin_fmaxf(__builtin_bit_cast(float, w[i] << 16),
+                                                           __builtin_bit_cast(float, w[i] & 0xffff0000u)));
+                else m = __builtin_fmaxf(m, __builtin_bit_cast(float, w[i]));
+            }
+            return m;
+        }
+    }
+    __device__ inline void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = kHalf ? 0x10001u * kNone : kNone;
+    }
+    // NaN counts as -inf.
+    __device__ inline void clean()
+    {
+        if constexpr (kHalf) {
+            const s2_t inf = {(short)Bits<T>::kInf, (short)Bits<T>::kInf};
+            s2_t most = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(s2_t, w[i] & 0x7fff7fffu));
+            if (max((int32_t)most[0], (int32_t)most[1]) > (int32_t)Bits<T>::kInf) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const s2_t bad = __builtin_bit_cast(s2_t, w[i] & 0x7fff7fffu) > inf;
+                    const uint32_t mask = __builtin_bit_cast(uint32_t, bad);
+                    w[i] = (w[i] & ~mask) | (0x10001u * kNone & mask);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = (w[i] & 0x7fffffffu) > Bits<T>::kInf ? kNone : w[i];
+        }
+    }
+    // +inf as 0, all others as -inf.
+    __device__ inline void only_infinite()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (kHalf)
+                w[i] = ((w[i] & 0xffffu) == Bits<T>::kInf ? 0 : kNone) | (w[i] >> 16 == Bits<T>::kInf ? 0 : kNone) << 16;
+            else w[i] = w[i] == Bits<T>::kInf ? 0 : kNone;
+        }
+    }
+};
+
+// A row in chunks, the first of which begins at a 16-byte boundary at or before the row.
 template <typename T>
 struct Row {
     const uint8_t *base;  // of chunk 0
     int32_t before;       // elements of it that lie before the row
     int32_t vocab, chunks, segments;
-    bool infinite;        // its largest is +inf: others count as -inf, that as 0
 
-    // Logits [8 c - before, ...): what is no logit is the number whose key is 0.
-    __device__ inline void load(int32_t c, float (&f)[8]) const
+    // The bits of chunk c; what is no logit of the row is -inf.
+    __device__ inline Chunk<T> bits(int32_t c) const
     {
         typedef typename T::elem E;
         const int32_t first = 8 * c - before;
+        Chunk<T> r;
+        r.clear();
         if (first >= 0 && first + 8 <= vocab) {
-            E v[8];
 #pragma unroll
-            for (int i = 0; i < (int)(8 * sizeof(E) / 16); ++i)
-                reinterpret_cast<uint4 *>(v)[i] = reinterpret_cast<const uint4 *>(base)[(8 * sizeof(E) / 16) * (int64_t)c + i];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = clean((float)v[e]);
-        } else {
-#pragma unroll
+            for (int i = 0; i < Chunk<T>::kWords; i += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(base + (int64_t)c * (8 * sizeof(E)) + 4 * i);
+                r.w[i] = v.x;
+                r.w[i + 1] = v.y;
+                r.w[i + 2] = v.z;
+                r.w[i + 3] = v.w;
+            }
+        } else if (c < chunks) {
+#pragma unroll 1
             for (int e = 0; e < 8; ++e) {
-                const int32_t at = first + e;
-                f[e] = at >= 0 && at < vocab ? clean((float)reinterpret_cast<const E *>(base)[at + before])
-                                             : __builtin_bit_cast(float, 0xffffffffu);
+                const bool in = first + e >= 0 && first + e < vocab;
+                if constexpr (Chunk<T>::kHalf) r.put(in ? reinterpret_cast<const uint16_t *>(base)[8 * c + e] : Chunk<T>::kNone);
+                else r.put(in ? reinterpret_cast<const uint32_t *>(base)[8 * c + e] : Chunk<T>::kNone);
             }
         }
-    }
-    __device__ inline float clean(float f) const
-    {
-        f = f > -INFINITY ? f + 0.f : -INFINITY;  // NaN; -0
-        return infinite ? (f == INFINITY ? 0.f : -INFINITY) : f;
+        return r;
     }
 };
 
 // ------------------------------------------------------------------------ weights
-// 2^(j / 128)
-struct PowerTable {
-    double v[128];
-    constexpr PowerTable() : v{}
-    {
-        for (int j = 0; j < 128; ++j) {
-            const double x = j * (0.693147180559945309417 / 128.0);
-            double term = 1.0, sum = 1.0;
-            for (int n = 1; n < 24; ++n) {
-                term *= x / n;
-                sum += term;
-            }
-            v[j] = sum;
-        }
-    }
-};
-__constant__ const PowerTable kPowers{};
-
-// floor(2^40 2^y) for y <= 0, to 2^-50 of it before the floor: y = k / 128 + f, 2^y = 2^(k / 128) e^(f ln 2), the
-// second factor by four terms of its series (the fifth is below 2^-49), the first from the table and a shift.
-__device__ inline uint64_t weight_of(double y, const double *powers)
+// a b + c with c in scalar registers (the compiler copies it into vector registers before every use).
+__device__ inline double fma_c(double a, double b, double c)
 {
-    y = __builtin_fmax(y, -64.0);  // NaN: no logit
-    const double big = y * 128.0 + 6755399441055744.0;  // rounded to a whole number in the low bits
-    const int32_t k = (int32_t)__builtin_bit_cast(uint64_t, big);
-    const double f = __builtin_fma(big - 6755399441055744.0, -1.0 / 128.0, y);
-    const double g = f * 0.693147180559945309417;
-    double s = __builtin_fma(g, 1.0 / 24.0, 1.0 / 6.0);
-    s = __builtin_fma(g, s, 0.5);
-    s = __builtin_fma(g, s, 1.0) * g;
-    const double t = powers[k & 127], m = __builtin_fma(t, s, t);
-    const uint64_t bits = __builtin_bit_cast(uint64_t, m);
-    const int shift = 52 - kUnitBits - (k >> 7) + 1023 - (int)(bits >> 52);
-    return ((bits & 0xfffffffffffffull) | 0x10000000000000ull) >> (shift < 63 ? shift : 63);
+    double r;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
+    return r;
+}
+
+// floor(2^40 2^y) for y <= 0, to 2^-37 of it before the floor, as a whole number in 64-bit floating point: y = k + f with
+// |f| <= 1/2, 2^f = e^(f ln 2) by nine terms of its series (the tenth is below 2^-37), 2^k by the exponent.  2^0 is exact.
+__device__ inline double weight_of(double y)
+{
+    constexpr double kRound = 6755399441055744.0 + kUnitBits;  // 1.5 2^52: a sum's low bits are a whole number, the nearest to y + 40
+    constexpr double l = 0.693147180559945309417;
+    constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6, c7 = c6 * l / 7,
+                     c8 = c7 * l / 8, c9 = c8 * l / 9;
+    y = __builtin_fmax(y, -64.0);
+    const double big = y + kRound, f = y - (big - kRound);
+    double s = fma_c(f, c9, c8);
+    s = fma_c(f, s, c7);
+    s = fma_c(f, s, c6);
+    s = fma_c(f, s, c5);
+    s = fma_c(f, s, c4);
+    s = fma_c(f, s, c3);
+    s = fma_c(f, s, c2);
+    s = fma_c(f, s, l);
+    s = __builtin_fma(f, s, 1.0);
+    return __builtin_floor(__builtin_ldexp(s, (int)__builtin_bit_cast(uint64_t, big)));
+}
+
+// A whole number below 2^52 as an integer.
+__device__ inline uint64_t whole(double x)
+{
+    return __builtin_bit_cast(uint64_t, x + 4503599627370496.0) & 0xfffffffffffffull;
 }
 
 // ------------------------------------------------------------------------ sums over the workgroup
-__device__ inline uint64_t wave_sum(uint64_t v)
+#define LORA_SCAN_STEP(ctrl, rows)                                                                             \
+    v += (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(v >> 32), ctrl, rows, 0xf, false) << 32 |    \
+         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false)
+// Inclusive sums over each row of sixteen lanes, and over the wavefront.
+__device__ inline uint64_t row_scan64(uint64_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    LORA_SCAN_STEP(0x111, 0xf);  // row_shr:1, 2, 4, 8
+    LORA_SCAN_STEP(0x112, 0xf);
+    LORA_SCAN_STEP(0x114, 0xf);
+    LORA_SCAN_STEP(0x118, 0xf);
     return v;
 }
-__device__ inline uint64_t wave_before(uint64_t v)  // sum of the lanes before
+__device__ inline uint64_t wave_scan64(uint64_t v)
 {
-    const int lane = threadIdx.x & 63;
-    uint64_t s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t x = __shfl_up(s, d);
-        if (lane >= d) s += x;
-    }
-    return s - v;
+    v = row_scan64(v);
+    LORA_SCAN_STEP(0x142, 0xa);  // row_bcast:15 into rows 1 and 3
+    LORA_SCAN_STEP(0x143, 0xc);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+#undef LORA_SCAN_STEP
+__device__ inline uint64_t lane_of(uint64_t v, int lane)
+{
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ inline float wave_max(float v)
+{
+#define LORA_MAX_STEP(ctrl, rows) \
+    v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, v), __builtin_bit_cast(int, v), ctrl, rows, 0xf, false)))
+    LORA_MAX_STEP(0x111, 0xf);
+    LORA_MAX_STEP(0x112, 0xf);
+    LORA_MAX_STEP(0x114, 0xf);
+    LORA_MAX_STEP(0x118, 0xf);
+    LORA_MAX_STEP(0x142, 0xa);
+    LORA_MAX_STEP(0x143, 0xc);
+#undef LORA_MAX_STEP
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+struct Pair {
+    uint64_t count, mass;
+};
+
 // Sums of the threads before this one, and of all.
-__device__ inline uint64_t group_before(uint64_t v, uint64_t *wave_sums, uint64_t &all)
+__device__ inline Pair group_before(Pair v, Pair *wave_sums, Pair &all)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t b = wave_before(v);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Pair s{wave_scan64(v.count), wave_scan64(v.mass)};
     __syncthreads();
-    if (lane == 63) wave_sums[wave] = b + v;
+    if (lane == 63) wave_sums[wave] = s;
     __syncthreads();
-    uint64_t before = 0;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = all;
-        all += wave_sums[w];
-    }
-    return before + b;
+    Pair w = wave_sums[lane & (kWaves - 1)];  // sixteen lanes, a wavefront each: sums up to theirs
+    w.count = row_scan64(w.count);
+    w.mass = row_scan64(w.mass);
+    all = Pair{lane_of(w.count, kWaves - 1), lane_of(w.mass, kWaves - 1)};
+    Pair before{0, 0};
+    if (wave > 0) before = Pair{lane_of(w.count, wave - 1), lane_of(w.mass, wave - 1)};
+    return Pair{before.count + s.count - v.count, before.mass + s.mass - v.mass};
 }
 
 // ------------------------------------------------------------------------ the draw
-// What stays of a row by order: keys above `key`, and of those equal to it the first `ties` by index.
+// What stays of a row by order: values above `value`, and of those equal to it the first `ties` by index.
 struct Border {
-    uint32_t key;
+    float value;
     int32_t ties;
 };
+
+constexpr int kList = 256;                // candidates on a list
+constexpr int kListTopK = 128;            // top-k of this many or fewer looks for one
+constexpr size_t kSampleLds = 120 << 10;  // for a row's logits, of a workgroup's 160 KB
 
 struct Shared {
     uint64_t mass[kBins];
     uint32_t count[kBins];
-    double powers[128];
-    uint64_t wave_sums[kWaves];
+    Pair wave_sums[kWaves];
+    float wave_best[kWaves], wave_bound[kWaves];
+    int32_t wave_at[kWaves];
+    // the list: value and index as one number, larger where it comes first; weight; what comes before
+    uint64_t order[kList], weight[kList], before[kList];
+    uint32_t rank[kList];
+    uint64_t total;
+    int32_t listed;
     uint64_t found_mass;
     int64_t found_count;
     int32_t found, found_ties;
-    float wave_max[kWaves];
-    int32_t wave_min[kWaves];
 };
 
-// One workgroup per row, several passes over its logits, which stay in the caches:
-//   - their largest;
-//   - for top-k and top-p, a histogram of how many and what mass lie how far below it; the bin in which the
-//     border lies; and a histogram of the keys of that bin (again, while a bin holds several keys), which gives the
-//     border's key and how many of its equals stay;
-//   - the mass that stays of each segment of 512 logits; the segment that the draw falls into, and the
-//     token in it.
-// Histograms and masses are whole numbers, so the order of their atomics does not matter.
-template <typename T>
+// One workgroup per row.  Its logits are kept in LDS (KEPT), or the row is read again in every pass.
+//   - The largest.
+//   - For top-k of few, a bound that at least k logits reach: every wavefront gives the value that k / 16 of its lanes' largest
+//     reach, and the lowest of these is taken.  What reaches it (mostly little more than k) is put on a list.
+//   - Otherwise, for top-k and top-p, a histogram of how many and what mass lie how far below the largest, and the
+//     bin in which the border lies.  If few lie above it, they are put on the list.
+//   - On the list, everything follows from how many and what mass come before each candidate, in order and by index,
+//     found by comparing all with all.
+//   - Without a list: histograms of the values between two bounds, narrower until a bin is one value, give the border and how
+//     many of its equals stay; then the mass that stays of each segment of 512 logits, the segment that the draw
+//     falls into, and the token in it.
+// Counts and masses are whole numbers, so the order of their atomics does not matter.
+//
+// Bound by arithmetic where every logit's weight is needed (no filter, top-p): some 30 instructions a logit, most
+// of them in 64 bits, which run at the rate of 32-bit ones here.
+template <typename T, bool KEPT>
 __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample_args a)
 {
     __shared__ Shared sh;
-    extern __shared__ uint64_t seg_mass[];  // [segments], then their ties
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    extern __shared__ __align__(16) uint64_t seg_mass[];  // [segments], then their ties, then the logits
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t r = blockIdx.x, src = a.rows ? a.rows[r] : r;
-    const float temperature = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f;
-    const float min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u[r];
-    const int32_t top_k = a.top_k ? a.top_k[r] : 0;
-    if (src < 0 || src >= a.n_logits || !(temperature >= 0.f) || temperature == INFINITY || top_k < 0 ||
-        !(top_p >= 0.f && top_p <= 1.f) || !(min_p >= 0.f && min_p <= 1.f) || !(u >= 0.f && u < 1.f))
-        return;
+    if (src < 0 || src >= a.n_logits) return;
     Row<T> row;
     const uint8_t *const first = static_cast<const uint8_t *>(a.logits) + (int64_t)src * a.ld * (int64_t)sizeof(typename T::elem);
     row.base = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(first) & ~uintptr_t(15));
@@ -203,31 +336,74 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     row.vocab = a.vocab;
     row.chunks = (a.vocab + row.before + 7) / 8;
     row.segments = (row.chunks + 63) / 64;
-    row.infinite = false;
-    uint32_t *const seg_ties = reinterpret_cast<uint32_t *>(seg_mass + row.segments);
-    // Calls fn(segment, logits) for the segments in turn, a wavefront each.
-    auto each = [&](auto &&fn) {
+    uint32_t *const seg_ties = reinterpret_cast<uint32_t *>(seg_mass + (row.segments + 1) / 2 * 2);
+    Chunk<T> *const held = reinterpret_cast<Chunk<T> *>(seg_ties + (row.segments + 3) / 4 * 4);
+    const float temperature = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f;
+    const float min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u[r];
+    const int32_t top_k = a.top_k ? a.top_k[r] : 0;
+    if (!(temperature >= 0.f) || temperature == INFINITY || top_k < 0 || !(top_p >= 0.f && top_p <= 1.f) ||
+        !(min_p >= 0.f && min_p <= 1.f) || !(u >= 0.f && u < 1.f))
+        return;
+    // fn(segment, chunk) for the row's segments of 64 chunks, a wavefront each
+    auto stream = [&](auto &&fn) __attribute__((always_inline)) {
+        Chunk<T> next = row.bits(64 * wave + lane);
         for (int32_t s = wave; s < row.segments; s += kWaves) {
-            float f[8];
-            if (64 * s + lane < row.chunks) row.load(64 * s + lane, f);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, 0xffffffffu);
-            fn(s, f);
+            Chunk<T> c = next;
+            next = row.bits(64 * (s + kWaves) + lane);
+            c.clean();
+            fn(s, c);
         }
     };
+    bool infinite = false;  // the largest is +inf: it counts as 0, all others as -inf
+    auto each = [&](auto &&fn) __attribute__((always_inline)) {
+        auto as_they_count = [&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+            if (infinite) c.only_infinite();
+            fn(s, c);
+        };
+        if constexpr (KEPT) {
+            for (int32_t s = wave; s < row.segments; s += kWaves) {
+                Chunk<T> c = held[64 * s + lane];
+                as_they_count(s, c);
+            }
+        } else {
+            stream(as_they_count);
+        }
+    };
+    // fn(value) for every logit
+    auto all = [&](auto &&fn) __attribute__((always_inline)) {
+        each([&](int32_t, Chunk<T> &c) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) fn(c.value(e));
+                c.swap();
+            }
+        });
+    };
 
-    float top = -INFINITY;
-    each([&](int32_t, const float (&f)[8]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, f[e]);
+    float best = -INFINITY;  // this thread's largest
+    stream([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+        best = __builtin_fmaxf(best, c.largest());
+        if constexpr (KEPT) held[64 * s + lane] = c;
     });
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) sh.wave_max[wave] = top;
-    if (tid < 128) sh.powers[tid] = kPowers.v[tid];
+    const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
+    const float wave_top = wave_max(best);
+    if (by_k && top_k <= kListTopK && temperature > 0.f) {
+        float left = best, bound = wave_top;
+        for (int32_t need = (top_k + kWaves - 1) / kWaves;;) {
+            const uint64_t on = __ballot(left == bound);
+            need -= __builtin_popcountll(on);
+            if (need <= 0 || bound == -INFINITY) break;
+            left = left == bound ? -INFINITY : left;
+            bound = wave_max(left);
+        }
+        if (lane == 0) sh.wave_bound[wave] = bound;
+    }
+    if (lane == 0) sh.wave_best[wave] = wave_top;
+    if (tid == 0) sh.listed = 0;
     __syncthreads();
-    for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, sh.wave_max[w]);
+    float top = sh.wave_best[lane & (kWaves - 1)];
+    top = wave_max(top);
     if (top == -INFINITY) {
         if (tid == 0) {
             a.token[r] = -1;
@@ -237,268 +413,415 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     }
     if (temperature == 0.f) {
         int32_t at = INT32_MAX;
-        each([&](int32_t s, const float (&f)[8]) {
+        each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+            if (!__any(c.largest() == top)) return;
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
 #pragma unroll
-            for (int e = 7; e >= 0; --e)
-                if (f[e] == top) at = min(at, 8 * (64 * s + lane) + e - row.before);
+                for (int e = 0; e < 4; ++e)
+                    if (c.value(e) == top) at = min(at, 8 * (64 * s + lane) + i + e - row.before);
+                c.swap();
+            }
         });
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) at = min(at, __shfl_xor(at, d));
-        if (lane == 0) sh.wave_min[wave] = at;
+        if (lane == 0) sh.wave_at[wave] = at;
         __syncthreads();
         if (tid == 0) {
-            for (int w = 0; w < kWaves; ++w) at = min(at, sh.wave_min[w]);
+            for (int w = 0; w < kWaves; ++w) at = min(at, sh.wave_at[w]);
             a.token[r] = at;
             if (a.logprob) a.logprob[r] = 0.f;
         }
         return;
     }
-    if (top == INFINITY) {
-        row.infinite = true;
-        top = 0.f;
-    }
+    infinite = top == INFINITY;
+    if (infinite) top = 0.f;
     const double rate = 1.44269504088896340736 / (double)temperature;
-    auto weight = [&](float f) { return weight_of(((double)f - (double)top) * rate, sh.powers); };
+    auto weight = [&](float v) { return weight_of(((double)v - (double)top) * rate); };
+    const double least = (double)min_p * (double)(1ull << kUnitBits);
     // Bins by the distance from the largest: 1/64 of a power of two each, the last one takes all beyond.
     const float per = (float)__builtin_fmin(rate * 64.0, 1e30);
-    auto bin_of = [&](float f) { return (int32_t)__builtin_fminf((top - f) * per, (float)(kBins - 1)); };
-    const uint32_t top_key = key_of<T>(top), no_key = key_of<T>(-INFINITY);
-    const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
+    auto bin_of = [&](float v) { return (int32_t)__builtin_fminf((top - v) * per, (float)(kBins - 1)); };
 
     auto clear = [&]() {
         __syncthreads();
-        for (int i = tid; i < kBins; i += kSampleThreads) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
+        *reinterpret_cast<uint4 *>(&sh.mass[2 * tid]) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint2 *>(&sh.count[2 * tid]) = make_uint2(0, 0);
         __syncthreads();
     };
-    auto add = [&](int32_t bin, uint64_t w) {
+    auto add = [&](int32_t bin, double w) {
         __hip_atomic_fetch_add(&sh.count[bin], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        if (by_p) __hip_atomic_fetch_add(&sh.mass[bin], w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (by_p) __hip_atomic_fetch_add(&sh.mass[bin], whole(w), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
-    // Where a border lies: the bin, and what lies before it (counts and masses beyond `count0`, `mass0`).
-    // By count: the bin of the k-th token.  By mass: the first bin at whose end `target` is reached.
-    struct Found {
-        int32_t bin;
-        int64_t count;
-        uint64_t mass;
-        int32_t ties;
+    // This thread's two bins of a histogram, and what lies before them.
+    struct Bins {
+        uint32_t c0, c1;
+        uint64_t m0, m1;
+        Pair before;
     };
-    auto find = [&](bool by_count, double target, int64_t count0, uint64_t mass0) {
+    auto scan = [&](Pair from) {
         __syncthreads();
+        Bins b{sh.count[2 * tid], sh.count[2 * tid + 1], sh.mass[2 * tid], sh.mass[2 * tid + 1], {0, 0}};
+        Pair every;
+        b.before = group_before(Pair{(uint64_t)b.c0 + b.c1, b.m0 + b.m1}, sh.wave_sums, every);
+        b.before.count += from.count;
+        b.before.mass += from.mass;
         if (tid == 0) sh.found = 0;
-        const uint32_t c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1];
-        const uint64_t m0 = sh.mass[2 * tid], m1 = sh.mass[2 * tid + 1];
-        uint64_t all;
-        const int64_t c = count0 + (int64_t)group_before((uint64_t)c0 + c1, sh.wave_sums, all);
-        const uint64_t m = mass0 + group_before(m0 + m1, sh.wave_sums, all);
+        __syncthreads();
+        return b;
+    };
+    // Where a border lies: the bin, what lies before it, and its count.  By count: the bin of the k-th token.  By
+    // mass: the first bin at whose end `target` is reached.
+    struct Found {
+        int32_t bin, ties;
+        Pair before;
+    };
+    auto locate = [&](const Bins &b, bool by_count, double target) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int64_t cb = c + (i ? c0 : 0), ce = cb + (i ? c1 : c0);
-            const uint64_t mb = m + (i ? m0 : 0), me = mb + (i ? m1 : m0);
-            const bool here = by_count ? cb < top_k && top_k <= ce : (double)mb < target && !((double)me < target);
-            if (here) {
+            const int64_t cb = (int64_t)b.before.count + (i ? b.c0 : 0), ce = cb + (i ? b.c1 : b.c0);
+            const uint64_t mb = b.before.mass + (i ? b.m0 : 0), me = mb + (i ? b.m1 : b.m0);
+            if (by_count ? cb < top_k && top_k <= ce : (double)mb < target && !((double)me < target)) {
                 sh.found = 2 * tid + i;
                 sh.found_count = cb;
                 sh.found_mass = mb;
-                sh.found_ties = (int32_t)(i ? c1 : c0);
+                sh.found_ties = (int32_t)(i ? b.c1 : b.c0);
             }
         }
         __syncthreads();
-        return Found{sh.found, sh.found_count, sh.found_mass, sh.found_ties};
+        const Found f{sh.found, sh.found_ties, Pair{(uint64_t)sh.found_count, sh.found_mass}};
+        __syncthreads();
+        return f;
     };
-    // The lowest key whose bin is at most b.
-    auto first_key = [&](int32_t b) {
-        uint32_t lo = no_key, hi = top_key;
+    // The lowest key for whose value fits() holds; it holds for the largest, and above any for which it does.
+    auto first_key = [&](auto &&fits) {
+        int32_t lo = key_of<T>(-INFINITY), hi = key_of<T>(top);
         while (lo < hi) {
-            const uint32_t step = (hi - lo) / 64 + 1, probe = min(lo + lane * step, hi);
-            const uint64_t on = __ballot(bin_of(value_of<T>(probe)) <= b);
+            const uint32_t step = ((uint32_t)hi - (uint32_t)lo) / 64 + 1;
+            const int32_t probe = (int32_t)min((int64_t)lo + (int64_t)lane * step, (int64_t)hi);
+            const uint64_t on = __ballot(fits(value_of<T>(probe)));
             const int j = on ? __builtin_ctzll(on) : 64;
-            const uint32_t to = j < 64 ? __builtin_amdgcn_readlane(probe, j & 63) : hi;
+            const int32_t to = j < 64 ? __builtin_amdgcn_readlane(probe, j & 63) : hi;
             if (j > 0) lo = __builtin_amdgcn_readlane(probe, (j - 1) & 63) + 1;
             hi = to;
         }
         return lo;
     };
-    // From a bin of the distances to the border's key: histograms of the keys in it, from the largest down.
-    auto refine = [&](Found f, bool by_count, double target) {
-        uint32_t hi = f.bin == 0 ? top_key : first_key(f.bin - 1) - 1, lo = first_key(f.bin);
-        for (;;) {
-            const uint32_t range = hi - lo;
-            const int shift = max(0, 32 - (range ? __builtin_clz(range) : 32) - 11);
-            clear();
-            each([&](int32_t, const float (&x)[8]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t k = key_of<T>(x[e]);
-                    if (k >= lo && k <= hi) add((hi - k) >> shift, by_p ? weight(x[e]) : 0);
-                }
-            });
-            f = find(by_count, target, f.count, f.mass);
-            hi -= (uint32_t)f.bin << shift;
-            if (shift == 0) break;
-            lo = max(lo, hi - ((1u << shift) - 1));
-        }
-        f.bin = (int32_t)hi;
-        return f;
-    };
 
-    Border border{0, 0};
-    if (by_k || by_p) {
+    // ---- a list, or where it would begin
+    float bound = -INFINITY;
+    bool list = by_k && top_k <= kListTopK;
+    if (list) {
+        const float b = sh.wave_bound[lane & (kWaves - 1)];
+        bound = -wave_max(-b);
+        if (infinite) bound = bound == INFINITY ? 0.f : -INFINITY;
+    }
+    Bins bins{};
+    uint64_t sum = 0;  // mass of what top-k leaves
+    auto histogram = [&]() {
         clear();
-        uint64_t total = 0;
-        uint32_t count = 0;
-        each([&](int32_t, const float (&f)[8]) {
+        double mass = 0.0;
+        uint64_t masses = 0;
+        each([&](int32_t, Chunk<T> &c) __attribute__((always_inline)) {
+            mass = 0.0;
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int32_t b = bin_of(f[e]);
-                const uint64_t w = by_p ? weight(f[e]) : 0;
-                total += w;
-                if (b < kBins - 1) add(b, w);
+                for (int e = 0; e < 4; ++e) {
+                    const float v = c.value(e);
+                    const int32_t b = bin_of(v);
+                    const double w = by_p ? weight(v) : 0.0;
+                    mass += w;
+                    if (b < kBins - 1) add(b, w);
+                }
+                c.swap();
             }
+            masses += whole(mass);
         });
         // the last bin: what the others have not
         __syncthreads();
-        for (int i = tid; i < kBins - 1; i += kSampleThreads) {
-            count += sh.count[i];
-            total -= sh.mass[i];
+        Pair others{0, masses}, every;
+        for (int i = 2 * tid; i < 2 * tid + 2 && i < kBins - 1; ++i) {
+            others.count += sh.count[i];
+            others.mass -= sh.mass[i];
         }
-        uint64_t all, rest;
-        group_before(count, sh.wave_sums, all);
-        group_before(total, sh.wave_sums, rest);
+        group_before(others, sh.wave_sums, every);
         if (tid == 0) {
-            sh.count[kBins - 1] = (uint32_t)(a.vocab - (int64_t)all);
-            sh.mass[kBins - 1] = rest;
+            sh.count[kBins - 1] = (uint32_t)(a.vocab - (int64_t)every.count);
+            sh.mass[kBins - 1] = every.mass;
         }
-        uint64_t sum = 0;  // mass of the first k
-        if (by_p && !by_k) {
-            __syncthreads();
-            group_before(sh.mass[2 * tid] + sh.mass[2 * tid + 1], sh.wave_sums, sum);
+        bins = scan(Pair{0, 0});
+        if (!by_k) {
+            group_before(Pair{0, bins.m0 + bins.m1}, sh.wave_sums, every);
+            sum = every.mass;
         }
-        Found by_count{};
-        if (by_k) {
-            // the histogram of distances is looked at once more for top-p
-            const Found f = find(true, 0.0, 0, 0);
-            uint64_t keep_m0 = sh.mass[2 * tid], keep_m1 = sh.mass[2 * tid + 1];
-            uint32_t keep_c0 = sh.count[2 * tid], keep_c1 = sh.count[2 * tid + 1];
-            by_count = refine(f, true, 0.0);
-            border = Border{(uint32_t)by_count.bin, (int32_t)(top_k - by_count.count)};
-            if (by_p) {
-                sum = by_count.mass + (uint64_t)border.ties * weight(value_of<T>(border.key));
-                __syncthreads();
-                sh.mass[2 * tid] = keep_m0;
-                sh.mass[2 * tid + 1] = keep_m1;
-                sh.count[2 * tid] = keep_c0;
-                sh.count[2 * tid + 1] = keep_c1;
-            }
+    };
+    bool counted = false;
+    if (!list && by_p && !by_k) {
+        histogram();
+        counted = true;
+        const double target = (double)top_p * (double)sum;
+        if (target > 0.0) {
+            const Found f = locate(bins, false, target);
+            list = (int64_t)f.before.count + f.ties <= kList && f.bin < kBins - 1;
+            if (list) bound = value_of<T>(first_key([&](float v) { return bin_of(v) <= f.bin; }));
+        } else {
+            list = true;
+            bound = top;
         }
-        if (by_p) {
-            const double target = (double)top_p * (double)sum;
-            Border p{top_key, 1};
-            if (target > 0.0) {
-                const Found f = refine(find(false, target, 0, 0), false, target);
-                p.key = (uint32_t)f.bin;
-                // equals stay while the mass before them is below the target
-                const uint64_t w = weight(value_of<T>(p.key));
-                int32_t lo = 0, hi = f.ties;  // the first that does not
-                while (lo < hi) {
-                    const int32_t mid = lo + (hi - lo) / 2;
-                    if ((double)(f.mass + (uint64_t)mid * w) < target) lo = mid + 1;
-                    else hi = mid;
+    }
+    if (list) {
+        each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+            if (!__any(c.largest() >= bound)) return;
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = c.value(e);
+                    if (v >= bound) {
+                        const int32_t n = __hip_atomic_fetch_add(&sh.listed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                        const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);  // -0 as 0
+                        const uint32_t at = (uint32_t)(8 * (64 * s + lane) + i + e - row.before);
+                        if (n < kList) {
+                            sh.order[n] = (uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | ~at;
+                            sh.weight[n] = whole(weight(v));
+                            sh.before[n] = 0;
+                            sh.rank[n] = 0;
+                        }
+                    }
                 }
-                p.ties = lo;
+                c.swap();
             }
-            if (!by_k || p.key > border.key) border = p;
-            else if (p.key == border.key) border.ties = min(border.ties, p.ties);
+        });
+        __syncthreads();
+        const int32_t n = sh.listed;
+        if (n <= kList) {
+            // Candidates in blocks of 64, a lane each; the wavefronts of a block share the others among them.
+            const int blocks = (n + 63) / 64, share = kWaves / blocks, part = wave / blocks;
+            const int i = 64 * (wave % blocks) + lane;
+            const int j0 = n * part / share, j1 = part < share ? n * (part + 1) / share : j0;
+            const bool mine = i < n;
+            const uint64_t order = mine ? sh.order[i] : 0, w = mine ? sh.weight[i] : 0;
+            uint32_t rank = 0;
+            uint64_t before = 0;
+            for (int j = j0; j < j1; ++j) {
+                const bool sooner = sh.order[j] > order;
+                rank += sooner ? 1 : 0;
+                before += sooner ? sh.weight[j] : 0;
+            }
+            if (mine && j0 < j1) {
+                __hip_atomic_fetch_add(&sh.rank[i], rank, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                __hip_atomic_fetch_add(&sh.before[i], before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+            __syncthreads();
+            if (mine) {
+                rank = sh.rank[i];
+                before = sh.before[i];
+            }
+            if (by_k) {
+                if (part == 0 && mine && (int32_t)rank == min(top_k, n) - 1) sh.total = before + w;
+                __syncthreads();
+                sum = sh.total;
+            }
+            bool stays = mine && (!by_k || (int32_t)rank < top_k);
+            stays = stays && (!by_p || rank == 0 || (double)before < (double)top_p * (double)sum);
+            const uint64_t kw = stays && (double)w >= least ? w : 0;
+            __syncthreads();  // every wavefront has read what comes before its candidates
+            if (part == 0 && mine) {
+                sh.weight[i] = kw;
+                sh.before[i] = 0;
+            }
+            __syncthreads();
+            // by index now; the sums of all parts are those of all candidates
+            before = 0;
+            uint64_t total = 0;
+            for (int j = j0; j < j1; ++j) before += (uint32_t)sh.order[j] > (uint32_t)order ? sh.weight[j] : 0;
+            if (mine && j0 < j1) __hip_atomic_fetch_add(&sh.before[i], before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __syncthreads();
+            if (wave >= blocks) return;
+            for (int j = lane; j < n; j += 64) total += sh.weight[j];
+            total = lane_of(wave_scan64(total), 63);
+            const uint64_t at = min((uint64_t)((double)u * (double)total), total - 1);
+            before = mine ? sh.before[i] : 0;
+            if (mine && before <= at && at < before + kw) {
+                a.token[r] = (int32_t)~(uint32_t)order;
+                if (a.logprob) {
+                    const uint32_t b = (uint32_t)(order >> 32);
+                    const float v = __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7fffffffu : ~b);
+                    a.logprob[r] = (float)(((double)v - (double)top) / (double)temperature -
+                                           log((double)total / (double)(1ull << kUnitBits)));
+                }
+            }
+            return;
         }
     }
 
-    // What stays, by segments.
-    const uint64_t least = (uint64_t)__builtin_ceil((double)min_p * (double)(1ull << kUnitBits));
-    auto kept = [&](float f) {
-        const uint64_t w = weight(f);
-        return w >= least ? w : 0;
-    };
-    each([&](int32_t s, const float (&f)[8]) {
-        uint64_t mass = 0;
-        uint32_t ties = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t k = key_of<T>(f[e]);
-            if (k > border.key) mass += kept(f[e]);
-            ties += k == border.key ? 1 : 0;
+    // ---- without one: the border
+    Border border{-INFINITY, a.vocab + 8};  // all stay (what is no logit, too: it weighs 0)
+    if (by_k || by_p) {
+        if (!counted) histogram();
+#pragma unroll 1
+        for (int what = by_k ? 0 : 1; what < (by_p ? 2 : 1); ++what) {
+            const bool by_count = what == 0;
+            const double target = by_count ? 0.0 : (double)top_p * (double)sum;
+            Border b{top, 1};
+            if (by_count || target > 0.0) {
+                Found f = locate(bins, by_count, target);
+                int32_t edge[2];
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i)  // (no bin is below 0: the largest)
+                    edge[i] = first_key([&](float v) { return bin_of(v) <= f.bin - i; });
+                int32_t lo = edge[0], hi = f.bin > 0 ? edge[1] - 1 : edge[1];
+                for (;;) {
+                    const uint32_t range = (uint32_t)hi - (uint32_t)lo;
+                    const int shift = max(0, 32 - (range ? __builtin_clz(range) : 32) - 11);
+                    const float from = value_of<T>(lo), to = value_of<T>(hi);
+                    clear();
+                    all([&](float v) __attribute__((always_inline)) {
+                        if (v >= from && v <= to)
+                            add((int32_t)(((uint32_t)hi - (uint32_t)key_of<T>(v)) >> shift), by_p ? weight(v) : 0.0);
+                    });
+                    f = locate(scan(f.before), by_count, target);
+                    hi = (int32_t)((uint32_t)hi - ((uint32_t)f.bin << shift));
+                    if (shift == 0) break;
+                    const uint32_t rest = (uint32_t)hi - (uint32_t)lo;
+                    if (rest > (1u << shift) - 1) lo = (int32_t)((uint32_t)hi - ((1u << shift) - 1));
+                }
+                b.value = value_of<T>(hi);
+                const uint64_t w = whole(weight(b.value));
+                if (by_count) {
+                    b.ties = (int32_t)(top_k - (int64_t)f.before.count);
+                    sum = f.before.mass + (uint64_t)b.ties * w;
+                } else {  // equals stay while the mass before them is below the target
+                    int32_t less = 0, more = f.ties;
+                    while (less < more) {
+                        const int32_t mid = less + (more - less) / 2;
+                        if ((double)(f.before.mass + (uint64_t)mid * w) < target) less = mid + 1;
+                        else more = mid;
+                    }
+                    b.ties = less;
+                }
+            }
+            if (what == 1 && by_k && b.value == border.value) b.ties = min(b.ties, border.ties);
+            if (what == 0 || !by_k || b.value >= border.value) border = b;
         }
-        mass = wave_sum(mass);
-        ties = (uint32_t)wave_sum(ties);
+    }
+
+    if (min_p > 0.f) {
+        const float v = value_of<T>(first_key([&](float x) { return weight(x) >= least; }));
+        if (v > border.value) border = Border{v, a.vocab + 8};
+    }
+
+    // ---- what stays, by segments
+    each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+        double mass = 0.0;
+        uint32_t ties = 0;
+        if (__any(c.largest() >= border.value)) {
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = c.value(e);
+                    if (v > border.value) mass += weight(v);
+                    ties += v == border.value ? 1 : 0;
+                }
+                c.swap();
+            }
+        }
+        const uint64_t m = lane_of(wave_scan64(whole(mass)), 63), n = lane_of(wave_scan64(ties), 63);
         if (lane == 0) {
-            seg_mass[s] = mass;
-            seg_ties[s] = ties;
+            seg_mass[s] = m;
+            seg_ties[s] = (uint32_t)n;
         }
     });
     __syncthreads();
-    const uint64_t tie = border.key ? kept(value_of<T>(border.key)) : 0;
+    const uint64_t tie = whole(weight(border.value));
     const int32_t per_thread = (row.segments + kSampleThreads - 1) / kSampleThreads;
     const int32_t s0 = min(tid * per_thread, row.segments), s1 = min(s0 + per_thread, row.segments);
-    uint64_t ties = 0, all, mass = 0, total;
-    for (int32_t s = s0; s < s1; ++s) ties += seg_ties[s];
-    const int64_t ties_before = (int64_t)group_before(ties, sh.wave_sums, all);
-    int64_t left = border.ties - ties_before;
+    auto stays = [&](int32_t s, int64_t left) {  // mass of a segment whose first `left` equals stay
+        return seg_mass[s] + (uint64_t)max((int64_t)0, min(left, (int64_t)seg_ties[s])) * tie;
+    };
+    Pair own{0, 0}, every;
+    for (int32_t s = s0; s < s1; ++s) own.count += seg_ties[s];
+    const int64_t left0 = border.ties - (int64_t)group_before(own, sh.wave_sums, every).count;
+    int64_t left = left0;
     for (int32_t s = s0; s < s1; ++s) {
-        mass += seg_mass[s] + (uint64_t)max((int64_t)0, min(left, (int64_t)seg_ties[s])) * tie;
+        own.mass += stays(s, left);
         left -= seg_ties[s];
     }
-    uint64_t before = group_before(mass, sh.wave_sums, total);
-    const uint64_t at = min((uint64_t)((double)u * (double)total), total - 1);
-    left = border.ties - ties_before;
-    for (int32_t s = s0; s < s1; ++s) {
-        const uint64_t m = seg_mass[s] + (uint64_t)max((int64_t)0, min(left, (int64_t)seg_ties[s])) * tie;
-        if (before <= at && at < before + m) {
-            sh.found = s;
-            sh.found_mass = before;
-            sh.found_count = left;
+    uint64_t before = group_before(own, sh.wave_sums, every).mass;
+    const uint64_t total = every.mass, at = min((uint64_t)((double)u * (double)total), total - 1);
+    if (before <= at && at < before + own.mass) {
+        left = left0;
+        for (int32_t s = s0; s < s1; ++s) {
+            const uint64_t m = stays(s, left);
+            if (before <= at && at < before + m) {
+                sh.found = s;
+                sh.found_mass = before;
+                sh.found_count = left;
+            }
+            before += m;
+            left -= seg_ties[s];
         }
-        before += m;
-        left -= seg_ties[s];
     }
     __syncthreads();
     // The token in its segment, by one wavefront.
     if (wave != 0) return;
     const int32_t c = 64 * sh.found + lane;
-    float f[8];
-    if (c < row.chunks) row.load(c, f);
-    else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(float, 0xffffffffu);
-    uint32_t mine = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mine += key_of<T>(f[e]) == border.key ? 1 : 0;
-    int64_t room = sh.found_count - (int64_t)wave_before(mine);
-    uint64_t w[8], sum = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t k = key_of<T>(f[e]);
-        const bool equal = k == border.key;
-        w[e] = k > border.key || (equal && room > 0) ? kept(f[e]) : 0;
-        if (equal) --room;
-        sum += w[e];
-    }
-    uint64_t from = sh.found_mass + wave_before(sum);
-    if (from <= at && at < from + sum) {
-        for (int e = 0; e < 8; ++e) {
-            if (at < from + w[e]) {
-                a.token[r] = 8 * c + e - row.before;
-                if (a.logprob)
-                    a.logprob[r] = (float)(((double)f[e] - (double)top) / (double)temperature -
-                                           log((double)total / (double)(1ull << kUnitBits)));
-                break;
-            }
-            from += w[e];
+    Chunk<T> chunk = row.bits(c);
+    chunk.clean();
+    if (infinite) chunk.only_infinite();
+    // thrice over the eight: their equals of the border, their mass, and the one that the draw falls on
+    uint64_t equals = 0, mass = 0, from = 0;
+    int64_t room0 = 0, room = 0;
+#pragma unroll 1
+    for (int i = 0; i < 24; ++i) {
+        if (i == 8) room0 = room = sh.found_count - (int64_t)(wave_scan64(equals) - equals);
+        if (i == 16) {
+            from = sh.found_mass + wave_scan64(mass) - mass;
+            room = room0;
         }
+        const float v = chunk.value(0);
+        const uint32_t bits = chunk.w[0];
+        const bool equal = v == border.value;
+        if (i < 8) {
+            equals += equal ? 1 : 0;
+        } else {
+            const uint64_t w = v > border.value || (equal && room > 0) ? whole(weight(v)) : 0;
+            if (equal) --room;
+            if (i < 16) {
+                mass += w;
+            } else {
+                if (from <= at && at < from + w) {
+                    a.token[r] = 8 * c + (i - 16) - row.before;
+                    if (a.logprob)
+                        a.logprob[r] = (float)(((double)v - (double)top) / (double)temperature -
+                                               log((double)total / (double)(1ull << kUnitBits)));
+                }
+                from += w;
+            }
+        }
+        chunk.put(bits & (Chunk<T>::kHalf ? 0xffffu : 0xffffffffu));
     }
 }
 
 int32_t sample_segments(int32_t vocab) { return (vocab + 7 + 7) / 8 / 64 + 1; }
+
+// LDS beside the histograms: segments' masses and ties, and the keys where they are kept.
+size_t sample_lds(int32_t vocab, int elem, bool kept)
+{
+    const size_t segments = sample_segments(vocab);
+    return (segments + 1) / 2 * 16 + (segments + 3) / 4 * 16 + (kept ? segments * 512 * elem : 0);
+}
+
+template <typename T>
+void sample_launch(const lora_sample_args &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)a.n_rows);
+    const size_t lds = sample_lds(a.vocab, sizeof(typename T::elem), true);
+    if (lds <= kSampleLds) launch(lora_sample_kernel<T, true>, grid, kSampleThreads, lds, s, a);
+    else launch(lora_sample_kernel<T, false>, grid, kSampleThreads, sample_lds(a.vocab, 0, false), s, a);
+}
 
 }  // namespace
 }  // namespace lora
@@ -539,11 +862,9 @@ int lora_sample(void *stream, const lora_sample_args *args)
     int st = check_rows(a.n_rows, kSampleThreads);
     if (st) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const size_t lds = (size_t)sample_segments(a.vocab) * 12;
-    const dim3 grid((unsigned)a.n_rows);
-    if (a.type == LORA_TYPE_F16) launch(lora_sample_kernel<F16>, grid, kSampleThreads, lds, s, a);
-    else if (a.type == LORA_TYPE_BF16) launch(lora_sample_kernel<BF16>, grid, kSampleThreads, lds, s, a);
-    else launch(lora_sample_kernel<F32>, grid, kSampleThreads, lds, s, a);
+    if (a.type == LORA_TYPE_F16) sample_launch<F16>(a, s);
+    else if (a.type == LORA_TYPE_BF16) sample_launch<BF16>(a, s);
+    else sample_launch<F32>(a, s);
     return launch_status("sample");
 }
 
