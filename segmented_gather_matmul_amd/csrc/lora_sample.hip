@@ -70,6 +70,13 @@ struct alignas(16) Chunk {
         else if constexpr (kHalf) return __builtin_bit_cast(float, e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
         else return __builtin_bit_cast(float, w[e]);
     }
+    // Logit e of the eight, in LDS.
+    __device__ inline float one(int e) const
+    {
+        if constexpr (std::is_same_v<T, F16>) return (float)reinterpret_cast<const _Float16 *>(w)[e];
+        else if constexpr (kHalf) return __builtin_bit_cast(float, (uint32_t)reinterpret_cast<const uint16_t *>(w)[e] << 16);
+        else return __builtin_bit_cast(float, w[e]);
+    }
     // The last four in the place of the first: loops over the logits take two rounds of four, for little code.
     __device__ inline void swap()
     {
@@ -153,6 +160,12 @@ struct Row {
     int32_t before;       // elements of it that lie before the row
     int32_t vocab, chunks, segments;
 
+    // Logit e, counted from the first chunk's beginning; NaN as -inf.
+    __device__ inline float one(int32_t e) const
+    {
+        const float v = (float)reinterpret_cast<const typename T::elem *>(base)[e];
+        return v >= -INFINITY ? v : -INFINITY;
+    }
     // The bits of chunk c; what is no logit of the row is -inf.
     __device__ inline Chunk<T> bits(int32_t c) const
     {
@@ -296,14 +309,16 @@ struct Shared {
     Pair wave_sums[kWaves];
     float wave_best[kWaves], wave_bound[kWaves];
     int32_t wave_at[kWaves];
-    // the list: value and index as one number, larger where it comes first; weight; what comes before
-    uint64_t order[kList], weight[kList], before[kList];
-    uint32_t rank[kList];
-    uint64_t total;
+    // the list: value and index as one number, larger where it comes first; weight; the candidates in order, and their
+    // places by index
+    uint64_t order[kList], weight[kList], line[kList];
+    uint8_t place[kList], place_by_index[kList];
+    int32_t chunk[kList];
     int32_t listed;
     uint64_t found_mass;
     int64_t found_count;
     int32_t found, found_ties;
+    float found_value;
 };
 
 // One workgroup per row.  Its logits are kept in LDS (KEPT), or the row is read again in every pass.
@@ -312,11 +327,11 @@ struct Shared {
 //     reach, and the lowest of these is taken.  What reaches it (mostly little more than k) is put on a list.
 //   - Otherwise, for top-k and top-p, a histogram of how many and what mass lie how far below the largest, and the
 //     bin in which the border lies.  If few lie above it, they are put on the list.
-//   - On the list, everything follows from how many and what mass come before each candidate, in order and by index,
-//     found by comparing all with all.
-//   - Without a list: histograms of the values between two bounds, narrower until a bin is one value, give the border and how
-//     many of its equals stay; then the mass that stays of each segment of 512 logits, the segment that the draw
-//     falls into, and the token in it.
+//   - On a list of at most 256, a candidate's place in order and by index is the number of those before it, counted by
+//     ballots; one wavefront then goes along the list.
+//   - Without one: the list of what lies in the border's bin gives the border and how many of its equals stay (or, where
+//     that is too much, histograms of the values between two bounds, narrower until a bin is one value); then the
+//     mass that stays of each segment of 512 logits, the segment that the draw falls into, and the token in it.
 // Counts and masses are whole numbers, so the order of their atomics does not matter.
 //
 // Bound by arithmetic where every logit's weight is needed (no filter, top-p): some 30 instructions a logit, most
@@ -439,6 +454,12 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     const double rate = 1.44269504088896340736 / (double)temperature;
     auto weight = [&](float v) { return weight_of(((double)v - (double)top) * rate); };
     const double least = (double)min_p * (double)(1ull << kUnitBits);
+    auto finish = [&](int32_t token, float v, uint64_t total) {
+        a.token[r] = token;
+        if (a.logprob)
+            a.logprob[r] = (float)(((double)v - (double)top) / (double)temperature -
+                                   log((double)total / (double)(1ull << kUnitBits)));
+    };
     // Bins by the distance from the largest: 1/64 of a power of two each, the last one takes all beyond.
     const float per = (float)__builtin_fmin(rate * 64.0, 1e30);
     auto bin_of = [&](float v) { return (int32_t)__builtin_fminf((top - v) * per, (float)(kBins - 1)); };
@@ -459,10 +480,9 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
         uint64_t m0, m1;
         Pair before;
     };
-    auto scan = [&](Pair from) {
+    auto scan = [&](Pair from, Pair &every) {
         __syncthreads();
         Bins b{sh.count[2 * tid], sh.count[2 * tid + 1], sh.mass[2 * tid], sh.mass[2 * tid + 1], {0, 0}};
-        Pair every;
         b.before = group_before(Pair{(uint64_t)b.c0 + b.c1, b.m0 + b.m1}, sh.wave_sums, every);
         b.before.count += from.count;
         b.before.mass += from.mass;
@@ -508,6 +528,86 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
         return lo;
     };
 
+    // One logit onto the list, whose length is counted beyond its end.
+    auto put = [&](float v, uint32_t at) {
+        const int32_t n = __hip_atomic_fetch_add(&sh.listed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);  // -0 as 0
+        if (n < kList) sh.order[n] = (uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | ~at;
+    };
+    // Puts all logits from `bound` up on the list: the chunks that have one, and then a thread for each of their logits.
+    auto gather_from = [&](float from) __attribute__((always_inline)) {
+        if (tid == 0) sh.found = 0;
+        __syncthreads();
+        each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+            if (c.largest() >= from) {
+                const int32_t n = __hip_atomic_fetch_add(&sh.found, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                if (n < kList) sh.chunk[n] = 64 * s + lane;
+            }
+        });
+        __syncthreads();
+        const int32_t n = sh.found;
+        if (n > kList) return n;
+        for (int32_t i = tid; i < 8 * n; i += kSampleThreads) {
+            const int32_t c = sh.chunk[i / 8];
+            const uint32_t at = (uint32_t)(8 * c + i % 8 - row.before);
+            if (at >= (uint32_t)row.vocab) continue;
+            float v;
+            if constexpr (KEPT) v = held[c].one(i % 8);
+            else v = row.one(8 * c + i % 8);
+            if (infinite) v = v == INFINITY ? 0.f : -INFINITY;
+            if (v >= from) put(v, at);
+        }
+        __syncthreads();
+        return sh.listed;
+    };
+    // Puts all logits of a bin on the list.
+    auto gather_bin = [&](int32_t bin) __attribute__((always_inline)) {
+        each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = c.value(e);
+                    const uint32_t at = (uint32_t)(8 * (64 * s + lane) + i + e - row.before);
+                    if (bin_of(v) == bin && at < (uint32_t)row.vocab) put(v, at);
+                }
+                c.swap();
+            }
+        });
+        __syncthreads();
+        return sh.listed;
+    };
+    auto value_on_list = [](uint64_t order) {
+        const uint32_t b = (uint32_t)(order >> 32);
+        return __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7fffffffu : ~b);
+    };
+    // The places of the list's n candidates and their weights; each wavefront counts for every sixteenth.
+    auto arrange = [&](int32_t n) {
+        uint64_t o[kList / 64];
+#pragma unroll
+        for (int q = 0; q < kList / 64; ++q) o[q] = 64 * q + lane < n ? sh.order[64 * q + lane] : 0;
+        if (tid < n) sh.weight[tid] = whole(weight(value_on_list(sh.order[tid])));
+#pragma unroll
+        for (int q = 0; q < kList / 64; ++q) {
+#pragma unroll 1
+            for (int l = wave; l < 64 && 64 * q + l < n; l += kWaves) {
+                const uint64_t mine = lane_of(o[q], l);
+                int sooner = 0, lower = 0;
+#pragma unroll
+                for (int j = 0; j < kList / 64; ++j) {
+                    if (64 * j >= n) break;
+                    sooner += __builtin_popcountll(__ballot(o[j] > mine));
+                    lower += __builtin_popcountll(__ballot((uint32_t)o[j] > (uint32_t)mine));
+                }
+                if (lane == 0) {
+                    sh.place[sooner] = (uint8_t)(64 * q + l);
+                    sh.place_by_index[64 * q + l] = (uint8_t)lower;
+                }
+            }
+        }
+        __syncthreads();
+    };
+
     // ---- a list, or where it would begin
     float bound = -INFINITY;
     bool list = by_k && top_k <= kListTopK;
@@ -518,170 +618,198 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     }
     Bins bins{};
     uint64_t sum = 0;  // mass of what top-k leaves
-    auto histogram = [&]() {
-        clear();
-        double mass = 0.0;
-        uint64_t masses = 0;
-        each([&](int32_t, Chunk<T> &c) __attribute__((always_inline)) {
-            mass = 0.0;
-#pragma unroll 1
-            for (int i = 0; i < 8; i += 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = c.value(e);
-                    const int32_t b = bin_of(v);
-                    const double w = by_p ? weight(v) : 0.0;
-                    mass += w;
-                    if (b < kBins - 1) add(b, w);
-                }
-                c.swap();
-            }
-            masses += whole(mass);
-        });
-        // the last bin: what the others have not
-        __syncthreads();
-        Pair others{0, masses}, every;
-        for (int i = 2 * tid; i < 2 * tid + 2 && i < kBins - 1; ++i) {
-            others.count += sh.count[i];
-            others.mass -= sh.mass[i];
-        }
-        group_before(others, sh.wave_sums, every);
-        if (tid == 0) {
-            sh.count[kBins - 1] = (uint32_t)(a.vocab - (int64_t)every.count);
-            sh.mass[kBins - 1] = every.mass;
-        }
-        bins = scan(Pair{0, 0});
-        if (!by_k) {
-            group_before(Pair{0, bins.m0 + bins.m1}, sh.wave_sums, every);
-            sum = every.mass;
-        }
-    };
     bool counted = false;
-    if (!list && by_p && !by_k) {
-        histogram();
-        counted = true;
-        const double target = (double)top_p * (double)sum;
-        if (target > 0.0) {
-            const Found f = locate(bins, false, target);
-            list = (int64_t)f.before.count + f.ties <= kList && f.bin < kBins - 1;
-            if (list) bound = value_of<T>(first_key([&](float v) { return bin_of(v) <= f.bin; }));
-        } else {
-            list = true;
-            bound = top;
-        }
-    }
-    if (list) {
-        each([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
-            if (!__any(c.largest() >= bound)) return;
 #pragma unroll 1
-            for (int i = 0; i < 8; i += 4) {
+    for (int round = 0; round < 2; ++round) {
+        // A histogram: for top-p alone at first, for all that is filtered where a list has come to nothing.
+        if ((by_k || by_p) && !counted && (round == 1 || !list) && (round == 1 || !by_k)) {
+            counted = true;
+            clear();
+            uint64_t masses = 0;
+            each([&](int32_t, Chunk<T> &c) __attribute__((always_inline)) {
+                double mass = 0.0;
+#pragma unroll 1
+                for (int i = 0; i < 8; i += 4) {
+                    double w[4] = {0.0, 0.0, 0.0, 0.0};
+                    if (by_p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = c.value(e);
-                    if (v >= bound) {
-                        const int32_t n = __hip_atomic_fetch_add(&sh.listed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                        const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);  // -0 as 0
-                        const uint32_t at = (uint32_t)(8 * (64 * s + lane) + i + e - row.before);
-                        if (n < kList) {
-                            sh.order[n] = (uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | ~at;
-                            sh.weight[n] = whole(weight(v));
-                            sh.before[n] = 0;
-                            sh.rank[n] = 0;
-                        }
+                        for (int e = 0; e < 4; ++e) w[e] = weight(c.value(e));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t b = bin_of(c.value(e));
+                        mass += w[e];
+                        if (b < kBins - 1) add(b, w[e]);
                     }
+                    c.swap();
                 }
-                c.swap();
-            }
-        });
-        __syncthreads();
-        const int32_t n = sh.listed;
-        if (n <= kList) {
-            // Candidates in blocks of 64, a lane each; the wavefronts of a block share the others among them.
-            const int blocks = (n + 63) / 64, share = kWaves / blocks, part = wave / blocks;
-            const int i = 64 * (wave % blocks) + lane;
-            const int j0 = n * part / share, j1 = part < share ? n * (part + 1) / share : j0;
-            const bool mine = i < n;
-            const uint64_t order = mine ? sh.order[i] : 0, w = mine ? sh.weight[i] : 0;
-            uint32_t rank = 0;
-            uint64_t before = 0;
-            for (int j = j0; j < j1; ++j) {
-                const bool sooner = sh.order[j] > order;
-                rank += sooner ? 1 : 0;
-                before += sooner ? sh.weight[j] : 0;
-            }
-            if (mine && j0 < j1) {
-                __hip_atomic_fetch_add(&sh.rank[i], rank, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-                __hip_atomic_fetch_add(&sh.before[i], before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            }
+                masses += whole(mass);
+            });
+            // the last bin: what the others have not
             __syncthreads();
-            if (mine) {
-                rank = sh.rank[i];
-                before = sh.before[i];
+            Pair others{0, masses}, every;
+            for (int i = 2 * tid; i < 2 * tid + 2 && i < kBins - 1; ++i) {
+                others.count += sh.count[i];
+                others.mass -= sh.mass[i];
             }
-            if (by_k) {
-                if (part == 0 && mine && (int32_t)rank == min(top_k, n) - 1) sh.total = before + w;
-                __syncthreads();
-                sum = sh.total;
+            group_before(others, sh.wave_sums, every);
+            if (tid == 0) {
+                sh.count[kBins - 1] = (uint32_t)(a.vocab - (int64_t)every.count);
+                sh.mass[kBins - 1] = every.mass;
             }
-            bool stays = mine && (!by_k || (int32_t)rank < top_k);
-            stays = stays && (!by_p || rank == 0 || (double)before < (double)top_p * (double)sum);
-            const uint64_t kw = stays && (double)w >= least ? w : 0;
-            __syncthreads();  // every wavefront has read what comes before its candidates
-            if (part == 0 && mine) {
-                sh.weight[i] = kw;
-                sh.before[i] = 0;
-            }
-            __syncthreads();
-            // by index now; the sums of all parts are those of all candidates
-            before = 0;
-            uint64_t total = 0;
-            for (int j = j0; j < j1; ++j) before += (uint32_t)sh.order[j] > (uint32_t)order ? sh.weight[j] : 0;
-            if (mine && j0 < j1) __hip_atomic_fetch_add(&sh.before[i], before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            __syncthreads();
-            if (wave >= blocks) return;
-            for (int j = lane; j < n; j += 64) total += sh.weight[j];
-            total = lane_of(wave_scan64(total), 63);
-            const uint64_t at = min((uint64_t)((double)u * (double)total), total - 1);
-            before = mine ? sh.before[i] : 0;
-            if (mine && before <= at && at < before + kw) {
-                a.token[r] = (int32_t)~(uint32_t)order;
-                if (a.logprob) {
-                    const uint32_t b = (uint32_t)(order >> 32);
-                    const float v = __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7fffffffu : ~b);
-                    a.logprob[r] = (float)(((double)v - (double)top) / (double)temperature -
-                                           log((double)total / (double)(1ull << kUnitBits)));
-                }
-            }
-            return;
+            bins = scan(Pair{0, 0}, every);
+            if (!by_k) sum = every.mass;
         }
+        if (round == 1) break;
+        if (counted) {  // top-p alone: a list of all that lies above the end of the border's bin
+            const double target = (double)top_p * (double)sum;
+            if (target > 0.0) {
+                const Found f = locate(bins, false, target);
+                list = (int64_t)f.before.count + f.ties <= kList && f.bin < kBins - 1;
+                if (list) bound = value_of<T>(first_key([&](float v) { return bin_of(v) <= f.bin; }));
+            } else {
+                list = true;
+                bound = top;
+            }
+        }
+        if (!list) continue;
+        const int32_t n = gather_from(bound);
+        if (n > kList) continue;
+        arrange(n);
+        if (wave != 0) return;
+        // Four candidates a lane, in order.
+        uint64_t w[4], before[4], mass = 0;
+        int32_t who[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int32_t rank = 4 * lane + q;
+            who[q] = rank < n ? sh.place[rank] : 0;
+            w[q] = rank < n ? sh.weight[who[q]] : 0;
+            before[q] = mass;
+            mass += w[q];
+        }
+        const uint64_t ahead = wave_scan64(mass) - mass;
+        if (by_k) {  // the mass of the first k
+            uint64_t k_mass = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) k_mass += 4 * lane + q < top_k ? w[q] : 0;
+            sum = lane_of(wave_scan64(k_mass), 63);
+        }
+        const double target = (double)top_p * (double)sum;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int32_t rank = 4 * lane + q;
+            const bool stays = rank < n && (!by_k || rank < top_k) &&
+                               (!by_p || rank == 0 || (double)(ahead + before[q]) < target) && (double)w[q] >= least;
+            if (rank < n) sh.line[sh.place_by_index[who[q]]] = stays ? w[q] : 0;
+        }
+        // and by index
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        mass = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            w[q] = 4 * lane + q < n ? sh.line[4 * lane + q] : 0;
+            before[q] = mass;
+            mass += w[q];
+        }
+        const uint64_t upto = wave_scan64(mass), total = lane_of(upto, 63);
+        const uint64_t at = min((uint64_t)((double)u * (double)total), total - 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint64_t from = upto - mass + before[q];
+            if (from <= at && at < from + w[q]) sh.found = 4 * lane + q;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int32_t chosen = sh.found;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (64 * q + lane < n && sh.place_by_index[64 * q + lane] == chosen) {
+                const uint64_t order = sh.order[64 * q + lane];
+                finish((int32_t)~(uint32_t)order, value_on_list(order), total);
+            }
+        return;
     }
 
     // ---- without one: the border
     Border border{-INFINITY, a.vocab + 8};  // all stay (what is no logit, too: it weighs 0)
-    if (by_k || by_p) {
-        if (!counted) histogram();
 #pragma unroll 1
-        for (int what = by_k ? 0 : 1; what < (by_p ? 2 : 1); ++what) {
-            const bool by_count = what == 0;
-            const double target = by_count ? 0.0 : (double)top_p * (double)sum;
-            Border b{top, 1};
-            if (by_count || target > 0.0) {
-                Found f = locate(bins, by_count, target);
-                int32_t edge[2];
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i)  // (no bin is below 0: the largest)
-                    edge[i] = first_key([&](float v) { return bin_of(v) <= f.bin - i; });
-                int32_t lo = edge[0], hi = f.bin > 0 ? edge[1] - 1 : edge[1];
-                for (;;) {
-                    const uint32_t range = (uint32_t)hi - (uint32_t)lo;
-                    const int shift = max(0, 32 - (range ? __builtin_clz(range) : 32) - 11);
+    for (int what = by_k ? 0 : 1; what < (by_p ? 2 : 1); ++what) {
+        const bool by_count = what == 0;
+        const double target = by_count ? 0.0 : (double)top_p * (double)sum;
+        Border b{top, 1};
+        if (by_count || target > 0.0) {
+            Found f = locate(bins, by_count, target);
+            const int32_t bin = f.bin;
+            if (f.ties <= kList) {  // (`ties` counts the bin)
+                if (tid == 0) sh.listed = 0;
+                __syncthreads();
+                const int32_t n = gather_bin(bin);  // (f.ties)
+                arrange(n);
+                if (wave == 0) {
+                    uint64_t w[4], before[4], mass = 0;
+                    int32_t who[4], left = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int32_t rank = 4 * lane + q;
+                        who[q] = rank < n ? sh.place[rank] : 0;
+                        w[q] = rank < n ? sh.weight[who[q]] : 0;
+                        before[q] = mass;
+                        mass += w[q];
+                    }
+                    const uint64_t ahead = f.before.mass + wave_scan64(mass) - mass;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int32_t rank = 4 * lane + q;
+                        const bool stays = rank < n && (by_count ? (int64_t)f.before.count + rank < top_k : (double)(ahead + before[q]) < target);
+                        left += __builtin_popcountll(__ballot(stays));
+                    }
+                    // the last that stays, and its equals before it
+                    const float value = value_on_list(sh.order[sh.place[max(left - 1, 0)]]);
+                    int32_t ties = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int32_t rank = 4 * lane + q;
+                        ties += __builtin_popcountll(__ballot(rank < left && value_on_list(sh.order[who[q]]) == value));
+                        if (rank == left - 1) sh.found_mass = ahead + before[q] + w[q];
+                    }
+                    if (lane == 0) {
+                        sh.found_value = value;
+                        sh.found_ties = ties;
+                    }
+                }
+                __syncthreads();
+                b = Border{sh.found_value, sh.found_ties};
+                if (by_count) sum = sh.found_mass;
+                __syncthreads();
+            } else {
+                // what lies in it, from the least to the largest
+                float least_in = INFINITY, most_in = -INFINITY;
+                all([&](float v) __attribute__((always_inline)) {
+                    const bool in = bin_of(v) == bin;
+                    least_in = in ? __builtin_fminf(least_in, v) : least_in;
+                    most_in = in ? __builtin_fmaxf(most_in, v) : most_in;
+                });
+                least_in = -wave_max(-least_in);
+                most_in = wave_max(most_in);
+                if (lane == 0) {
+                    sh.wave_best[wave] = most_in;
+                    sh.wave_bound[wave] = -least_in;
+                }
+                __syncthreads();
+                most_in = wave_max(sh.wave_best[lane & (kWaves - 1)]);
+                least_in = -wave_max(sh.wave_bound[lane & (kWaves - 1)]);
+                int32_t lo = key_of<T>(least_in), hi = key_of<T>(most_in);
+                while (lo < hi) {
+                    const int shift = max(0, 32 - __builtin_clz((uint32_t)hi - (uint32_t)lo) - 11);
                     const float from = value_of<T>(lo), to = value_of<T>(hi);
                     clear();
                     all([&](float v) __attribute__((always_inline)) {
                         if (v >= from && v <= to)
                             add((int32_t)(((uint32_t)hi - (uint32_t)key_of<T>(v)) >> shift), by_p ? weight(v) : 0.0);
                     });
-                    f = locate(scan(f.before), by_count, target);
+                    Pair every;
+                    f = locate(scan(f.before, every), by_count, target);
                     hi = (int32_t)((uint32_t)hi - ((uint32_t)f.bin << shift));
                     if (shift == 0) break;
                     const uint32_t rest = (uint32_t)hi - (uint32_t)lo;
@@ -702,11 +830,10 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
                     b.ties = less;
                 }
             }
-            if (what == 1 && by_k && b.value == border.value) b.ties = min(b.ties, border.ties);
-            if (what == 0 || !by_k || b.value >= border.value) border = b;
         }
+        if (what == 1 && by_k && b.value == border.value) b.ties = min(b.ties, border.ties);
+        if (what == 0 || !by_k || b.value >= border.value) border = b;
     }
-
     if (min_p > 0.f) {
         const float v = value_of<T>(first_key([&](float x) { return weight(x) >= least; }));
         if (v > border.value) border = Border{v, a.vocab + 8};
@@ -722,7 +849,7 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v = c.value(e);
-                    if (v > border.value) mass += weight(v);
+                    mass += weight(v > border.value ? v : -INFINITY);
                     ties += v == border.value ? 1 : 0;
                 }
                 c.swap();
@@ -743,7 +870,8 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     };
     Pair own{0, 0}, every;
     for (int32_t s = s0; s < s1; ++s) own.count += seg_ties[s];
-    const int64_t left0 = border.ties - (int64_t)group_before(own, sh.wave_sums, every).count;
+    int64_t left0 = border.ties;  // (all equals stay where there are more than logits)
+    if (border.ties <= a.vocab) left0 -= (int64_t)group_before(own, sh.wave_sums, every).count;
     int64_t left = left0;
     for (int32_t s = s0; s < s1; ++s) {
         own.mass += stays(s, left);
@@ -771,37 +899,36 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     Chunk<T> chunk = row.bits(c);
     chunk.clean();
     if (infinite) chunk.only_infinite();
-    // thrice over the eight: their equals of the border, their mass, and the one that the draw falls on
-    uint64_t equals = 0, mass = 0, from = 0;
-    int64_t room0 = 0, room = 0;
-#pragma unroll 1
-    for (int i = 0; i < 24; ++i) {
-        if (i == 8) room0 = room = sh.found_count - (int64_t)(wave_scan64(equals) - equals);
-        if (i == 16) {
-            from = sh.found_mass + wave_scan64(mass) - mass;
-            room = room0;
-        }
-        const float v = chunk.value(0);
-        const uint32_t bits = chunk.w[0];
-        const bool equal = v == border.value;
-        if (i < 8) {
-            equals += equal ? 1 : 0;
-        } else {
-            const uint64_t w = v > border.value || (equal && room > 0) ? whole(weight(v)) : 0;
-            if (equal) --room;
-            if (i < 16) {
-                mass += w;
-            } else {
-                if (from <= at && at < from + w) {
-                    a.token[r] = 8 * c + (i - 16) - row.before;
-                    if (a.logprob)
-                        a.logprob[r] = (float)(((double)v - (double)top) / (double)temperature -
-                                               log((double)total / (double)(1ull << kUnitBits)));
-                }
-                from += w;
+    float v[8];
+    int32_t equals = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = chunk.value(e % 4);
+        if (e == 3) chunk.swap();
+        equals += v[e] == border.value ? 1 : 0;
+    }
+    int64_t room = sh.found_count - (int64_t)(wave_scan64(equals) - equals);
+    uint64_t w[8], mass = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool equal = v[e] == border.value;
+        w[e] = whole(weight(v[e] > border.value || (equal && room > 0) ? v[e] : -INFINITY));
+        room -= equal ? 1 : 0;
+        mass += w[e];
+    }
+    uint64_t from = sh.found_mass + wave_scan64(mass) - mass;
+    if (from <= at && at < from + mass) {
+        float value = 0.f;
+        int32_t token = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (from <= at && at < from + w[e]) {
+                token = 8 * c + e - row.before;
+                value = v[e];
             }
+            from += w[e];
         }
-        chunk.put(bits & (Chunk<T>::kHalf ? 0xffffu : 0xffffffffu));
+        finish(token, value, total);
     }
 }
 
