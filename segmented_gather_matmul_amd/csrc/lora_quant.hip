@@ -401,7 +401,7 @@ lora_quant_attention_kernel(QuantArgs a)
             if (from < to) return Part{p.row, p.begin, p.end, p.w0, last - p.w0 + 1, p.table};
             // else the row's tiles lie in the next workgroup's share
         }
-        return Part{-1, 0, 0, 0, 0, nullptr};
+        return Part{-1, 0, 0, 0, 0, a.table};
     };
     // This lane's columns: unit c (of KC) is the eight columns from col_of(c) on.
     auto col_of = [&](int c) { return DP < 128 ? 16 * lg + 8 * c : 128 * (c / 4) + 32 * lg + 8 * (c % 4); };
@@ -414,23 +414,24 @@ lora_quant_attention_kernel(QuantArgs a)
         code_at[j] = exp_at[j] * (4 * BITS) + (DP < 128 ? (lg & 1) * (2 * BITS) : 0);
     }
     // Tokens t0 + 16 u + li of a tile: table entries, then cell offsets; a token past the end or
-    // without a page reads cell 0 and is masked.
+    // without a page reads page 0 and is masked.
     struct Tile {
         uint32_t code[kQSub][NB][W], exp[kQSub][NB];
     };
     auto ids_of = [&](const Part &p, int32_t t0, int32_t (&id)[kQSub]) {
 #pragma unroll
-        for (int u = 0; u < kQSub; ++u) id[u] = t0 < p.end ? p.table[min(t0 + 16 * u + li, p.end - 1) >> a.shift] : -1;
+        for (int u = 0; u < kQSub; ++u) id[u] = p.table[max(min(t0 + 16 * u + li, p.end - 1), 0) >> a.shift];
     };
+    const int64_t head_code = kvh * a.c.head_stride, head_exp = kvh * a.c.exp_head_stride;
     auto cells_of = [&](const Part &p, int32_t t0, const int32_t (&id)[kQSub], Cell (&cell)[kQSub]) {
         uint64_t seen = 0;
 #pragma unroll
         for (int u = 0; u < kQSub; ++u) {
             const int32_t t = t0 + 16 * u + li;
-            const bool ok = t < p.end && id[u] >= 0 && id[u] < a.c.num_pages;
-            const int64_t page = ok ? id[u] : 0, off = ok ? t & in_page : 0;
-            cell[u] = Cell{page * a.c.page_stride + off * a.c.token_stride + kvh * a.c.head_stride,
-                           page * a.c.exp_page_stride + off * a.c.exp_token_stride + kvh * a.c.exp_head_stride};
+            const bool ok = t < p.end && (uint32_t)id[u] < (uint32_t)a.c.num_pages;
+            const uint32_t page = ok ? id[u] : 0, off = t & in_page;
+            cell[u] = Cell{(int64_t)((uint64_t)page * (uint64_t)a.c.page_stride + off * (uint32_t)a.c.token_stride) + head_code,
+                           (int64_t)((uint64_t)page * (uint64_t)a.c.exp_page_stride + off * (uint32_t)a.c.exp_token_stride) + head_exp};
             seen |= (__ballot(ok) & 0xffffu) << (16 * u);
         }
         return seen;
@@ -520,6 +521,7 @@ lora_quant_attention_kernel(QuantArgs a)
                     s[u] = mfma(__builtin_bit_cast(vec8<T>, unit_of(kr, u, c)), __builtin_bit_cast(vec8<T>, q[c]), s[u]);
             }
             const uint64_t seen_now = seen;
+            const bool whole = seen_now == ~(uint64_t)0;
             if (more) {
                 seen = cells_of(part, t0 + kStep, id, cell);
                 ids_of(part, t0 + 2 * kStep, id);
@@ -536,13 +538,32 @@ lora_quant_attention_kernel(QuantArgs a)
                 f4_t v = s[p * R];
 #pragma unroll
                 for (int r = 1; r < R; ++r) v = copy == r ? s[p * R + r] : v;
-                const uint32_t ok = (uint32_t)(seen_now >> (16 * (p * R + copy) + 4 * lg));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[p][e] = ok >> e & 1 ? v[e] * scale : -INFINITY;
-                    mx = __builtin_fmaxf(mx, x[p][e]);
+                for (int e = 0; e < 4; ++e) x[p][e] = v[e] * scale;
+            }
+            if (!whole) {
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    const uint32_t ok = (uint32_t)(seen_now >> (16 * (p * R + copy) + 4 * lg));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[p][e] = ok >> e & 1 ? x[p][e] : -INFINITY;
+                }
+                // what is masked of V is 0
+#pragma unroll
+                for (int u = 0; u < kQSub; ++u) {
+                    const bool mine = (seen_now >> (16 * u + li) & 1) != 0;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        vr.exp[u][j] = mine ? vr.exp[u][j] : 127;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) vr.code[u][j][w] = mine ? vr.code[u][j][w] : 0;
+                    }
                 }
             }
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, x[p][e]);
             mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
             mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
             if (__any(mx != m)) {
@@ -566,16 +587,12 @@ lora_quant_attention_kernel(QuantArgs a)
             }
 #pragma unroll
             for (int half = 0; half < kQSub / 2; ++half) {
-                // V rows of two subtiles to LDS; what is masked is 0 there
+                // V rows of two subtiles to LDS
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const bool mine = (seen_now >> (16 * (2 * half + u) + li) & 1) != 0;
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int c = 0; c < KC; ++c) {
-                        const uint4 r = unit_of(vr, 2 * half + u, c);
-                        *reinterpret_cast<uint4 *>(&tile[(16 * u + li) * kPitch + col_of(c)]) = mine ? r : make_uint4(0, 0, 0, 0);
-                    }
-                }
+                    for (int c = 0; c < KC; ++c)
+                        *reinterpret_cast<uint4 *>(&tile[(16 * u + li) * kPitch + col_of(c)]) = unit_of(vr, 2 * half + u, c);
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
                 if (half == kQSub / 2 - 1) load_tile(a.c.v, a.c.v_exp, cell, vr);
@@ -704,6 +721,9 @@ int check_quant_cache(const lora_quant_cache *c)
         if (s < bytes) return fail(LORA_E_SHAPE, "cache stride %lld < %lld bytes", (long long)s, (long long)bytes);
         if (s % 16) return fail(LORA_E_ALIGN, "cache stride %lld is not a multiple of 16 bytes", (long long)s);
     }
+    if ((c->page_size - 1) * (__int128)c->token_stride + bytes > INT32_MAX ||
+        (c->page_size - 1) * (__int128)c->exp_token_stride + blocks > INT32_MAX)
+        return fail(LORA_E_SHAPE, "a page's tokens span more than 2^31 bytes");
     for (int64_t s : {c->exp_page_stride, c->exp_token_stride, c->exp_head_stride})
         if (s < blocks) return fail(LORA_E_SHAPE, "cache exponent stride %lld < %lld blocks", (long long)s, (long long)blocks);
     auto reach = [&](int64_t page, int64_t token, int64_t head, int64_t cell) {
