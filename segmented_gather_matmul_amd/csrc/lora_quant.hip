@@ -302,8 +302,11 @@ struct QuantArgs : AttnArgs {
     lora_quant_cache c;
 };
 
-constexpr int kQWaves = 4, kQTile = 64, kQMinShare = 4, kQRowTiles = 4;
-typedef AttnLine<kQWaves, kQTile, kQMinShare, kQRowTiles> QuantLine;
+constexpr int kQWaves = 4, kQTile = 64;
+// The two ways to split the rows' tiles (quant_solo): a workgroup's wavefronts take those of a part in turn and join
+// at its end, or each wavefront has parts of its own and waits for no other.
+typedef AttnLine<kQWaves, kQTile, 8, 8, 16, false, 8, 32> GangLine;
+typedef AttnLine<kQWaves, kQTile, 4, 2, 16, true, 8, 32> SoloLine;
 constexpr int kQSub = kQTile / 16;  // 16-token subtiles of a tile
 // Wavefronts per SIMD, and so workgroups per CU, that the registers are kept to.
 constexpr int quant_occupancy(int dp) { return dp <= 128 ? 2 : 1; }
@@ -328,6 +331,17 @@ __device__ inline void split_weight<BF16>(float p0, float p1, uint32_t &hi, uint
     lo = (__builtin_bit_cast(uint32_t, r0) >> 16) | (__builtin_bit_cast(uint32_t, r1) & 0xffff0000u);
 }
 
+// Largest over the four lanes that hold a column.  (The exchanges are written out, with the two wait states that they
+// need behind a vector write: given one value twice, the compiler takes both results for the same.)
+__device__ inline float column_max(float x)
+{
+    float y = x;
+    asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    x = y = __builtin_fmaxf(x, y);
+    asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    return __builtin_fmaxf(x, y);
+}
+
 // One workgroup per (share of the rows, key/value head, 16 of its query heads), as in the 16-bit
 // attention, whose split of the rows and join of their parts it takes.
 //
@@ -343,7 +357,7 @@ __device__ inline void split_weight<BF16>(float p0, float p1, uint32_t &hi, uint
 // keeps the scores of its own column's subtile and lays the others aside, so the softmax
 // of R subtiles costs what one does, and each copy has its own maximum and sums, which are joined
 // at the row's end.
-template <typename T, int BITS, int DP, int R>
+template <typename T, int BITS, int DP, int R, typename LINE, bool PAGES>
 __global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(quant_occupancy(DP)))) void
 lora_quant_attention_kernel(QuantArgs a)
 {
@@ -371,37 +385,41 @@ lora_quant_attention_kernel(QuantArgs a)
         ht = blockIdx.x / 8 - eight * a.head_tiles;
         pair = 8 * eight + blockIdx.x % 8;
     }
+    if (LINE::kSolo) pair = pair * kQWaves + wave;
     const int32_t wg = pair / a.kv_heads, kvh = pair - wg * a.kv_heads, rest = kvh * a.head_tiles + ht;
     if (wg >= a.shares) return;
     const int heads = min(G, a.group - 16 * ht);  // query heads of this tile
     const int64_t head0 = (int64_t)kvh * a.group + 16 * ht;
     const int32_t in_page = (1 << a.shift) - 1;
     int32_t share, total;
-    RowWalk<QuantLine> walk;
+    RowWalk<LINE> walk;
     RowWork rw = first_row(a, wg, walk, share, total);
     if (rw.row >= a.n_rows) return;
     const int32_t line0 = wg * share, line1 = (int32_t)min((int64_t)line0 + share, (int64_t)total);
 
-    // A row's part in this share: tokens [begin, end); the row has `parts` parts from workgroup w0 on.
+    // A row's part in this share: tokens [begin, end), of which those before `first` lie before the window; the row has
+    // `parts` parts from share w0 on.
     struct Part {
-        int32_t row, begin, end, w0, parts;
+        int32_t row, begin, end, first, w0, parts;
         const int32_t *table;
     };
     auto next_part = [&]() {
         while (rw.row < a.n_rows) {
             const int32_t row_end = rw.tile0 + rw.tiles;
             const int32_t from = max(rw.tile0, line0), to = min(row_end, line1), tile0 = rw.tile0;
+            const int32_t n = rw.rs.first + rw.rs.span;
             const Part p{rw.row, rw.rs.first + (from - tile0) * kQTile,
                          rw.rs.first + (int32_t)min((int64_t)(to - tile0) * kQTile, (int64_t)rw.rs.span),
-                         tile0 < line0 ? tile0 / share : wg, 1, a.table + (int64_t)rw.rs.req * a.ld_table};
+                         a.window > 0 ? max(n - a.window, 0) : 0, tile0 < line0 ? tile0 / share : wg, 1,
+                         a.table + (int64_t)rw.rs.req * a.ld_table};
             int32_t last = wg;
             if (row_end > line1) last = (row_end - 1) / share;
-            if (row_end < line1) rw = walk.after(a, rw.row, row_end + kQRowTiles);
+            if (row_end < line1) rw = walk.after(a, rw.row, row_end + LINE::kRowTiles);
             else rw.row = a.n_rows;
-            if (from < to) return Part{p.row, p.begin, p.end, p.w0, last - p.w0 + 1, p.table};
+            if (from < to) return Part{p.row, p.begin, p.end, p.first, p.w0, last - p.w0 + 1, p.table};
             // else the row's tiles lie in the next workgroup's share
         }
-        return Part{-1, 0, 0, 0, 0, a.table};
+        return Part{-1, 0, 0, 0, 0, 0, a.table};
     };
     // This lane's columns: unit c (of KC) is the eight columns from col_of(c) on.
     auto col_of = [&](int c) { return DP < 128 ? 16 * lg + 8 * c : 128 * (c / 4) + 32 * lg + 8 * (c % 4); };
@@ -413,35 +431,53 @@ lora_quant_attention_kernel(QuantArgs a)
         exp_at[j] = min(DP < 128 ? lg / 2 : 4 * j + lg, blocks - 1);
         code_at[j] = exp_at[j] * (4 * BITS) + (DP < 128 ? (lg & 1) * (2 * BITS) : 0);
     }
-    // Tokens t0 + 16 u + li of a tile: table entries, then cell offsets; a token past the end or
-    // without a page reads page 0 and is masked.
+    // Tokens t0 + 16 u + li of a tile: table entries, then where their cells begin; a token past the end or
+    // without a page reads page 0 and is masked.  Where pages hold whole subtiles (PAGES), a subtile's page and place in
+    // it are scalars.
     struct Tile {
         uint32_t code[kQSub][NB][W], exp[kQSub][NB];
     };
-    auto ids_of = [&](const Part &p, int32_t t0, int32_t (&id)[kQSub]) {
-#pragma unroll
-        for (int u = 0; u < kQSub; ++u) id[u] = p.table[max(min(t0 + 16 * u + li, p.end - 1), 0) >> a.shift];
-    };
+    constexpr int kIds = PAGES ? 1 : kQSub;
     const int64_t head_code = kvh * a.c.head_stride, head_exp = kvh * a.c.exp_head_stride;
-    auto cells_of = [&](const Part &p, int32_t t0, const int32_t (&id)[kQSub], Cell (&cell)[kQSub]) {
+    const uint32_t lane_code = li * (uint32_t)a.c.token_stride, lane_exp = li * (uint32_t)a.c.exp_token_stride;
+    auto ids_of = [&](const Part &p, int32_t t0, int32_t (&id)[kIds]) {
+#pragma unroll
+        for (int u = 0; u < kIds; ++u)
+            id[u] = p.table[max(min(t0 + (PAGES ? 16 * (lane % kQSub) : 16 * u + li), p.end - 1), 0) >> a.shift];
+    };
+    auto cells_of = [&](const Part &p, int32_t t0, const int32_t (&id)[kIds], Cell (&cell)[kQSub]) {
         uint64_t seen = 0;
 #pragma unroll
         for (int u = 0; u < kQSub; ++u) {
-            const int32_t t = t0 + 16 * u + li;
-            const bool ok = t < p.end && (uint32_t)id[u] < (uint32_t)a.c.num_pages;
-            const uint32_t page = ok ? id[u] : 0, off = t & in_page;
-            cell[u] = Cell{(int64_t)((uint64_t)page * (uint64_t)a.c.page_stride + off * (uint32_t)a.c.token_stride) + head_code,
-                           (int64_t)((uint64_t)page * (uint64_t)a.c.exp_page_stride + off * (uint32_t)a.c.exp_token_stride) + head_exp};
-            seen |= (__ballot(ok) & 0xffffu) << (16 * u);
+            if constexpr (PAGES) {
+                const int32_t page = __builtin_amdgcn_readlane(id[0], u), s0 = t0 + 16 * u;
+                const bool ok = (uint32_t)page < (uint32_t)a.c.num_pages;
+                const uint32_t off = s0 & in_page;
+                const uint64_t at = ok ? page : 0;
+                cell[u] = Cell{(int64_t)(at * (uint64_t)a.c.page_stride + off * (uint32_t)a.c.token_stride) + head_code,
+                               (int64_t)(at * (uint64_t)a.c.exp_page_stride + off * (uint32_t)a.c.exp_token_stride) + head_exp};
+                const int before = min(max(p.first - s0, 0), 16), behind = min(max(p.end - s0, 0), 16);
+                const uint64_t in = ok ? (1u << behind) - 1 & ~((1u << before) - 1) : 0;
+                seen |= in << (16 * u);
+            } else {
+                const int32_t t = t0 + 16 * u + li;
+                const bool ok = t < p.end && t >= p.first && (uint32_t)id[u] < (uint32_t)a.c.num_pages;
+                const uint32_t page = ok ? id[u] : 0, off = t & in_page;
+                cell[u] = Cell{(int64_t)((uint64_t)page * (uint64_t)a.c.page_stride + off * (uint32_t)a.c.token_stride) + head_code,
+                               (int64_t)((uint64_t)page * (uint64_t)a.c.exp_page_stride + off * (uint32_t)a.c.exp_token_stride) + head_exp};
+                seen |= (__ballot(ok) & 0xffffu) << (16 * u);
+            }
         }
         return seen;
     };
     auto load_tile = [&](const void *codes, const uint8_t *exps, const Cell (&cell)[kQSub], Tile &r) {
 #pragma unroll
-        for (int u = 0; u < kQSub; ++u)
+        for (int u = 0; u < kQSub; ++u) {
+            const uint8_t *const code_base = static_cast<const uint8_t *>(codes) + cell[u].code;
+            const uint8_t *const exp_base = exps + cell[u].exp;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const uint8_t *const p = static_cast<const uint8_t *>(codes) + cell[u].code + code_at[j];
+                const uint8_t *const p = code_base + ((PAGES ? lane_code : 0u) + (uint32_t)code_at[j]);
                 if constexpr (W == 2) {
                     const uint2 v = *reinterpret_cast<const uint2 *>(p);
                     r.code[u][j][0] = v.x;
@@ -456,7 +492,21 @@ lora_quant_attention_kernel(QuantArgs a)
                         r.code[u][j][w + 3] = v.w;
                     }
                 }
-                r.exp[u][j] = exps[cell[u].exp + exp_at[j]];
+                r.exp[u][j] = exp_base[(PAGES ? lane_exp : 0u) + (uint32_t)exp_at[j]];
+            }
+        }
+    };
+    // Two subtiles of it.
+    auto load_half = [&](const void *codes, const uint8_t *exps, const Cell (&cell)[kQSub], Tile &r, int half) {
+        Tile all;  // (what of it is not used is not loaded)
+        load_tile(codes, exps, cell, all);
+#pragma unroll
+        for (int u = 2 * half; u < 2 * half + 2; ++u)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) r.code[u][j][w] = all.code[u][j][w];
+                r.exp[u][j] = all.exp[u][j];
             }
     };
     // Unit c of subtile u as 16-bit values.
@@ -477,7 +527,8 @@ lora_quant_attention_kernel(QuantArgs a)
         }
     };
 
-    constexpr int kStep = kQWaves * kQTile;
+    constexpr int kStep = LINE::kWaves * kQTile;
+    const int turn = LINE::kSolo ? 0 : wave;  // which of a part's tiles it begins with
     const float scale = a.scale * kLog2e;
     uint16_t *const tile = vt[wave];
     const int tr_row = 4 * lg + (li >> 2), tr_col = 4 * (li & 3);
@@ -487,11 +538,11 @@ lora_quant_attention_kernel(QuantArgs a)
     // first of the next part, and the page ids of the tile after it (id).
     Part part = next_part();
     if (part.row < 0) return;
-    int32_t id[kQSub];
+    int32_t id[kIds];
     Cell cell[kQSub];
     Tile kr, vr;
     uint4 q[KC];
-    int32_t t0 = part.begin + wave * kQTile;
+    int32_t t0 = part.begin + turn * kQTile;
     ids_of(part, t0, id);
     load_q(part.row, q);
     uint64_t seen = cells_of(part, t0, id, cell);
@@ -501,8 +552,8 @@ lora_quant_attention_kernel(QuantArgs a)
 
     for (;;) {
         const Part next = next_part();
-        const int32_t next_t0 = next.begin + wave * kQTile;
-        int32_t next_id[kQSub];
+        const int32_t next_t0 = next.begin + turn * kQTile;
+        int32_t next_id[kIds];
         ids_of(next, next_t0, next_id);
         float m = -INFINITY, l = 0.f;
         f4_t o[DB];
@@ -564,8 +615,7 @@ lora_quant_attention_kernel(QuantArgs a)
             for (int p = 0; p < PASSES; ++p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, x[p][e]);
-            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
-            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+            mx = column_max(mx);
             if (__any(mx != m)) {
                 const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
                 l *= f;
@@ -593,9 +643,9 @@ lora_quant_attention_kernel(QuantArgs a)
 #pragma unroll
                     for (int c = 0; c < KC; ++c)
                         *reinterpret_cast<uint4 *>(&tile[(16 * u + li) * kPitch + col_of(c)]) = unit_of(vr, 2 * half + u, c);
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
-                if (half == kQSub / 2 - 1) load_tile(a.c.v, a.c.v_exp, cell, vr);
+                load_half(a.c.v, a.c.v_exp, cell, vr, half);
                 // the weights of the two subtiles, each in its own columns
                 uint4 wh, wl;
                 if constexpr (R == 1) {
@@ -616,46 +666,47 @@ lora_quant_attention_kernel(QuantArgs a)
                     o[b] = mfma(vv, ph, o[b]);
                     o[b] = mfma(vv, pl, o[b]);
                 }
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
             }
             if (!more) break;
             t0 += kStep;
         }
         // Join the wavefronts and the copies: every one's sums in LDS, scaled to the common maximum.
+        const int w0 = LINE::kSolo ? wave : 0;
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (lg == 0) {
             jm[wave][li] = m;
             jl[wave][li] = l;
         }
-        __syncthreads();
+        line_sync<LINE>();
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kQWaves; ++w)
+        for (int w = 0; w < LINE::kWaves; ++w)
 #pragma unroll
-            for (int r = 0; r < R; ++r) mx = __builtin_fmaxf(mx, jm[w][r * G + hcol]);
+            for (int r = 0; r < R; ++r) mx = __builtin_fmaxf(mx, jm[w0 + w][r * G + hcol]);
         const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.f : mx));
         float *const mine_o = reinterpret_cast<float *>(vt[wave]);
         if (hcol < heads)
 #pragma unroll
             for (int b = 0; b < DB; ++b) *reinterpret_cast<f4_t *>(&mine_o[li * DP + 16 * b + 4 * lg]) = o[b] * f;
-        __syncthreads();
-        for (int i = tid; i < heads * (DP / 4); i += 64 * kQWaves) {
+        line_sync<LINE>();
+        for (int i = LINE::kSolo ? lane : tid; i < heads * (DP / 4); i += 64 * LINE::kWaves) {
             const int h = i / (DP / 4), d = 4 * (i - h * (DP / 4));
             if (d >= a.head_dim) continue;
             float hm = -INFINITY, hl = 0.f;
 #pragma unroll
-            for (int w = 0; w < kQWaves; ++w)
+            for (int w = 0; w < LINE::kWaves; ++w)
 #pragma unroll
-                for (int r = 0; r < R; ++r) hm = __builtin_fmaxf(hm, jm[w][r * G + h]);
+                for (int r = 0; r < R; ++r) hm = __builtin_fmaxf(hm, jm[w0 + w][r * G + h]);
             f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kQWaves; ++w)
+            for (int w = 0; w < LINE::kWaves; ++w)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    hl = __builtin_fmaf(jl[w][r * G + h], __builtin_amdgcn_exp2f(jm[w][r * G + h] - (hm == -INFINITY ? 0.f : hm)), hl);
-                    sum += *reinterpret_cast<const f4_t *>(&reinterpret_cast<const float *>(vt[w])[(r * G + h) * DP + d]);
+                    hl = __builtin_fmaf(jl[w0 + w][r * G + h], __builtin_amdgcn_exp2f(jm[w0 + w][r * G + h] - (hm == -INFINITY ? 0.f : hm)), hl);
+                    sum += *reinterpret_cast<const f4_t *>(&reinterpret_cast<const float *>(vt[w0 + w])[(r * G + h) * DP + d]);
                 }
             const int64_t head = head0 + h;
             if (part.parts > 1) {
@@ -668,34 +719,57 @@ lora_quant_attention_kernel(QuantArgs a)
             }
         }
         if (part.parts > 1)
-            join_row<T, QuantLine>(a, part.row, part.w0, part.parts, wg - part.w0, per_share, rest, head0, heads);
+            join_row<T, LINE>(a, part.row, part.w0, part.parts, wg - part.w0, per_share, rest, head0, heads);
         if (next.row < 0) break;
-        __syncthreads();  // the join is done with the LDS tiles
+        line_sync<LINE>();  // the join is done with the LDS tiles
         part = next;
         t0 = next_t0;
     }
 }
 
-// Workgroups per head tile: what the CUs hold at once.
-int32_t quant_shares(int32_t tiles, int32_t head_dim)
+// Shares per head tile: what the CUs hold at once.
+int32_t quant_shares(int32_t tiles, int32_t head_dim, bool solo)
 {
-    return std::max(1, kAttnCUs * quant_occupancy(head_dim) / tiles);
+    return std::max(1, kAttnCUs * quant_occupancy(head_dim) * (solo ? kQWaves : 1) / tiles);
 }
 
-template <typename T, int BITS, int DP>
-void quant_attention_launch(const QuantArgs &a, dim3 grid, hipStream_t s)
+// Whether wavefronts take parts of their own: where each has half a row and key/value head or more, so that few rows are
+// split.  Measured (4 bits, 128 columns, gang / solo): 32 rows of 64-4096 tokens, 32/32 heads 44.8 / 37.0 us, 256 rows of
+// 100-900 144 / 107; 61 rows of 1-16,381 tokens, 64/8 heads 41 / 49, one row of 131,071, 8/1 heads 24 / 43.
+bool quant_solo(int32_t n_rows, int32_t tiles, int32_t head_dim)
 {
-    if (a.group <= 4) launch(lora_quant_attention_kernel<T, BITS, DP, 4>, grid, 64 * kQWaves, 0, s, a);
-    else if (a.group <= 8) launch(lora_quant_attention_kernel<T, BITS, DP, 2>, grid, 64 * kQWaves, 0, s, a);
-    else launch(lora_quant_attention_kernel<T, BITS, DP, 1>, grid, 64 * kQWaves, 0, s, a);
+    return 2 * (int64_t)n_rows * tiles >= kAttnCUs * kQWaves * quant_occupancy(head_dim);
 }
 
-template <typename T, int BITS>
+template <typename T, int BITS, int DP, int R, typename LINE>
 void quant_attention_launch(const QuantArgs &a, dim3 grid, hipStream_t s)
 {
-    if (a.head_dim <= 64) quant_attention_launch<T, BITS, 64>(a, grid, s);
-    else if (a.head_dim <= 128) quant_attention_launch<T, BITS, 128>(a, grid, s);
-    else quant_attention_launch<T, BITS, 256>(a, grid, s);
+    if (a.c.page_size >= 16) launch(lora_quant_attention_kernel<T, BITS, DP, R, LINE, true>, grid, 64 * kQWaves, 0, s, a);
+    else launch(lora_quant_attention_kernel<T, BITS, DP, R, LINE, false>, grid, 64 * kQWaves, 0, s, a);
+}
+
+template <typename T, int BITS, int DP, typename LINE>
+void quant_attention_launch(const QuantArgs &a, dim3 grid, hipStream_t s)
+{
+    if (a.group <= 4) quant_attention_launch<T, BITS, DP, 4, LINE>(a, grid, s);
+    else if (a.group <= 8) quant_attention_launch<T, BITS, DP, 2, LINE>(a, grid, s);
+    else quant_attention_launch<T, BITS, DP, 1, LINE>(a, grid, s);
+}
+
+template <typename T, int BITS, typename LINE>
+void quant_attention_launch(const QuantArgs &a, dim3 grid, hipStream_t s)
+{
+    if (a.head_dim <= 64) quant_attention_launch<T, BITS, 64, LINE>(a, grid, s);
+    else if (a.head_dim <= 128) quant_attention_launch<T, BITS, 128, LINE>(a, grid, s);
+    else quant_attention_launch<T, BITS, 256, LINE>(a, grid, s);
+}
+
+template <typename LINE>
+void quant_attention_launch(const QuantArgs &a, dim3 grid, hipStream_t s)
+{
+    const bool bf = a.c.type == LORA_TYPE_BF16;
+    if (a.c.bits == 4) bf ? quant_attention_launch<BF16, 4, LINE>(a, grid, s) : quant_attention_launch<F16, 4, LINE>(a, grid, s);
+    else bf ? quant_attention_launch<BF16, 8, LINE>(a, grid, s) : quant_attention_launch<F16, 8, LINE>(a, grid, s);
 }
 
 // ------------------------------------------------------------------------ host checks
@@ -837,7 +911,7 @@ size_t lora_quant_attention_bytes(int32_t n_rows, int32_t q_heads, int32_t kv_he
         return 0;
     const int32_t tiles = attn_tiles(q_heads, kv_heads);
     if (tiles > kAttnMaxTiles) return 0;
-    const size_t slots = 2 * (size_t)quant_shares(tiles, head_dim) * q_heads;
+    const size_t slots = 2 * (size_t)quant_shares(tiles, head_dim, quant_solo(n_rows, tiles, head_dim)) * q_heads;
     return (kAttnCounters * sizeof(uint32_t) + slots * (head_dim + 2) * sizeof(float) + 255) & ~size_t(255);
 }
 
@@ -855,17 +929,19 @@ int lora_quant_attention(void *stream, int32_t n_rows, int32_t q_heads, void *ou
         return st;
     if (n_rows == 0) return LORA_OK;
     QuantArgs a{};
-    const int32_t tiles = attn_tiles(q_heads, cache->kv_heads), most = quant_shares(tiles, cache->head_dim);
-    if ((st = fill_attention<QuantLine>(a, n_rows, q_heads, out, ldo, q, ldq, n_req, block_table, ld_table, max_blocks,
-                                        kv_len, req, scale, window, lse, work, cache->kv_heads, cache->head_dim,
-                                        cache->page_size, most)))
+    const int32_t tiles = attn_tiles(q_heads, cache->kv_heads);
+    const bool solo = quant_solo(n_rows, tiles, cache->head_dim);
+    const int32_t most = quant_shares(tiles, cache->head_dim, solo);
+    // rows of two tiles at most are a wavefront's, too (one row of 17 tokens: 8.6 us in a gang, 7.8 alone)
+    const bool alone = solo || std::min<int64_t>((int64_t)max_blocks * cache->page_size, window > 0 ? window : INT32_MAX) <= 2 * kQTile;
+    auto fill = alone ? fill_attention<SoloLine> : fill_attention<GangLine>;
+    if ((st = fill(a, n_rows, q_heads, out, ldo, q, ldq, n_req, block_table, ld_table, max_blocks, kv_len, req, scale, window,
+                   lse, work, cache->kv_heads, cache->head_dim, cache->page_size, most)))
         return st;
     a.c = *cache;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid = attention_grid(a);
-    const bool bf = cache->type == LORA_TYPE_BF16;
-    if (cache->bits == 4) bf ? quant_attention_launch<BF16, 4>(a, grid, s) : quant_attention_launch<F16, 4>(a, grid, s);
-    else bf ? quant_attention_launch<BF16, 8>(a, grid, s) : quant_attention_launch<F16, 8>(a, grid, s);
+    if (alone) quant_attention_launch<SoloLine>(a, attention_grid(a, kQWaves), s);
+    else quant_attention_launch<GangLine>(a, attention_grid(a), s);
     return launch_status("quantised attention");
 }
 

@@ -442,7 +442,7 @@ struct PagedArgs : AttnArgs {
 };
 
 constexpr int kAttnWaves = 4, kAttnTile = 32, kAttnMinShare = 4, kAttnRowTiles = 4;
-typedef AttnLine<kAttnWaves, kAttnTile, kAttnMinShare, kAttnRowTiles> PagedLine;
+typedef AttnLine<kAttnWaves, kAttnTile, kAttnMinShare, kAttnRowTiles, 1, false, 8, kAttnJoin> PagedLine;
 // Wavefronts per SIMD, and so workgroups per CU, that the registers are kept to.
 constexpr int attn_occupancy(int dp) { return dp <= 64 ? 2 : 1; }
 

@@ -107,9 +107,13 @@ struct AttnArgs {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 // How a kernel splits its rows.
-template <int WAVES, int TILE, int MIN_SHARE, int ROW_TILES>
+template <int WAVES, int TILE, int MIN_SHARE, int ROW_TILES, int ALIGN, bool SOLO, int BATCH, int ONCE>
 struct AttnLine {
-    static constexpr int kWaves = WAVES;         // wavefronts of a workgroup
+    static constexpr int kBatch = BATCH;         // parts that a join loads at a time
+    static constexpr int kOnce = ONCE;           // parts that are joined in one step; more in groups of kAttnJoin first
+    static constexpr int kAlign = ALIGN;         // a row's first tile begins at a multiple of this (a power of two)
+    static constexpr bool kSolo = SOLO;          // a wavefront has a share of its own, and not its workgroup
+    static constexpr int kWaves = SOLO ? 1 : WAVES;  // wavefronts that work on one
     static constexpr int kTile = TILE;           // tokens a wavefront takes at a time
     static constexpr int kMinShare = MIN_SHARE;  // tiles a workgroup takes at least: one per wavefront
     static constexpr int kRowTiles = ROW_TILES;  // what starting and finishing a row costs, in tiles
@@ -123,17 +127,18 @@ constexpr int32_t kAttnMaxSpan = 1 << 30;  // tokens of a table row: positions a
 // different shapes sharing a workspace never put sums where another finds its counters.
 constexpr size_t kAttnCounters = 2 * (4 * kAttnCUs + kAttnMaxTiles);
 
-// Visible tokens [first, first + span) of row i; span -1: the row is not active, or none.
+// Visible tokens [first, first + span) of row i (from a multiple of kAlign on); span -1: the row is not active, or none.
 struct RowSpan {
     int32_t req, first, span;
 };
 
+template <typename LINE>
 __device__ inline RowSpan row_span(const AttnArgs &a, int32_t i)
 {
     const int32_t at = min(i, a.n_rows - 1);  // loads without a branch, so many can be in flight
     const int32_t n = a.kv_len[at], r = a.req ? a.req[at] : at;
     const bool on = i < a.n_rows && n >= 0 && n <= a.max_blocks << a.shift && r >= 0 && r < a.n_req;
-    const int32_t first = a.window > 0 && n > a.window ? n - a.window : 0;
+    const int32_t first = a.window > 0 && n > a.window ? (n - a.window) & -LINE::kAlign : 0;
     return RowSpan{r, first, on ? n - first : -1};
 }
 
@@ -175,7 +180,7 @@ struct RowWalk {
     __device__ inline void load(const AttnArgs &a, int32_t b)
     {
         base = b;
-        rs = row_span(a, b + (int32_t)(threadIdx.x & 63));
+        rs = row_span<LINE>(a, b + (int32_t)(threadIdx.x & 63));
         tiles = row_tiles<LINE>(rs);
     }
     __device__ inline RowWork row(int lane, int32_t tile0) const
@@ -207,7 +212,7 @@ __device__ inline RowWork first_row(const AttnArgs &a, int32_t w, RowWalk<LINE> 
     int32_t sum = walk.tiles > 0 ? walk.tiles + LINE::kRowTiles : 0;
 #pragma unroll 8
     for (int32_t c = 64; c < a.n_rows; c += 64) {
-        const int32_t t = row_tiles<LINE>(row_span(a, c + lane));
+        const int32_t t = row_tiles<LINE>(row_span<LINE>(a, c + lane));
         sum += t > 0 ? t + LINE::kRowTiles : 0;
     }
     total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
@@ -310,20 +315,44 @@ __device__ inline float2 get_part(const float *p)
     return make_float2(__builtin_bit_cast(float, (uint32_t)v), __builtin_bit_cast(float, (uint32_t)(v >> 32)));
 }
 
-// True in the workgroup that is the n-th to come here with this counter, which is then 0
+// Waits for those that work on one share.
+template <typename LINE>
+__device__ inline void line_sync()
+{
+    if constexpr (LINE::kSolo) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        __syncthreads();
+    }
+}
+
+// True in the workgroup (or, alone, wavefront) that is the n-th to come here with this counter, which is then 0
 // again.  Every wavefront waits for its own stores to complete before the workgroup
 // counts itself, so the last one's loads find all parts.
+template <typename LINE>
 __device__ inline bool last_arrival(uint32_t *count, int n)
 {
-    __shared__ bool last;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
-        if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if constexpr (LINE::kSolo) {
+        uint32_t before = 0;
+        if ((threadIdx.x & 63) == 0) {
+            before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (before == (uint32_t)(n - 1)) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        const bool last = __builtin_amdgcn_readfirstlane(before) == (uint32_t)(n - 1);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        return last;
+    } else {
+        __shared__ bool last;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
+            if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        return last;
     }
-    __syncthreads();
-    return last;
 }
 
 // Slot of part p of a row whose first part is in workgroup w0: a workgroup has one slot for
@@ -336,14 +365,15 @@ template <typename T, typename LINE>
 __device__ inline void join_parts(const AttnArgs &a, int32_t row, int32_t w0, int64_t head0, int heads, int part0,
                                   int step, int n, bool finish)
 {
-    __shared__ float2 joined[16];
-    constexpr int kBatch = 8;
-    const int cols = a.head_dim / 4, tid = threadIdx.x;
+    __shared__ float2 joined_all[LINE::kSolo ? 16 : 1][16];  // (a workgroup has sixteen wavefronts at most)
+    float2 *const joined = joined_all[LINE::kSolo ? threadIdx.x >> 6 : 0];
+    constexpr int kBatch = LINE::kBatch;
+    const int cols = a.head_dim / 4, tid = LINE::kSolo ? threadIdx.x & 63 : threadIdx.x;
     for (int i0 = 0; i0 < heads * cols; i0 += 64 * LINE::kWaves) {
         const int i = i0 + tid;
         const bool on = i < heads * cols;
         const int h = on ? i / cols : 0, d = on ? 4 * (i - h * cols) : 0;
-        // eight parts at a time, all their loads in flight together
+        // kBatch parts at a time, all their loads in flight together
         float m = -INFINITY, l = 0.f;
         f4_t sum = f4_t{0.f, 0.f, 0.f, 0.f};
         for (int p0 = 0; p0 < n; p0 += kBatch) {
@@ -382,7 +412,7 @@ __device__ inline void join_parts(const AttnArgs &a, int32_t row, int32_t w0, in
         }
     }
     if (finish) return;
-    __syncthreads();  // every lane has read its heads' (m, l) of part0
+    line_sync<LINE>();  // every lane has read its heads' (m, l) of part0
     if (tid < heads)
         put_part(&a.part_ml[2 * ((int64_t)part_slot(w0, part0) * a.q_heads + head0 + tid)], joined[tid].x, joined[tid].y);
 }
@@ -395,12 +425,13 @@ template <typename T, typename LINE>
 __device__ inline void join_row(const AttnArgs &a, int32_t row, int32_t w0, int32_t parts, int32_t part, int per_share,
                                 int rest, int64_t head0, int heads)
 {
-    const int group0 = part / kAttnJoin * kAttnJoin, n_groups = (parts + kAttnJoin - 1) / kAttnJoin;
-    const int in_group = min(kAttnJoin, parts - group0);
-    if (!last_arrival(a.count + (int64_t)part_slot(w0, group0) * per_share + rest, in_group)) return;
+    const int width = parts <= LINE::kOnce ? parts : kAttnJoin;
+    const int group0 = part / width * width, n_groups = (parts + width - 1) / width;
+    const int in_group = min(width, parts - group0);
+    if (!last_arrival<LINE>(a.count + (int64_t)part_slot(w0, group0) * per_share + rest, in_group)) return;
     join_parts<T, LINE>(a, row, w0, head0, heads, group0, 1, in_group, n_groups == 1);
     // (part 1 leads no group, so its counter is free for the groups)
-    if (n_groups == 1 || !last_arrival(a.count + (int64_t)part_slot(w0, 1) * per_share + rest, n_groups)) return;
+    if (n_groups == 1 || !last_arrival<LINE>(a.count + (int64_t)part_slot(w0, 1) * per_share + rest, n_groups)) return;
     join_parts<T, LINE>(a, row, w0, head0, heads, 0, kAttnJoin, n_groups, true);
 }
 
@@ -548,7 +579,7 @@ int fill_attention(AttnArgs &a, int32_t n_rows, int32_t q_heads, void *out, int6
     a.group = q_heads / kv_heads;
     a.head_tiles = (a.group + 15) / 16;
     // no row is longer than its table or the window, and no share shorter than kMinShare
-    const int64_t span = std::min<int64_t>((int64_t)max_blocks * page_size, window > 0 ? window : INT32_MAX);
+    const int64_t span = std::min<int64_t>((int64_t)max_blocks * page_size, window > 0 ? (int64_t)window + LINE::kAlign - 1 : INT32_MAX);
     const int64_t line = n_rows * ((span + LINE::kTile - 1) / LINE::kTile + LINE::kRowTiles);
     if (line > INT32_MAX - most)  // (rounded up to whole shares)
         return fail(LORA_E_UNSUPPORTED, "%d rows of up to %lld tokens", n_rows, (long long)span);
@@ -569,9 +600,10 @@ int fill_attention(AttnArgs &a, int32_t n_rows, int32_t q_heads, void *out, int6
     return LORA_OK;
 }
 
-dim3 attention_grid(const AttnArgs &a)
+// Workgroups of `per` shares each.
+dim3 attention_grid(const AttnArgs &a, int per = 1)
 {
-    const int32_t pairs = a.shares * a.kv_heads;
+    const int32_t pairs = (a.shares * a.kv_heads + per - 1) / per;
     return dim3((unsigned)(a.head_tiles > 1 ? (pairs + 7) / 8 * 8 * a.head_tiles : pairs));
 }
 
