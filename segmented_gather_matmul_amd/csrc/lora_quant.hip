@@ -133,7 +133,7 @@ __device__ inline Cell cell_of(const lora_quant_cache &c, int shift, int32_t slo
 
 // ------------------------------------------------------------------------ rotary positions and append
 struct QuantAppendArgs {
-    int32_t q_heads, kv_heads, head_dim, rot, n_axes, shift;
+    int32_t n_rows, q_heads, kv_heads, head_dim, rot, n_axes, shift;
     int32_t units_q;   // chunks of a head of q, or pairs of chunks that turn together
     int32_t units_kv;  // chunks of a padded head of k or v
     int32_t n_q;       // units of all heads of q, rounded up to a multiple of 4
@@ -166,16 +166,33 @@ __device__ inline uint32_t quad_max(uint32_t v)
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
 }
 
-// blockIdx.x is the token row; its units go round over the threads of its gridDim.y workgroups.  A unit is
-// eight columns of the cells of k or v, four neighbouring lanes a block, or what turns together of a head of
-// q.  k is turned in 64 bits: where a value rounds to one code or the next must not hang on the last
+// Rows of a launch with one workgroup each: the rows of a page lie 16 to a group, and groups go to the 8 XCDs in turn
+// (workgroups do), so that what neighbouring tokens write of a line meets in one L2.
+constexpr int kRowGroup = 16;
+constexpr int32_t kFillRows = 1024;  // rows that fill the CUs with one workgroup each
+__device__ inline int64_t row_of_group(uint32_t b)
+{
+    return ((int64_t)(b / (8 * kRowGroup)) * 8 + b % 8) * kRowGroup + b / 8 % kRowGroup;
+}
+unsigned groups_of_rows(int32_t n) { return (unsigned)(((int64_t)n + 8 * kRowGroup - 1) / (8 * kRowGroup) * (8 * kRowGroup)); }
+
+// A workgroup works on one token row (GROUPED: see above; else blockIdx.x, and its units go round over the threads of
+// gridDim.y workgroups).  A unit is eight columns of the cells of k or v, four neighbouring lanes a block, or what turns
+// together of a head of q.  k is turned in 64 bits: where a value rounds to one code or the next must not hang on the last
 // bits of a sine, and 64-bit multiply-adds run at the rate of 32-bit ones here.
-template <typename T, bool INTER, int BITS>
+//
+// What it reads and writes bounds a long call (4096 rows of 64 and 8 heads of 128, 8 bits: 30.3 us, 5.1 TB/s), and the
+// sines and turns in 64 bits one with as many heads of k (8192 rows of 32 heads, 4 bits: 111 us, 4.3 TB/s); a short one
+// (32 rows of 32 heads) is 3.6 us of one row's latency.  Rows in groups are 3% faster there, and marking q_out as not
+// read again makes 35.7 us into 30.3.  Two units at a time, asked for before the turns, cost more in registers and so in
+// wavefronts than they hid: 121 us.
+template <typename T, bool INTER, int BITS, bool GROUPED, bool STREAM>
 __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs a)
 {
     __shared__ double2 cs[LORA_KV_MAX_HEAD_DIM / 2];
     const int tid = threadIdx.x;
-    const int64_t t = blockIdx.x;
+    const int64_t t = GROUPED ? row_of_group(blockIdx.x) : blockIdx.x;
+    if (t >= a.n_rows) return;
     const int32_t slot = a.slots[t];
     const int half = a.rot / 2;
     for (int i = tid; i < half; i += blockDim.x) {
@@ -197,7 +214,7 @@ __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs 
             const int64_t from = t * a.ldq + (int64_t)h * a.head_dim + d, to = t * a.ldqo + (int64_t)h * a.head_dim + d;
             const uint4 ra = load16(a.q, from);
             if (turn < 0) {
-                store16(a.q_out, to, ra);
+                store16<STREAM>(a.q_out, to, ra);
                 continue;
             }
             float x[8], y[8];
@@ -209,7 +226,7 @@ __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs 
                     y[2 * e] = __builtin_fmaf(x[2 * e], c, -(x[2 * e + 1] * s));
                     y[2 * e + 1] = __builtin_fmaf(x[2 * e], s, x[2 * e + 1] * c);
                 }
-                store16(a.q_out, to, pack8<T>(y));
+                store16<STREAM>(a.q_out, to, pack8<T>(y));
             } else {
                 float b[8], z[8];
                 unpack8<T>(load16(a.q, from + half), b);
@@ -219,8 +236,8 @@ __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs 
                     y[e] = __builtin_fmaf(x[e], c, -(b[e] * s));
                     z[e] = __builtin_fmaf(x[e], s, b[e] * c);
                 }
-                store16(a.q_out, to, pack8<T>(y));
-                store16(a.q_out, to + half, pack8<T>(z));
+                store16<STREAM>(a.q_out, to, pack8<T>(y));
+                store16<STREAM>(a.q_out, to + half, pack8<T>(z));
             }
             continue;
         }
@@ -268,32 +285,48 @@ __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs 
 // ------------------------------------------------------------------------ reading back
 struct QuantReadArgs {
     int32_t n_rows, kv_heads, head_dim, shift;
+    int32_t rows, units;  // rows of a workgroup; units of a row
+    uint32_t magic;       // 2^32 / units, rounded up: its product with fewer than 2^16 has the quotient in its upper half
     void *k_out, *v_out;
     int64_t ldko, ldvo;
     const int32_t *slots;
     lora_quant_cache c;
 };
 
-// blockIdx.x is the row; its chunks of eight columns go round over the threads.
-template <typename T, int BITS>
+// A unit is eight columns of k or v of one row.  A workgroup has a.rows rows (then gridDim.y is 1) or a part of one; a
+// thread asks for AHEAD units before it stores the first.  Bound by what it writes, 16 bits a value: 16,384 rows of 32
+// heads of 128, of 4 bits, read in 45 us (6.0 TB/s); 131,072 rows of 1 head, of 8 bits, in 35 us (5.8 TB/s).  One unit at
+// a time took 52 us there, and 68 the larger, whose outputs a last-use mark then kept from driving the cells out of L2.
+template <typename T, int BITS, bool STREAM, int AHEAD>
 __global__ __launch_bounds__(256) void lora_quant_read_kernel(QuantReadArgs a)
 {
-    const int64_t t = blockIdx.x;
-    const int32_t slot = a.slots[t];
-    if (slot < 0 || slot >= (int64_t)a.c.num_pages << a.shift) return;
-    const Cell cell = cell_of(a.c, a.shift, slot);
-    const int chunks = a.head_dim / 8, n = a.kv_heads * chunks;
-    const int first = a.k_out ? 0 : n, last = a.v_out ? 2 * n : n;
-    for (int u = first + blockIdx.y * blockDim.x + threadIdx.x; u < last; u += blockDim.x * gridDim.y) {
-        const bool is_k = u < n;
-        const int i = is_k ? u : u - n, h = i / chunks, d = 8 * (i - h * chunks);
-        const uint8_t *const codes = static_cast<const uint8_t *>(is_k ? a.c.k : a.c.v);
-        const uint8_t *const exps = is_k ? a.c.k_exp : a.c.v_exp;
-        const Codes<BITS> c = load_codes<BITS>(codes + cell.code + h * a.c.head_stride + d * BITS / 8);
-        const float scale = power_of(exps[cell.exp + h * a.c.exp_head_stride + d / kBlock]);
-        const uint4 v = values_of(T{}, c.w, scale);
-        if (is_k) store16(a.k_out, t * a.ldko + 8 * (int64_t)i, v);
-        else store16(a.v_out, t * a.ldvo + 8 * (int64_t)i, v);
+    const int chunks = a.head_dim / 8, n = a.kv_heads * chunks, first = a.k_out ? 0 : n;
+    const int64_t t0 = (int64_t)blockIdx.x * a.rows;
+    const int all = a.rows * a.units, step = blockDim.x * gridDim.y;
+    for (int f0 = blockIdx.y * blockDim.x + threadIdx.x; f0 < all; f0 += AHEAD * step) {
+        Codes<BITS> c[AHEAD];
+        uint32_t exp[AHEAD];
+        void *to[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int f = f0 + j * step, r = a.rows > 1 ? (int)__umulhi((uint32_t)f, a.magic) : 0;
+            const int64_t t = t0 + r;
+            const int32_t slot = f < all && t < a.n_rows ? a.slots[t] : -1;
+            to[j] = nullptr;
+            if (slot < 0 || slot >= (int64_t)a.c.num_pages << a.shift) continue;
+            const Cell cell = cell_of(a.c, a.shift, slot);
+            const int u = first + f - r * a.units;
+            const bool is_k = u < n;
+            const int i = is_k ? u : u - n, h = i / chunks, d = 8 * (i - h * chunks);
+            const uint8_t *const codes = static_cast<const uint8_t *>(is_k ? a.c.k : a.c.v);
+            const uint8_t *const exps = is_k ? a.c.k_exp : a.c.v_exp;
+            c[j] = load_codes<BITS>(codes + cell.code + h * a.c.head_stride + d * BITS / 8);
+            exp[j] = exps[cell.exp + h * a.c.exp_head_stride + d / kBlock];
+            to[j] = static_cast<uint16_t *>(is_k ? a.k_out : a.v_out) + t * (is_k ? a.ldko : a.ldvo) + 8 * (int64_t)i;
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (to[j]) store16<STREAM>(to[j], 0, values_of(T{}, c[j].w, power_of(exp[j])));
     }
 }
 
@@ -829,6 +862,7 @@ int lora_quant_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out
         return st;
     if (n_rows == 0) return LORA_OK;
     QuantAppendArgs a{};
+    a.n_rows = n_rows;
     a.q_heads = q_heads;
     a.kv_heads = cache->kv_heads;
     a.head_dim = cache->head_dim;
@@ -855,14 +889,18 @@ int lora_quant_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t units = a.n_q + 2 * (int64_t)a.kv_heads * a.units_kv;
     // One workgroup per row, unless there are too few rows to fill the CUs: then one per 256 units.
-    const int64_t groups = n_rows < 1024 ? std::min<int64_t>((units + 255) / 256, 64) : 1;
-    const dim3 grid((unsigned)n_rows, (unsigned)groups);
+    const bool grouped = n_rows >= kFillRows;
+    const int64_t groups = grouped ? 1 : std::min<int64_t>((units + 255) / 256, 64);
+    const dim3 grid(grouped ? groups_of_rows(n_rows) : (unsigned)n_rows, (unsigned)groups);
     const int threads = (int)std::min<int64_t>((units + 63) / 64 * 64, 256);
-    if ((st = check_rows(n_rows, threads))) return st;
+    if ((st = check_rows(n_rows, threads, 8 * kRowGroup))) return st;
     const bool bf = cache->type == LORA_TYPE_BF16, four = cache->bits == 4;
-#define LORA_QAPPEND(T, INTER)                                                                   \
-    (four ? launch(lora_quant_append_kernel<T, INTER, 4>, grid, threads, 0, s, a)                \
-          : launch(lora_quant_append_kernel<T, INTER, 8>, grid, threads, 0, s, a))
+    const bool stream_out = 2 * (int64_t)n_rows * q_heads * cache->head_dim > kStreamBytes;
+#define LORA_QAPPEND3(T, INTER, BITS)                                                                           \
+    (!grouped ? launch(lora_quant_append_kernel<T, INTER, BITS, false, false>, grid, threads, 0, s, a)          \
+     : stream_out ? launch(lora_quant_append_kernel<T, INTER, BITS, true, true>, grid, threads, 0, s, a)        \
+                  : launch(lora_quant_append_kernel<T, INTER, BITS, true, false>, grid, threads, 0, s, a))
+#define LORA_QAPPEND(T, INTER) (four ? LORA_QAPPEND3(T, INTER, 4) : LORA_QAPPEND3(T, INTER, 8))
     if (rope->interleaved) {
         if (bf) LORA_QAPPEND(BF16, true);
         else LORA_QAPPEND(F16, true);
@@ -871,6 +909,7 @@ int lora_quant_append(void *stream, int32_t n_rows, int32_t q_heads, void *q_out
         else LORA_QAPPEND(F16, false);
     }
 #undef LORA_QAPPEND
+#undef LORA_QAPPEND3
     return launch_status("quantising append");
 }
 
@@ -889,18 +928,28 @@ int lora_quant_read(void *stream, int32_t n_rows, void *k_out, int64_t ldko, voi
     if (v_out && (st = check_matrix(v_out, ldvo, cols, "v_out"))) return st;
     if ((st = check_apart(k_out, ldko, cols, v_out, ldvo, cols, n_rows, false, "k_out and v_out"))) return st;
     if (!slots) return fail(LORA_E_NULL, "slots is NULL");
-    QuantReadArgs a{n_rows, cache->kv_heads, cache->head_dim, page_shift(cache->page_size), k_out, v_out, ldko, ldvo, slots, *cache};
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t units = ((k_out ? 1 : 0) + (v_out ? 1 : 0)) * cols / 8;
-    const int64_t groups = n_rows < 1024 ? std::min<int64_t>((units + 255) / 256, 64) : 1;
-    const dim3 grid((unsigned)n_rows, (unsigned)groups);
-    const int threads = (int)std::min<int64_t>((units + 63) / 64 * 64, 256);
+    // Where there are rows enough, workgroups with 8 KB of codes or one row, four units a thread at a time; else one unit
+    // a thread.  16,384 rows of 32 heads of 128: 4 bits 51.2 us with 4 KB and 44.9 with 8; 8 bits 64.3 with 8 and 66.9 with 16.
+    const int64_t share = 8192 / cache->bits;
+    const bool many = n_rows * units >= kFillRows * (int64_t)1024;
+    const int32_t rows = many ? (int32_t)std::max<int64_t>(1, share / units) : 1;
+    const int64_t groups = many ? 1 : std::min<int64_t>((units + 255) / 256, 64);
+    QuantReadArgs a{n_rows, cache->kv_heads, cache->head_dim, page_shift(cache->page_size), rows, (int32_t)units,
+                    (uint32_t)((((uint64_t)1 << 32) + units - 1) / units), k_out, v_out, ldko, ldvo, slots, *cache};
+    const dim3 grid((unsigned)((n_rows + (int64_t)rows - 1) / rows), (unsigned)groups);
+    const int threads = (int)std::min<int64_t>((rows * units + 63) / 64 * 64, 256);
     if ((st = check_rows(n_rows, threads))) return st;
     const bool bf = cache->type == LORA_TYPE_BF16, four = cache->bits == 4;
-    if (four) bf ? launch(lora_quant_read_kernel<BF16, 4>, grid, threads, 0, s, a)
-                 : launch(lora_quant_read_kernel<F16, 4>, grid, threads, 0, s, a);
-    else bf ? launch(lora_quant_read_kernel<BF16, 8>, grid, threads, 0, s, a)
-            : launch(lora_quant_read_kernel<F16, 8>, grid, threads, 0, s, a);
+    const bool stream_out = 16 * n_rows * units > kStreamBytes;
+#define LORA_QREAD(T, BITS)                                                                      \
+    (!many ? launch(lora_quant_read_kernel<T, BITS, false, 1>, grid, threads, 0, s, a)           \
+     : stream_out ? launch(lora_quant_read_kernel<T, BITS, true, 4>, grid, threads, 0, s, a)     \
+                  : launch(lora_quant_read_kernel<T, BITS, false, 4>, grid, threads, 0, s, a))
+    if (four) bf ? LORA_QREAD(BF16, 4) : LORA_QREAD(F16, 4);
+    else bf ? LORA_QREAD(BF16, 8) : LORA_QREAD(F16, 8);
+#undef LORA_QREAD
     return launch_status("quantised read");
 }
 

@@ -479,10 +479,10 @@ int check_apart(const void *out, int64_t ldo, int64_t cols_o, const void *in, in
     return fail(LORA_E_SHAPE, "%s overlap", what);
 }
 
-// A launch of one workgroup per row has at most 2^32 - 1 threads along its rows.
-int check_rows(int32_t n_rows, int threads)
+// A launch of one workgroup per row has at most 2^32 - 1 threads along its rows, which may be rounded up by `more`.
+int check_rows(int32_t n_rows, int threads, int more = 0)
 {
-    if ((int64_t)n_rows * threads > UINT32_MAX)
+    if (((int64_t)n_rows + more) * threads > UINT32_MAX)
         return fail(LORA_E_UNSUPPORTED, "%d rows of %d threads are too many for one launch", n_rows, threads);
     return LORA_OK;
 }
