@@ -43,8 +43,9 @@ extern "C" {
  * and whose exponents are the `blocks` bytes at
  *     k_exp + p*exp_page_stride + off*exp_token_stride + h*exp_head_stride   (v_exp alike).
  * Heads before tokens in memory ([page][head][token]) keeps the tokens that one head reads
- * together, which is what the attention runs fastest on.  The tokens of one page and head span less
- * than 2^31 bytes; everything else may lie 2^48 bytes apart.  The slot of a token is p*page_size + off; num_pages * page_size <= 2^31 - 1.  Memory of zeros reads as zeros.
+ * together, which is what the attention runs fastest on.  The tokens of one page and head span
+ * less than 2^31 bytes; everything else may lie 2^48 bytes apart.  The slot of a token is
+ * p*page_size + off; num_pages * page_size <= 2^31 - 1.  Memory of zeros reads as zeros.
  * Codes of columns from head_dim on are written as 0 and take no part in any result, but a
  * block's exponent byte is shared: they must not be NaN (8 bits: 0x7f, 0xff) in a cache that
  * something else has written.

@@ -24,7 +24,8 @@ extern "C" {
  * One draw.  With l the row's logits (NaN counts as -inf), top their largest and t its temperature:
  *   order   tokens by logit, largest first, equal ones by index;
  *   weight  w_i = floor(2^40 exp((l_i - top) / t)), a whole number (where top is +inf: 2^40 for l_i = +inf,
- *           else 0); masses are sums of weights, exact in 64 bits, so that nothing depends on their order;
+ *           else 0), the exponential being right to 2^-37 of itself; masses are sums of weights, exact in
+ *           64 bits, so that nothing depends on their order;
  *   top-k   the first k in order stay (k = 0: all);
  *   top-p   of these, the ones stay before which, in order, lies a mass below p times theirs; the first stays
  *           always;
@@ -46,7 +47,8 @@ extern "C" {
  *   token        device int32 [n_rows]
  *   logprob      device fp32 [n_rows] or NULL
  *   work         device memory of at least lora_sample_bytes(n_rows, vocab) bytes, 256-byte aligned, of any
- *                content; calls that may run at the same time need their own
+ *                content; calls that may run at the same time need their own (rows fit a CU's LDS
+ *                today, so its least size is all that is asked for, and it is not written)
  */
 typedef struct lora_sample_args {
     int32_t type;        /* LORA_TYPE_F16, LORA_TYPE_BF16 or LORA_TYPE_F32 */

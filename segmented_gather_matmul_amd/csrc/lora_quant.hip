@@ -174,15 +174,18 @@ __device__ inline int64_t row_of_group(uint32_t b)
 {
     return ((int64_t)(b / (8 * kRowGroup)) * 8 + b % 8) * kRowGroup + b / 8 % kRowGroup;
 }
-unsigned groups_of_rows(int32_t n) { return (unsigned)(((int64_t)n + 8 * kRowGroup - 1) / (8 * kRowGroup) * (8 * kRowGroup)); }
+unsigned groups_of_rows(int32_t n)
+{
+    return (unsigned)(((int64_t)n + 8 * kRowGroup - 1) / (8 * kRowGroup) * (8 * kRowGroup));
+}
 
 // A workgroup works on one token row (GROUPED: see above; else blockIdx.x, and its units go round over the threads of
 // gridDim.y workgroups).  A unit is eight columns of the cells of k or v, four neighbouring lanes a block, or what turns
 // together of a head of q.  k is turned in 64 bits: where a value rounds to one code or the next must not hang on the last
 // bits of a sine, and 64-bit multiply-adds run at the rate of 32-bit ones here.
 //
-// What it reads and writes bounds a long call (4096 rows of 64 and 8 heads of 128, 8 bits: 30.3 us, 5.1 TB/s), and the
-// sines and turns in 64 bits one with as many heads of k (8192 rows of 32 heads, 4 bits: 111 us, 4.3 TB/s); a short one
+// What it reads and writes bounds a long call (4096 rows of 64 and 8 heads of 128, 4 bits: 30.3 us, 5.1 TB/s), and the
+// sines and turns in 64 bits one with as many heads of k (12,907 rows of 32 heads, 4 bits: 111 us, 4.3 TB/s); a short one
 // (32 rows of 32 heads) is 3.6 us of one row's latency.  Rows in groups are 3% faster there, and marking q_out as not
 // read again makes 35.7 us into 30.3.  Two units at a time, asked for before the turns, cost more in registers and so in
 // wavefronts than they hid: 121 us.
@@ -294,9 +297,9 @@ struct QuantReadArgs {
 };
 
 // A unit is eight columns of k or v of one row.  A workgroup has a.rows rows (then gridDim.y is 1) or a part of one; a
-// thread asks for AHEAD units before it stores the first.  Bound by what it writes, 16 bits a value: 16,384 rows of 32
-// heads of 128, of 4 bits, read in 45 us (6.0 TB/s); 131,072 rows of 1 head, of 8 bits, in 35 us (5.8 TB/s).  One unit at
-// a time took 52 us there, and 68 the larger, whose outputs a last-use mark then kept from driving the cells out of L2.
+// thread asks for AHEAD units before it stores the first.  Bound by what it writes, 16 bits a value: 12,907 rows of 32
+// heads of 128, of 4 bits, in 45 us (6.0 TB/s); 32,749 rows of 8 heads, of 8 bits, in 35 us (5.8 TB/s).  One row a
+// workgroup and one unit a thread at a time took 68 and 52 us; marking the outputs as not read again makes the former 51.
 template <typename T, int BITS, bool STREAM, int AHEAD>
 __global__ __launch_bounds__(256) void lora_quant_read_kernel(QuantReadArgs a)
 {
@@ -337,7 +340,8 @@ struct QuantArgs : AttnArgs {
 
 constexpr int kQWaves = 4, kQTile = 64;
 // The two ways to split the rows' tiles (quant_solo): a workgroup's wavefronts take those of a part in turn and join
-// at its end, or each wavefront has parts of its own and waits for no other.
+// at its end, or each wavefront has parts of its own and waits for no other.  A tile of 64 tokens is what the registers
+// hold of K and V in flight while the one before is worked on; two workgroups fit a CU up to 128 columns, one beyond.
 typedef AttnLine<kQWaves, kQTile, 8, 8, 16, false, 8, 32> GangLine;
 typedef AttnLine<kQWaves, kQTile, 4, 2, 16, true, 8, 32> SoloLine;
 constexpr int kQSub = kQTile / 16;  // 16-token subtiles of a tile
@@ -390,6 +394,15 @@ __device__ inline float column_max(float x)
 // keeps the scores of its own column's subtile and lays the others aside, so the softmax
 // of R subtiles costs what one does, and each copy has its own maximum and sums, which are joined
 // at the row's end.
+//
+// What is rounded: nothing on the way from codes to products, which are summed in 32 bits; the weights, cut to two 16-bit
+// parts (split_weight); the output, once.  Maxima, sums and joins are in 32 bits.
+//
+// Long rows are bound by the cells' bytes: 32 rows of 8192 tokens, 32/32 heads of 128, in 200 us with 4 bits (5.7 TB/s),
+// 8 bits at 5.3 TB/s.  32 rows of 64 to 4096 tokens (135 MB) take 34.7 us, of which the read is 22.4 and the rest
+// starting, the rows' ends and joins; one row of 131,071 tokens of 1 head 18.4 (a read of 3); one of 17 tokens 7.6, loads
+// one after another.  All of V converted at the top of a round, in twice the LDS, was slower; joins that load 16 parts
+// at a time, and not 8, cost every call registers.
 template <typename T, int BITS, int DP, int R, typename LINE, bool PAGES>
 __global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(quant_occupancy(DP)))) void
 lora_quant_attention_kernel(QuantArgs a)
@@ -931,7 +944,7 @@ int lora_quant_read(void *stream, int32_t n_rows, void *k_out, int64_t ldko, voi
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t units = ((k_out ? 1 : 0) + (v_out ? 1 : 0)) * cols / 8;
     // Where there are rows enough, workgroups with 8 KB of codes or one row, four units a thread at a time; else one unit
-    // a thread.  16,384 rows of 32 heads of 128: 4 bits 51.2 us with 4 KB and 44.9 with 8; 8 bits 64.3 with 8 and 66.9 with 16.
+    // a thread.  12,907 rows of 32 heads of 128: 4 bits 51.2 us with 4 KB and 44.9 with 8; 8 bits 64.3 with 8, 66.9 with 16.
     const int64_t share = 8192 / cache->bits;
     const bool many = n_rows * units >= kFillRows * (int64_t)1024;
     const int32_t rows = many ? (int32_t)std::max<int64_t>(1, share / units) : 1;

@@ -16,16 +16,17 @@ form, for tiles of fewer than 8 rows).  Optionally each shrink runs on a second 
 while the backbone GEMM of the same input runs, so only the expands stay on the layer's
 critical path.
 
-Left out of the dense step on purpose: rotary position embedding.  In the dense step (LoraDecoderLayer.forward) the current token's k and v are
-written into the last position of the cache, so attention spans `seq_len` positions
-including it.
+Left out of the dense step on purpose: rotary position embedding.  In the dense step
+(LoraDecoderLayer.forward) the current token's k and v are written into the last position of
+the cache, so attention spans `seq_len` positions including it.
 
 The paged step (forward_paged) serves requests of any lengths, new tokens of prompts and of
 decoding requests in one batch, over a paged cache: PagedStep plans the step on the
 device from the requests' lengths once for all layers (pages, cache slots, the rows'
 adapter ids), and each layer runs the residual adds with their norms, rotary positions
-with the append to the cache, and attention over it in this library's kernels too.  The cache holds
-16-bit values, or (kv_bits) 8- or 4-bit ones; PagedStep.sample draws the requests' next tokens.
+with the append to the cache, and attention over it in this library's kernels too.  The
+cache holds 16-bit values, or (kv_bits) 8- or 4-bit ones; PagedStep.sample draws the requests'
+next tokens.
 """
 from __future__ import annotations
 
@@ -315,8 +316,8 @@ class LoraDecoderLayer:
     def forward_paged(self, hidden, cache, step: PagedStep, meta: BatchMeta | None, trace: dict | None = None):
         """hidden [step.max_tokens, h] fp16 -> the same, for the token rows of the step planned
         last; rows behind the last token are not read by any other row.  cache: this layer's
-        step.PagedKV, or quant.QuantKV where the step's kv_bits is 8 or 4, of the step's page size and heads
-        and at least its number of pages.
+        step.PagedKV, or quant.QuantKV where the step's kv_bits is 8 or 4, of the step's page size
+        and heads and at least its number of pages.
         meta and trace as for forward (meta: BatchMeta.of_step)."""
         import torch
         import torch.nn.functional as F

@@ -1,11 +1,11 @@
 """Plain reference of sampling (lora_sample.h) on the CPU, row by row by its definition.  Test infrastructure only.
 
-Weights are floor(2^40 exp(z)) of a 64-bit exponential, off by 2^-50 of itself here and in the kernel, so a weight may
-differ by one unit of 2^-40 where the product is that near a whole number; masses then differ by a few units, and a draw
-whose u M lies that near a border between two tokens takes the other one.  For n tokens of which a part of 2^-9 differ,
-that is a chance below n (n 2^-9) 2^-40 a row, 10^-5 at 70,000 tokens; the inputs here are fixed and were drawn once.
-logprob: z and the logarithm in 64 bits, rounded to 32: 2^-24 (|z| + |log|) and half a step of the result; the mass
-M by one unit in 2^40 a token.
+Weights are floor(2^40 exp(z)) of a 64-bit exponential here and of one right to 2^-37 in the kernel, so that they differ
+by 2^-37 of a weight and a unit; the masses up to a token then by 2^-37 of themselves and a unit a token, and a draw whose
+u M lies that near a border between two of n tokens takes the other one: a chance below n (2^-37 + n 2^-40) a row,
+5 10^-3 at 70,000 tokens of equal weight and far less where few hold the mass; the inputs here are fixed and were drawn
+once.  logprob: z and the logarithm in 64 bits, rounded to 32: 2^-24 (|z| + |log|) and half a step of the result; the
+mass M by 2^-37 of itself, within half of the bound from 8 tokens on (one token's weight is exact), and a unit in 2^40 a token.
 """
 import math
 
