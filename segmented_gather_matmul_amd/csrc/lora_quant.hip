@@ -289,7 +289,8 @@ __global__ __launch_bounds__(256) void lora_quant_append_kernel(QuantAppendArgs 
 struct QuantReadArgs {
     int32_t n_rows, kv_heads, head_dim, shift;
     int32_t rows, units;  // rows of a workgroup; units of a row
-    uint32_t magic;       // 2^32 / units, rounded up: its product with fewer than 2^16 has the quotient in its upper half
+    uint32_t magic;       // 2^32 / units, rounded up: its product with fewer than 2^16 has the quotient in its upper
+                          // half; 0 where there is one unit, which 32 bits do not hold
     void *k_out, *v_out;
     int64_t ldko, ldvo;
     const int32_t *slots;
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(256) void lora_quant_read_kernel(QuantReadArgs a)
         void *to[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            const int f = f0 + j * step, r = a.rows > 1 ? (int)__umulhi((uint32_t)f, a.magic) : 0;
+            const int f = f0 + j * step, r = a.rows == 1 ? 0 : a.magic ? (int)__umulhi((uint32_t)f, a.magic) : f;
             const int64_t t = t0 + r;
             const int32_t slot = f < all && t < a.n_rows ? a.slots[t] : -1;
             to[j] = nullptr;

@@ -218,6 +218,61 @@ def test_read_gives_every_code_at_every_exponent(K, D, P, layout, bits, dt):
     assert torch.equal(only.view(torch.int16), ko.contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("what", ["k", "v", "kv"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("K,D,n", [(1, 8, 1100000), (1, 16, 600001), (3, 40, 140003), (2, 256, 17001), (70, 128, 1021)])
+def test_reads_of_many_rows_are_those_of_few(K, D, n, bits, what):
+    """Rows of one unit and of many, several to a workgroup, outputs beside which the cache does not stay in L2: the
+    same bits as one row of each slot at a time."""
+    say(f"case quant-read-many K={K} D={D} n={n} bits={bits} {what}")
+    pages, P = 9, 8
+    c = new_cache(pages, P, K, D, BF16, bits, seed=n)
+    each = [torch.full((pages * P, K * D), 5.0, dtype=BF16, device="cuda") for _ in range(2)]
+    Q.lora_quant_read(*each, c, torch.arange(pages * P, dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(n)
+    slots = torch.randint(-4, pages * P + 4, (n,), generator=g, device="cuda").int()
+    outs = [torch.full((n + 1, K * D), 5.0, dtype=BF16, device="cuda") if w in what else None for w in "kv"]
+    Q.lora_quant_read(*[None if o is None else o[:n] for o in outs], c, slots)
+    torch.cuda.synchronize()
+    live = (slots >= 0) & (slots < pages * P)
+    for o, e in zip(outs, each):
+        if o is not None:
+            want = torch.where(live[:, None], e.view(torch.int16)[slots.clamp(0, pages * P - 1).long()],
+                               torch.full((1,), 5.0, dtype=BF16, device="cuda").view(torch.int16))
+            assert torch.equal(o[:n].view(torch.int16), want) and bool((o[n:] == 5.0).all())
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("H,K,D,n", [(130, 2, 128, 1031), (2, 1, 64, 5001), (0, 3, 40, 1153), (300, 1, 80, 1025)])
+def test_appends_of_many_rows_are_those_of_few(H, K, D, n, bits, inter):
+    """A workgroup to a row, in groups, and q_out beyond what the L2s hold: the same bits as the rows a hundred at a
+    time, with rows between them that name no slot."""
+    say(f"case quant-append-many H={H} K={K} D={D} n={n} bits={bits} inter={inter}")
+    g = torch.Generator(device="cuda").manual_seed(n)
+    P = 16
+    pages = -(-n // P)
+    x = torch.randn(n, (H + 2 * K) * D, generator=g, device="cuda").to(BF16)
+    q, k, v = x[:, :H * D], x[:, H * D:(H + K) * D], x[:, (H + K) * D:]
+    slots = torch.randperm(pages * P, generator=g, device="cuda")[:n].int()
+    slots[torch.rand(n, generator=g, device="cuda") < 0.1] = -1
+    pos = torch.randint(0, 100000, (1, n), generator=g, device="cuda", dtype=torch.int32)
+    rope = S.Rope(S.Rope.base(D if D != 40 else 32).inv_freq, None, 1, inter)
+    got = []
+    for step in (n, 100):
+        c = new_cache(pages, P, K, D, BF16, bits, seed=3)
+        out = torch.full((n + 1, max(H, 1) * D), 5.0, dtype=BF16, device="cuda")
+        for a in range(0, n, step):
+            b = min(a + step, n)
+            Q.lora_quant_append(out[a:b] if H else None, q[a:b] if H else None, k[a:b], v[a:b], c, slots[a:b], rope=rope,
+                                positions=pos[:, a:b].contiguous())
+        torch.cuda.synchronize()
+        got.append(bytes_of(c) + [out])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool((got[0][-1][n:] == 5.0).all()) and bool((got[0][-1][:n][slots < 0] == 5.0).all())
+
+
 # ------------------------------------------------------------------ attention
 class Attn:
     """A batch of requests of those lengths over a cache of normal values."""
