@@ -135,9 +135,16 @@ def attention_workspace(n_rows, heads, cache: QuantKV, device=None):
     return workspace(n_rows, heads, cache.kv_heads, cache.head_dim, cache.k.device if device is None else device)
 
 
+def _quantised(cache):
+    """The library reads a descriptor by its address, so another cache's must not get there."""
+    if not isinstance(cache, QuantKV):
+        raise ValueError(f"cache must be a QuantKV (got {type(cache).__name__})")
+
+
 def lora_quant_append(q_out, q, k, v, cache: QuantKV, slots, rope: S.Rope | None = None, positions=None, stream=None):
     """Rotate q into q_out and k into the cache at `slots`, and append v; k and v are quantised.  Arguments as for
     step.lora_rope_append."""
+    _quantised(cache)
     rope = S._NoRope if rope is None else rope
     if S._fast:
         dev = S._device(slots)
@@ -151,6 +158,7 @@ def lora_quant_append(q_out, q, k, v, cache: QuantKV, slots, rope: S.Rope | None
 def lora_quant_read(k_out, v_out, cache: QuantKV, slots, stream=None):
     """k_out and v_out [n_rows, kv_heads * head_dim] take the values of the cells at `slots` int32 [n_rows]; rows of
     another slot than one of the cache's (-1: none) stay as they were.  Either output may be None."""
+    _quantised(cache)
     if S._fast:
         dev = S._device(slots)
         if dev >= 0 and S._done(S._fast.quant_read(S._address("lora_quant_read"), S._raw(stream, dev), dev, k_out, v_out,
@@ -168,6 +176,7 @@ def lora_quant_attention(out, q, cache: QuantKV, block_table, kv_len, work, req=
                          stream=None):
     """Attention of one query token per row over the values of the cells; arguments as for
     step.lora_paged_attention, work from attention_workspace."""
+    _quantised(cache)
     scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
     if S._fast:
         dev = S._device(q)

@@ -361,10 +361,17 @@ def lora_kv_plan(plan: KVPlan, pages: KVPages, kv_len, new_len, req_slot=None, s
                                   _ptr(req_slot), plan.ref)
 
 
+def _paged(cache):
+    """The library reads a descriptor by its address, so another cache's must not get there."""
+    if not isinstance(cache, PagedKV):
+        raise ValueError(f"cache must be a PagedKV (got {type(cache).__name__})")
+
+
 def lora_rope_append(q_out, q, k, v, cache: PagedKV, slots, rope: Rope | None = None, positions=None, stream=None):
     """Rotate q into q_out and k into the cache at `slots`, and append v.  positions int32
     [axes, n_rows] (1-D for one axis); rope None appends without rotation.  q and q_out may
     both be None (k and v only); q_out may be q."""
+    _paged(cache)
     rope = _NoRope if rope is None else rope
     if _fast:
         dev = _device(slots)
@@ -412,6 +419,7 @@ def lora_paged_attention(out, q, cache: PagedKV, block_table, kv_len, work, req=
     """Attention of one query token per row: q and out [n_rows, heads * head_dim], block_table
     int32 [n_req, max_blocks], kv_len int32 [n_rows], req int32 [n_rows] or None (row i reads
     table row i), lse fp32 [n_rows, heads] or None, work from attention_workspace."""
+    _paged(cache)
     scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
     if _fast:
         dev = _device(q)

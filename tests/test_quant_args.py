@@ -300,3 +300,21 @@ def test_reference_on_worked_blocks():
     assert big[0, 0] == 49152.0
     code = QR.pack(*[t for t in QR.quantise(torch.arange(32, dtype=torch.float64)[None], 4, F16)], 4)
     assert code.shape == (1, 16)
+
+
+def test_a_cache_of_the_other_kind_is_refused():
+    """Their descriptors differ: one must not be read as the other, by the compiled calls either."""
+    quant = Q.QuantKV.zeros(4, 8, 2, 64, F16, 4, device="cpu")
+    paged = S.PagedKV(*(torch.zeros(4, 8, 2, 64, dtype=F16) for _ in range(2)))
+    x, slots, n = torch.zeros(3, 128, dtype=F16), torch.zeros(3, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
+    work = torch.zeros(64, dtype=torch.int32)
+    for cache in (paged, None):
+        for call in (lambda: Q.lora_quant_append(x.clone(), x, x, x, cache, slots), lambda: Q.lora_quant_read(x, None, cache, slots),
+                     lambda: Q.lora_quant_attention(x.clone(), x, cache, n, slots, work)):
+            with pytest.raises(ValueError, match="must be a QuantKV"):
+                call()
+    for cache in (quant, None):
+        for call in (lambda: S.lora_rope_append(x.clone(), x, x, x, cache, slots),
+                     lambda: S.lora_paged_attention(x.clone(), x, cache, n, slots, work)):
+            with pytest.raises(ValueError, match="must be a PagedKV"):
+                call()
