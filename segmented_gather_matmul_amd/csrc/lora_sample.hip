@@ -11,6 +11,7 @@ namespace {
 constexpr int kSampleThreads = 1024;
 constexpr int kWaves = kSampleThreads / 64;
 constexpr int kBins = 2 * kSampleThreads;  // of a histogram: two a thread
+constexpr int kAhead = 4;                  // segments of 512 logits that a wavefront asks for at a time
 constexpr int kUnitBits = 40;              // the largest weight is 2^kUnitBits
 
 // ------------------------------------------------------------------------ logits
@@ -400,10 +401,23 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     };
 
     float best = -INFINITY;  // this thread's largest
-    stream([&](int32_t s, Chunk<T> &c) __attribute__((always_inline)) {
-        best = __builtin_fmaxf(best, c.largest());
-        if constexpr (KEPT) held[64 * s + lane] = c;
-    });
+    if constexpr (KEPT) {
+        // (a short row in one trip to memory: 0.3 us less than one segment ahead, which long ones are as fast with)
+        for (int32_t s0 = wave; s0 < row.segments; s0 += kAhead * kWaves) {
+            Chunk<T> c[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) c[j] = row.bits(64 * (s0 + j * kWaves) + lane);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int32_t s = s0 + j * kWaves;
+                c[j].clean();
+                best = __builtin_fmaxf(best, c[j].largest());
+                if (s < row.segments) held[64 * s + lane] = c[j];
+            }
+        }
+    } else {
+        stream([&](int32_t, Chunk<T> &c) __attribute__((always_inline)) { best = __builtin_fmaxf(best, c.largest()); });
+    }
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
     const float wave_top = wave_max(best);
     if (by_k && top_k <= kListTopK && temperature > 0.f) {
