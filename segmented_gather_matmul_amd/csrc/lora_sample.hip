@@ -337,8 +337,8 @@ struct Shared {
 //
 // Bound by arithmetic where every logit's weight is needed (no filter, top-p): some 30 instructions a logit, most
 // of them in 64 bits, which run at the rate of 32-bit ones here.  A row is one CU's, so a call of few rows leaves the
-// others idle and lasts as long as its slowest row: one row of 32,000 with top-k and top-p (a list) 10.8 us, without a
-// filter 15, with a top-p that keeps too many for a list 34; 32 rows of both kinds 36.7; 251 rows of 128,257 121.9.
+// others idle and lasts as long as its slowest row: one row of 32,000 with top-k and top-p (a list) 10.5 us, without a
+// filter 15, with a top-p that keeps too many for a list 33; 32 rows of all kinds 36.6; 251 rows of 128,257 121.5.
 // Masses in whole numbers cost 64-bit atomics in LDS and buy draws that are the same every time and exact sums.
 template <typename T, bool KEPT>
 __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample_args a)
