@@ -204,14 +204,16 @@ __device__ inline double fma_c(double a, double b, double c)
     return r;
 }
 
-// floor(2^40 2^y) for y <= 0, to 2^-37 of it before the floor, as a whole number in 64-bit floating point: y = k + f with
-// |f| <= 1/2, 2^f = e^(f ln 2) by nine terms of its series (the tenth is below 2^-37), 2^k by the exponent.  2^0 is exact.
+// floor(2^40 2^y) for y <= 0, to 2^-40 of it before the floor, as a whole number in 64-bit floating point: y = k + f with
+// |f| <= 1/2, 2^f = e^(f ln 2) by nine terms of its series, 2^k by the exponent.  2^0 is exact.  The tenth term (2^-36.6 of
+// 2^f at f = -1/2) lies on the eighth: f^10 is within 2^-14 of 15/64 f^8, so it costs nothing, and 2^-40.5 of 2^f is left.
+// Two y that lie closer than that on both sides of some k + 1/2 may get weights one apart in the wrong order.
 __device__ inline double weight_of(double y)
 {
     constexpr double kRound = 6755399441055744.0 + kUnitBits;  // 1.5 2^52: a sum's low bits are a whole number, the nearest to y + 40
     constexpr double l = 0.693147180559945309417;
     constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6, c7 = c6 * l / 7,
-                     c8 = c7 * l / 8, c9 = c8 * l / 9;
+                     c8_of_series = c7 * l / 8, c9 = c8_of_series * l / 9, c8 = c8_of_series + c9 * l / 10 * (15.0 / 64);
     y = __builtin_fmax(y, -64.0);
     const double big = y + kRound, f = y - (big - kRound);
     double s = fma_c(f, c9, c8);

@@ -1,4 +1,5 @@
 """GPU: sampling (lora_sample.h) against its definition, at the sizes, settings and values where it can go wrong."""
+import decimal
 import math
 import random
 
@@ -292,3 +293,36 @@ def test_captured_and_replayed_with_other_logits_and_settings():
         got = token.tolist()
         c.run().check("eager")
         assert got == c.token[:n].tolist() and lp.tolist() == c.logprob[:n].tolist()
+
+
+# (logit, temperature, u): with the largest logit 0 behind it, floor(u M) lies below the logit's weight by so little that
+# one smaller by 2^-36.62 of itself (nine terms of the series) gives the other token, and by so much that none right to
+# 2^-37 does.
+NEAR_A_BORDER = [("-0x1.f8939cp-3", "0x1.6cp-1", "0x1.a8291cp-2"), ("-0x1.c0d9a8p-3", "0x1.44p-1", "0x1.a836c6p-2"),
+                 ("-0x1.94834cp-3", "0x1.24p-1", "0x1.a83720p-2"), ("-0x1.6aef60p-2", "0x1.06p+0", "0x1.a8383cp-2"),
+                 ("-0x1.811fd2p-2", "0x1.16p+0", "0x1.a836cap-2"), ("-0x1.9d14bcp-2", "0x1.2ap+0", "0x1.a82974p-2"),
+                 ("-0x1.ad7650p-2", "0x1.36p+0", "0x1.a8366ep-2"), ("-0x1.df4ceep-2", "0x1.5ap+0", "0x1.a83806p-2"),
+                 ("-0x1.e4b824p-2", "0x1.5ep+0", "0x1.a83d94p-2"), ("-0x1.110d7ap-1", "0x1.8ap+0", "0x1.a82b6cp-2"),
+                 ("-0x1.50a33ep-1", "0x1.e6p+0", "0x1.a836c6p-2"), ("-0x1.b7361ep-1", "0x1.3dp+1", "0x1.a833d6p-2")]
+
+
+@pytest.mark.parametrize("V,k,p", [(2, 0, 1.0), (3, 2, 1.0), (700, 0, 0.99999994), (900, 200, 1.0), (40000, 0, 1.0), (40000, 40, 1.0)])
+def test_weights_are_right_to_their_bound_where_the_series_ends(V, k, p):
+    """Half way between two powers of 2, where the exponential's series is furthest off."""
+    say(f"case sample-weight V={V} k={k} p={p}")
+    with decimal.localcontext() as ctx:
+        ctx.prec = 50
+        dec, unit = decimal.Decimal, decimal.Decimal(2) ** 40
+        l, t, u = ([float.fromhex(c[i]) for c in NEAR_A_BORDER] for i in range(3))
+        for a, b, c in zip(l, t, u):
+            assert [float(torch.tensor(x, dtype=torch.float32)) for x in (a, b, c)] == [a, b, c]
+            w = (dec(a) / dec(b)).exp() * unit
+            least, most = int(w * (1 - dec(2) ** -37)), int(w * (1 + dec(2) ** -37))
+            assert all(int(dec(c) * (unit + m)) < m for m in range(least, most + 1))
+            low = int(w * (1 - dec("9.44e-12")))
+            assert int(dec(c) * (unit + low)) >= low
+    x = torch.full((len(l), V), -math.inf)
+    x[:, 0], x[:, 1] = torch.tensor(l), 0.0
+    d = Draw(x, t=t, k=k, p=p, u=u).run()
+    torch.cuda.synchronize()
+    assert d.token[:len(l)].tolist() == [0] * len(l)
