@@ -1,6 +1,7 @@
 // HIP kernels (gfx950 / CDNA4) and launchers of sampling (lora_sample.h).
 #include "lora_sample.h"
 
+#include <cstddef>
 #include <type_traits>
 
 #include "step_device.hpp"
@@ -306,7 +307,7 @@ constexpr int kList = 256;                // candidates on a list
 constexpr int kListTopK = 128;            // top-k of this many or fewer looks for one
 constexpr size_t kSampleLds = 120 << 10;  // for a row's logits, of a workgroup's 160 KB
 
-struct Shared {
+struct alignas(16) Shared {
     uint64_t mass[kBins];
     uint32_t count[kBins];
     Pair wave_sums[kWaves];
@@ -484,6 +485,7 @@ __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample
     auto bin_of = [&](float v) { return (int32_t)__builtin_fminf((top - v) * per, (float)(kBins - 1)); };
 
     auto clear = [&]() {
+        static_assert(alignof(Shared) % alignof(uint4) == 0 && offsetof(Shared, mass) % alignof(uint4) == 0, "16-byte stores");
         __syncthreads();
         *reinterpret_cast<uint4 *>(&sh.mass[2 * tid]) = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint2 *>(&sh.count[2 * tid]) = make_uint2(0, 0);
