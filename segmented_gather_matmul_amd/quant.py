@@ -33,7 +33,7 @@ class CQuantCache(ctypes.Structure):
 
 def _cells(t, what, shape):
     """t: uint8 [num_pages, page_size, kv_heads, cell], unit stride along a cell, entries apart; the bytes from
-    its first entry to its last, and those of one page."""
+    its first entry to its last."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
         raise ValueError(f"{what} must have dtype uint8 (got {getattr(t, 'dtype', type(t).__name__)})")
     if t.layout is not torch.strided or t.is_nested:
@@ -42,30 +42,48 @@ def _cells(t, what, shape):
         raise ValueError(f"{what} is {tuple(t.shape)}, must be {shape}")
     if t.stride(3) != 1 and shape[3] > 1:
         raise ValueError(f"{what} needs unit stride along a cell (stride {t.stride(3)})")
-    reach = page = shape[3]
+    reach = shape[3]
     for s, n in sorted((s, n) for n, s in zip(shape[:3], t.stride()[:3]) if n > 1):
         if s < reach:
             raise ValueError(f"{what} has overlapping entries (shape {shape}, strides {t.stride()})")
         reach = s * (n - 1) + reach
-    page += sum((n - 1) * s for n, s in zip(shape[1:3], t.stride()[1:3]) if n > 1)
-    return reach, page
+    return reach
 
 
-def _apart(x, y, whole_x, whole_y, page_x, page_y):
-    """x and y (their bytes from first to last, and those of one page) share no entry: they lie apart, or each page
-    of the one between pages of the other."""
+def _apart(x, y, whole_x, whole_y):
+    """x and y (of that many bytes from first to last) share no entry: they lie apart, or were cut from records that
+    repeat along some dimension and all those outside it: pages with both, or tokens or heads with both."""
     off = y.data_ptr() - x.data_ptr()
-    if off >= whole_x or -off >= whole_y:
+    if off < 0:
+        x, y, whole_x, whole_y, off = y, x, whole_y, whole_x, -off
+    if off >= whole_x:
         return True
-    s = x.stride(0)
-    return x.shape[0] > 1 and y.stride(0) == s and page_x <= off % s <= s - page_y
+    dims = sorted(((s, t, n) for n, s, t in zip(x.shape[:3], x.stride(), y.stride()) if n > 1), reverse=True)
+    for i, (s, t, n) in enumerate(dims):
+        if s != t:
+            return False
+        # records of s bytes hold an entry of each, in the same place wherever one begins: at multiples of s, or where
+        # the outer dimensions keep them apart
+        in_x = x.shape[3] + sum((m - 1) * a for a, _, m in dims[i + 1:])
+        in_y = y.shape[3] + sum((m - 1) * b for _, b, m in dims[i + 1:])
+        at, reach, clear = off, s * n, True
+        if all(a % s == 0 for a, _, _ in dims[:i]):
+            at = off % s
+        else:
+            for a, _, m in reversed(dims[:i]):
+                clear = clear and a >= reach
+                reach = a * (m - 1) + reach
+        if clear and in_x <= at and at + in_y <= s:
+            return True
+    return False
 
 
 class QuantKV:
     """lora_quant_cache: k and v uint8 [num_pages, page_size, kv_heads, bytes of codes], k_exp and v_exp uint8
     [num_pages, page_size, kv_heads, blocks], of heads of head_dim columns whose values have dtype (f16 or bf16).
     bits (4 or 8) goes by the bytes of a cell.  Views of another memory order are fine (equal strides for k and v,
-    and for k_exp and v_exp); ``zeros`` has heads before tokens in memory, which the attention reads fastest."""
+    and for k_exp and v_exp), and views of one tensor, cut from pages, tokens or heads that hold several of the four;
+    ``zeros`` has heads before tokens in memory, which the attention reads fastest."""
 
     def __init__(self, k, v, k_exp, v_exp, head_dim, dtype):
         ty = S._TYPES.get(dtype)
@@ -97,7 +115,7 @@ class QuantKV:
                 raise ValueError(f"k is on {k.device}, {what} on {t.device}")
         for i in range(4):
             for j in range(i + 1, 4):
-                if not _apart(all_[i], all_[j], sizes[i][0], sizes[j][0], sizes[i][1], sizes[j][1]):
+                if not _apart(all_[i], all_[j], sizes[i], sizes[j]):
                     raise ValueError(f"{names[i]} and {names[j]} overlap")
         # a dimension of one entry may have any stride; give the library a valid one
         st = [s if n > 1 else shape[3] for n, s in zip(shape[:3], k.stride()[:3])]

@@ -614,3 +614,28 @@ def test_cells_beyond_32_bit_offsets():
     w = QR.attention(q.reshape(1, 1, D), kk, -kk, table.cpu(), [45], None, 1 / math.sqrt(D), 0, 1)[0]
     close(out.reshape(1, D), w[0], w[2], "out")
     close(lse[0], w[1], w[3], "lse")
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_cells_in_records_of_one_tensor(bits):
+    """Codes of k and v and their exponents side by side, token by token and head by head: the bits of a cache of
+    separate tensors."""
+    say(f"case quant-records bits={bits}")
+    pages, P, H, K, D, n = 9, 16, 8, 2, 64, 130
+    cb, eb = 8 * bits, 2
+    one = torch.zeros(pages, P, K, -(-2 * (cb + eb) // 16) * 16, dtype=torch.uint8, device="cuda")
+    rec = Q.QuantKV(one[..., :cb], one[..., cb:2 * cb], one[..., 2 * cb:2 * cb + eb], one[..., 2 * cb + eb:2 * (cb + eb)], D, F16)
+    g = torch.Generator(device="cuda").manual_seed(bits)
+    x = torch.randn(n, 2 * K * D, generator=g, device="cuda").to(F16)
+    q = torch.randn(1, H * D, generator=g, device="cuda").to(F16)
+    slots, table = torch.arange(n, dtype=torch.int32, device="cuda"), torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    got = []
+    for c in (rec, Q.QuantKV.zeros(pages, P, K, D, F16, bits)):
+        Q.lora_quant_append(None, None, x[:, :K * D], x[:, K * D:], c, slots, rope=S.Rope.base(D), positions=slots)
+        outs = [torch.zeros(n, K * D, dtype=F16, device="cuda") for _ in range(2)]
+        Q.lora_quant_read(*outs, c, slots)
+        out = torch.zeros_like(q)
+        Q.lora_quant_attention(out, q, c, table, ints([n]), Q.attention_workspace(1, H, c))
+        torch.cuda.synchronize()
+        got.append(bytes_of(c) + outs + [out])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and bool(got[0][-1].any())

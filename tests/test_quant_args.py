@@ -4,6 +4,7 @@ import ctypes
 import importlib
 import math
 import os
+import random
 import re
 import subprocess
 
@@ -318,3 +319,68 @@ def test_a_cache_of_the_other_kind_is_refused():
                      lambda: S.lora_paged_attention(x.clone(), x, cache, n, slots, work)):
             with pytest.raises(ValueError, match="must be a PagedKV"):
                 call()
+
+
+def _bytes_of(t):
+    """Every byte that a tensor holds, counted from its storage's first."""
+    at = torch.tensor(t.storage_offset())
+    for n, st in zip(t.shape, t.stride()):
+        at = at[..., None] + torch.arange(n) * st
+    return set(at.flatten().tolist())
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("cut", ["pages", "tokens", "heads", "cells", "padded", "behind"])
+def test_k_and_v_of_one_tensor(cut, bits):
+    """k and v (and their exponents) taken from one tensor along any dimension, as a 16-bit cache takes them, and all
+    four from records of every size of entry."""
+    P, T, K, D, cb, eb = 3, 4, 2, 64, 8 * bits, 2
+    z = lambda *s: torch.zeros(s, dtype=U8)
+    if cut in ("pages", "tokens", "heads"):
+        i = {"pages": 1, "tokens": 2, "heads": 3}[cut]
+        both = lambda n: z(*[(P, T, K)[j] for j in range(i)], 2, *[(P, T, K)[j] for j in range(i, 3)], n).unbind(i)
+        (k, v), (ke, ve) = both(cb), both(eb)
+    elif cut == "behind":       # v's pages lie behind k's of the page after
+        one = z(P + 1, T * K * 2 * (cb + eb))
+        at = lambda first, o, n: one[first:first + P, o * T * K:(o + n) * T * K].view(P, T, K, n)
+        k, v, ke, ve = at(0, 0, cb), at(1, cb, cb), at(0, 2 * cb, eb), at(1, 2 * cb + eb, eb)
+    else:                       # a token and head: codes of k and v, then exponents, in records of a multiple of 16 bytes
+        rec = -(-2 * (cb + eb) // 16) * 16
+        if cut == "cells":
+            one = z(P, T, K, rec)
+        else:                   # and pages that are no multiple of one
+            one = z(P, T * K * rec + 16)[:, :T * K * rec].view(P, T, K, rec)
+        k, v, ke, ve = one[..., :cb], one[..., cb:2 * cb], one[..., 2 * cb:2 * cb + eb], one[..., 2 * cb + eb:2 * (cb + eb)]
+    c = Q.QuantKV(k, v, ke, ve, D, F16)
+    assert c.bits == bits and (c.k.shape, c.k_exp.shape) == ((P, T, K, cb), (P, T, K, eb))
+
+
+def test_layouts_are_refused_where_entries_meet():
+    """Random layouts inside one buffer: none is taken in which two of the four share a byte."""
+    g = random.Random(0)
+    D, cb, eb, taken, met = 32, 16, 1, 0, 0
+    buf = torch.zeros(1 << 14, dtype=U8)
+    for _ in range(4000):
+        shape = [g.choice([1, 2, 3]) for _ in range(3)]
+
+        def strides(cell):
+            st, reach = [0, 0, 0], cell
+            for i in g.sample(range(3), 3):
+                st[i] = -(-reach // 16) * 16 * g.choice([1, 1, 2, 3]) if cell == cb else reach * g.choice([1, 1, 3]) + g.choice([0, 0, 5])
+                reach = st[i] * (shape[i] - 1) + reach
+            return st
+
+        kst = strides(cb)
+        est = kst if g.random() < 0.5 else strides(eb)
+        step = g.choice([1, 16, 16, 32])
+        t = [buf.as_strided((*shape, n), (*st, 1), step * g.randrange(0, 40))
+             for i, (n, st) in enumerate(((cb, kst), (cb, kst), (eb, est), (eb, est)))]
+        apart = sum(len(_bytes_of(x)) for x in t) == len(set().union(*map(_bytes_of, t)))
+        try:
+            Q.QuantKV(*t, D, F16)
+            assert apart, (shape, kst, est, [x.storage_offset() for x in t])
+            taken += 1
+        except ValueError as e:
+            assert "overlap" in str(e)
+            met += not apart
+    assert taken > 200 and met > 200
