@@ -5,7 +5,8 @@
  * take; a layer uses either cache.
  *
  * The conventions of lora_step.h hold (pointers to codes and to 16-bit data are 16-byte
- * aligned; exponents are bytes of any alignment).
+ * aligned; exponents are bytes of any alignment).  lora_quant_append and lora_quant_read take
+ * any number of rows below 2^24 - 128, and may refuse more.
  *
  * The format.  The head_dim columns of one token and head are cut into blocks of 32 (the
  * last one padded with zeros).  A block is 32 codes and one exponent byte e; code c stands for
@@ -17,7 +18,10 @@
  *                          4 bits             8 bits
  *     LORA_TYPE_F16     e - 127 in -23..13      -15..7
  *     LORA_TYPE_BF16            -125..125      -117..119
- * so every value of a cell is a value of the 16-bit type exactly: reading rounds nothing.
+ * so every value of a cell that was appended is a value of the 16-bit type exactly: reading
+ * rounds nothing.  Where something else has written a cell, its exponent may be any byte (e = 0 is
+ * the power 2^-127): a value that the type does not hold is rounded to it wherever the cell is
+ * read, to nearest, ties to even, as far as to 0 and to infinity.
  *
  * Quantising a block: e - 127 is the smallest power with max|x| < 7 * 2^(e-127) (4 bits; no
  * element is then off by more than 2^(e-127), half of the largest step), or with max|x| <
@@ -88,9 +92,11 @@ int lora_quant_read(void *stream, int32_t n_rows, void *k_out, int64_t ldko, voi
 
 /*
  * lora_paged_attention over a quantised cache: the same arguments, rows, masks and results
- * with k_t and v_t the values of the cells.  The products are those of the exact values;
- * softmax weights multiply v as two 16-bit parts, as there (fp16: a weight below 2^-38 of the row's
- * largest counts as 0).  A visible NaN makes its row's head NaN.
+ * with k_t and v_t the values of the cells, as lora_quant_read gives them.  The products are those of
+ * the exact values; softmax weights multiply v as two 16-bit parts, as there (fp16: a weight below
+ * 2^-38 of the row's largest counts as 0).  A visible NaN makes its row's head NaN, and a
+ * visible infinity (appended cells hold none) may.  n_rows times the tiles of the longest row, here 64
+ * tokens each and eight more a row, stays 2048 below 2^31, or the call is refused.
  *   work   device memory of at least lora_quant_attention_bytes(...) bytes, 256-byte aligned,
  *          all zero before its first use; every call leaves its counters zero again.  Calls
  *          ordered on one stream (graph replays included) may share it, with

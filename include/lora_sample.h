@@ -6,7 +6,8 @@
  * The conventions of lora_step.h hold: asynchronous on `stream`, no allocation, no
  * synchronisation, arguments checked on the host, device-resident settings read without a host
  * check (a row whose settings lie outside their range, or which names no row of the logits, is
- * a no-op: its outputs stay as they were), and calls may be captured and replayed.
+ * a no-op: its outputs stay as they were), and calls may be captured and replayed.  More than
+ * 2^22 - 1 rows are refused.
  */
 #ifndef LORA_SAMPLE_H
 #define LORA_SAMPLE_H

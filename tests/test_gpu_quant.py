@@ -218,6 +218,56 @@ def test_read_gives_every_code_at_every_exponent(K, D, P, layout, bits, dt):
     assert torch.equal(only.view(torch.int16), ko.contiguous().view(torch.int16))
 
 
+def every_code_at_every_exponent(dt, bits, least=0, most=255):
+    """256 tokens: block b of token t has exponent byte t (kept to least..most); with 8 bits a token's first 256 columns
+    have all codes, with 4 bits the 16 of them over and over."""
+    D, P = 256, 16
+    c = Q.QuantKV.zeros(16, P, 1, D, dt, bits)
+    codes = torch.arange(256) if bits == 8 else (torch.arange(128) * 2 % 16) | ((torch.arange(128) * 2 + 1) % 16) << 4
+    exps = torch.arange(256).clamp(least, most).to(torch.uint8).view(16, P, 1, 1).cuda()
+    for code, exp in ((c.k, c.k_exp), (c.v, c.v_exp)):
+        code.copy_(codes.to(torch.uint8).cuda().expand_as(code))
+        exp.copy_(exps.expand_as(exp))
+    return c
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+def test_read_rounds_what_the_type_does_not_hold(dt, bits):
+    """Every exponent byte, 0 and those that an append never writes too: to nearest even, down to 0, up to infinity.  (The
+    values have four significant bits, so one rounding to 32 bits on the way to dt changes none.)"""
+    say(f"case quant-read-foreign bits={bits} {dt}")
+    c = every_code_at_every_exponent(dt, bits)
+    outs = [torch.empty(256, 256, dtype=dt, device="cuda") for _ in range(2)]
+    Q.lora_quant_read(*outs, c, torch.arange(256, dtype=torch.int32, device="cuda"))
+    for o, what in zip(outs, "kv"):
+        want, got = cells(c, what).reshape(256, 256).to(dt), o.cpu()
+        assert bool(((got == want) | (got.isnan() & want.isnan())).all())
+        assert torch.equal(torch.signbit(got)[~want.isnan()], torch.signbit(want)[~want.isnan()])
+        assert bool(want.isinf().any()) and bool((want[1:128] == 0).any()) and bool(got[255].isnan().all())
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+def test_attention_over_cells_that_the_type_does_not_hold(dt, bits):
+    """Exponents below those that an append writes: the products are those of the values as they are read back."""
+    say(f"case quant-attention-foreign bits={bits} {dt}")
+    c = every_code_at_every_exponent(dt, bits, most=127)
+    if bits == 8:       # no NaN codes
+        for code in (c.k, c.v):
+            code[code % 128 == 127] = 0
+    H, n = 3, 256
+    val = [cells(c, what).to(dt) for what in "kv"]
+    g = torch.Generator().manual_seed(bits)
+    q = torch.randn(1, H * 256, generator=g).to(dt)
+    out, lse = torch.empty(1, H * 256, dtype=dt, device="cuda"), torch.empty(1, H, device="cuda")
+    table = torch.arange(16, dtype=torch.int32)[None]
+    Q.lora_quant_attention(out, q.cuda(), c, table.cuda(), ints([n]), Q.attention_workspace(1, H, c), scale=0.01, lse=lse)
+    w = QR.attention(q.reshape(1, H, 256), *val, table, [n], None, 0.01, 0, H)[0]
+    close(out.reshape(H, 256), w[0], w[2], "out")
+    close(lse[0], w[1], w[3], "lse")
+
+
 @pytest.mark.parametrize("what", ["k", "v", "kv"])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("K,D,n", [(1, 8, 1100000), (1, 16, 600001), (3, 40, 140003), (2, 256, 17001), (70, 128, 1021)])
