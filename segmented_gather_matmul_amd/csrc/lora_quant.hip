@@ -343,6 +343,8 @@ constexpr int kQWaves = 4, kQTile = 64;
 // The two ways to split the rows' tiles (quant_solo): a workgroup's wavefronts take those of a part in turn and join
 // at its end, or each wavefront has parts of its own and waits for no other.  A tile of 64 tokens is what the registers
 // hold of K and V in flight while the one before is worked on; two workgroups fit a CU up to 128 columns, one beyond.
+// (Of 8-bit cells in pages below 16 tokens, whose cells every lane finds for itself, not quite: the 128-column instances
+// keep 9 to 14 registers a lane in scratch.  32 rows of 64 to 4096 tokens of 32 heads: 59 us in pages of 16, 65 of 8.)
 typedef AttnLine<kQWaves, kQTile, 8, 8, 16, false, 8, 32> GangLine;
 typedef AttnLine<kQWaves, kQTile, 4, 2, 16, true, 8, 32> SoloLine;
 constexpr int kQSub = kQTile / 16;  // 16-token subtiles of a tile
@@ -401,9 +403,11 @@ __device__ inline float column_max(float x)
 //
 // Long rows are bound by the cells' bytes: 32 rows of 8192 tokens, 32/32 heads of 128, in 200 us with 4 bits (5.7 TB/s),
 // 8 bits at 5.3 TB/s.  32 rows of 64 to 4096 tokens (135 MB) take 34.7 us, of which the read is 22.4 and the rest
-// starting, the rows' ends and joins; one row of 131,071 tokens of 1 head 18.4 (a read of 3); one of 17 tokens 7.6, loads
+// starting, the rows' ends and joins (8 bits: 262 MB, 59 us, the read 43); one row of 131,071 tokens of 1 head 18.4 (a
+// read of 3), 256 parts of 8 tiles on half of the places that the CUs have; one of 17 tokens 7.6, loads
 // one after another.  All of V converted at the top of a round, in twice the LDS, was slower; joins that load 16 parts
-// at a time, and not 8, cost every call registers.
+// at a time, and not 8, cost every call registers.  Rows know nothing of each other: a prompt's tokens as rows read the
+// cells before them once each (12,907 rows of 16 prompts, 32 heads: 5.0 ms with 4 bits, 8.3 with 8).
 template <typename T, int BITS, int DP, int R, typename LINE, bool PAGES>
 __global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(quant_occupancy(DP)))) void
 lora_quant_attention_kernel(QuantArgs a)
@@ -782,7 +786,9 @@ int32_t quant_shares(int32_t tiles, int32_t head_dim, bool solo)
 
 // Whether wavefronts take parts of their own: where each has half a row and key/value head or more, so that few rows are
 // split.  Measured (4 bits, 128 columns, gang / solo): 32 rows of 64-4096 tokens, 32/32 heads 44.8 / 37.0 us, 256 rows of
-// 100-900 144 / 107; 61 rows of 1-16,381 tokens, 64/8 heads 41 / 49, one row of 131,071, 8/1 heads 24 / 43.
+// 100-900 144 / 107; 61 rows of 1-16,381 tokens, 64/8 heads 41 / 49, one row of 131,071, 8/1 heads 24 / 43.  That is at
+// 1024 and 8192 rows x tiles for it and at 512 and 1 against it; between 512 and 1024 both sides have not been measured, and
+// the border lies at the upper end (31 rows of 32 heads, a gang's: 37.8 us, 32 of them: 32).  Rows that are not active count.
 bool quant_solo(int32_t n_rows, int32_t tiles, int32_t head_dim)
 {
     return 2 * (int64_t)n_rows * tiles >= kAttnCUs * kQWaves * quant_occupancy(head_dim);

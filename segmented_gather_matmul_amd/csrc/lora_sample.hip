@@ -328,7 +328,9 @@ struct alignas(16) Shared {
 // One workgroup per row.  Its logits are kept in LDS (KEPT), or the row is read again in every pass.
 //   - The largest.
 //   - For top-k of few, a bound that at least k logits reach: every wavefront gives the value that k / 16 of its lanes' largest
-//     reach, and the lowest of these is taken.  What reaches it (mostly little more than k) is put on a list.
+//     reach, and the lowest of these is taken.  What reaches it (for k = 50 of normal logits some 135) is put on a
+//     list.  (A row of fewer than 16 segments leaves wavefronts without logits, and a bound that all reach: beyond kList
+//     logits such a row takes a histogram.  32 rows of 4,000 with top-k 50 and top-p 19 us, of 9,000 11.5.)
 //   - Otherwise, for top-k and top-p, a histogram of how many and what mass lie how far below the largest, and the
 //     bin in which the border lies.  If few lie above it, they are put on the list.
 //   - On a list of at most 256, a candidate's place in order and by index is the number of those before it, counted by
@@ -338,10 +340,12 @@ struct alignas(16) Shared {
 //     mass that stays of each segment of 512 logits, the segment that the draw falls into, and the token in it.
 // Counts and masses are whole numbers, so the order of their atomics does not matter.
 //
-// Bound by arithmetic where every logit's weight is needed (no filter, top-p): some 30 instructions a logit, most
-// of them in 64 bits, which run at the rate of 32-bit ones here.  A row is one CU's, so a call of few rows leaves the
-// others idle and lasts as long as its slowest row: one row of 32,000 with top-k and top-p (a list) 10.5 us, without a
-// filter 15, with a top-p that keeps too many for a list 33; 32 rows of all kinds 36.6; 251 rows of 128,257 121.5.
+// Where every logit's weight is needed (no filter, top-p), a pass that weighs is some 30 instructions a logit, most of them
+// in 64 bits, which run at the rate of 32-bit ones here: 251 rows of 128,257 without a filter take 53 us with the vector
+// units busy 68% of it.  A row is one CU's, so a call of few rows leaves the others idle and lasts as long as its slowest
+// row: one row of 32,000 with top-k and top-p (a list) 10.5 us, without a filter 15, with a top-p that keeps too many for a
+// list 33; 32 rows of all kinds 36.6; 251 rows of 128,257 of all kinds 121.5, where a row is at work for 46 on average and
+// the vector units are busy 27%.
 // Masses in whole numbers cost 64-bit atomics in LDS and buy draws that are the same every time and exact sums.
 template <typename T, bool KEPT>
 __global__ __launch_bounds__(kSampleThreads) void lora_sample_kernel(lora_sample_args a)

@@ -163,7 +163,8 @@ class PagedStep:
         """Draw the next token of every request that had tokens in the step planned last, from the logits of its last
         row: token int32 [n_req] (entries of other requests stay as they were), logits [max_tokens, vocab] of
         the step's token rows; u and the settings are per request, work from sample.sample_workspace(n_req, vocab)
-        (sample.lora_sample)."""
+        (sample.lora_sample).  Logits of the requests' last rows alone, plan.q_ptr[1:] - 1, go to sample.lora_sample
+        by themselves, with rows -1 for the requests without tokens."""
         import torch
         from . import sample as SA
         if logits.shape[0] != self.max_tokens or token.numel() != self.n_req:
